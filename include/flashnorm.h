@@ -372,6 +372,63 @@ fn_status fn_dequant_fp8(const void* q, const float* scales, int64_t d, int64_t 
 fn_status fn_dequant_mxfp8(const void* q, const void* scales, int64_t d, int64_t ncols, void* W,
                            fn_stream_t stream);
 
+typedef enum {
+  FN_T_BF16 = 0,
+  FN_T_FP16 = 1,
+  FN_T_FP32 = 2
+} fn_dtype;
+
+/*
+ * fn_token_logprobs — log probabilities of given tokens, entropies and the
+ * top alternatives, from the logits of a head projection (fn_norm_proj with
+ * N = vocabulary size), in one pass over the logits.  Per row m, with
+ * z = scale * logits[m, :]:
+ *   lse      = log sum_v e^{z_v}
+ *   logprob  = z_{targets[m]} - lse
+ *   entropy  = lse - sum_v p_v z_v,   p_v = e^{z_v - lse}
+ *   top_ids, top_logprobs: the top_k largest logits, largest first, ties to
+ *     the lower index, with z - lse; NaN ranks above every number
+ * Sums are fp32; a masked logit (-inf) adds nothing.  A row whose mask leaves
+ * nothing (its largest z is -inf) has lse = -inf, log probabilities -inf and
+ * entropy 0.  A row that holds NaN or +inf has NaN results (top_ids as above).
+ *   logits   [M, V] of `type` (bf16, fp16 or fp32), rows ld >= V elements
+ *            apart; only element alignment is needed (rows at odd addresses
+ *            run at the same speed)
+ *   targets  int32 [M]: the token of each row; negative: no token, logprob 0;
+ *            >= V: logprob NaN (nothing is read out of range).  May be NULL
+ *            when logprob is.
+ *   scale    > 0 and finite: the inverse temperature
+ *   top_k    0 .. 32 and at most V; above 32 FN_ERR_UNSUPPORTED_SHAPE
+ *   logprob, entropy, lse   fp32 [M], each may be NULL (not computed)
+ *   top_ids int32 [M, top_k], top_logprobs fp32 [M, top_k]: NULL iff top_k is 0
+ * No output may overlap an input or another output (FN_ERR_ALIAS); at least
+ * one is given.  M == 0 is a no-op; M < 2^28.  No workspace; deterministic.
+ */
+fn_status fn_token_logprobs(const void* logits, fn_dtype type, int64_t M, int64_t V, int64_t ld, const int32_t* targets,
+                            float scale, int top_k, float* logprob, float* entropy, float* lse, int32_t* top_ids,
+                            float* top_logprobs, fn_stream_t stream);
+
+/*
+ * fn_token_logprobs_backward — the gradient of fn_token_logprobs' logprob and
+ * entropy with respect to the logits:
+ *   dlogits_v = scale * (gl (1[v = target] - p_v) - gh p_v (log p_v + entropy))
+ * with gl = grad_logprob[m] (0 where targets[m] < 0), gh = grad_entropy[m],
+ * p_v = e^{z_v - lse[m]}.  Masked logits (p_v = 0) and every logit of a row
+ * with lse = -inf get 0, except that a masked target gets its scale * gl.
+ *   lse, entropy   fp32 [M] from the forward call on the same logits, targets
+ *                  and scale (entropy may be NULL when grad_entropy is)
+ *   grad_logprob, grad_entropy   fp32 [M]; either may be NULL (zero), not both;
+ *                  targets may be NULL when grad_logprob is
+ *   dlogits        [M, V] of `type`, rows ldd >= V elements apart, one round at
+ *                  the store; may be the logits themselves (same address and
+ *                  row stride), may not overlap any input otherwise
+ * The top alternatives carry no gradient.  M == 0 is a no-op.
+ */
+fn_status fn_token_logprobs_backward(const void* logits, fn_dtype type, int64_t M, int64_t V, int64_t ld,
+                                     const int32_t* targets, const float* lse, const float* entropy,
+                                     const float* grad_logprob, const float* grad_entropy, float scale, void* dlogits,
+                                     int64_t ldd, fn_stream_t stream);
+
 /* Human-readable name of a status code (static string). */
 const char* fn_status_string(fn_status s);
 

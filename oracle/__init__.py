@@ -12,3 +12,4 @@ itself (closed forms, invariants, brute force, torch's own casts); see
 ``tests/test_oracle.py``.
 """
 from .flashnorm_oracle import *  # noqa: F401,F403
+from .operators_oracle import *  # noqa: F401,F403

@@ -30,6 +30,10 @@ FN_W_BF16 = 0
 FN_W_FP8_E4M3_B128 = 1
 FN_W_MXFP8_E4M3 = 2
 
+FN_T_BF16 = 0
+FN_T_FP16 = 1
+FN_T_FP32 = 2
+
 FN_DEBUG_WAIT_BUDGET_NS = 1
 FN_DEBUG_WITHHOLD_ARRIVE = 2
 FN_DEBUG_FORCE_PATH = 3
@@ -61,6 +65,9 @@ _SIGNATURES = {
     "fn_rmsnorm": (_int, [_vp, _i64, _i64, _vp, _f32, _vp, _vp]),
     "fn_dequant_fp8": (_int, [_vp, _vp, _i64, _i64, _vp, _vp]),
     "fn_dequant_mxfp8": (_int, [_vp, _vp, _i64, _i64, _vp, _vp]),
+    "fn_token_logprobs": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _f32, _int, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "fn_token_logprobs_backward": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _f32, _vp, _i64,
+                                          _vp]),
     "fn_status_string": (ctypes.c_char_p, [_int]),
     "fn_version": (_int, []),
     "fn_kernel_launches": (ctypes.c_uint64, []),
@@ -221,3 +228,16 @@ def fn_norm_proj_swiglu_nvfp4_swizzled(x, M: int, d: int, Wp, scales, wt: int, N
     return lib().fn_norm_proj_swiglu_nvfp4_swizzled(_ptr(x), M, d, _ptr(Wp), _ptr(scales), wt, N, eps,
                                                     _ptr(global_scale), _ptr(out_q), _ptr(out_sf), _ptr(workspace),
                                                     ws_bytes, _stream(stream))
+
+
+def fn_token_logprobs(logits, type: int, M: int, V: int, ld: int, targets, scale: float, top_k: int, logprob, entropy,
+                      lse, top_ids, top_logprobs, stream=None) -> int:
+    return lib().fn_token_logprobs(_ptr(logits), type, M, V, ld, _ptr(targets), scale, top_k, _ptr(logprob),
+                                   _ptr(entropy), _ptr(lse), _ptr(top_ids), _ptr(top_logprobs), _stream(stream))
+
+
+def fn_token_logprobs_backward(logits, type: int, M: int, V: int, ld: int, targets, lse, entropy, grad_logprob,
+                               grad_entropy, scale: float, dlogits, ldd: int, stream=None) -> int:
+    return lib().fn_token_logprobs_backward(_ptr(logits), type, M, V, ld, _ptr(targets), _ptr(lse), _ptr(entropy),
+                                            _ptr(grad_logprob), _ptr(grad_entropy), scale, _ptr(dlogits), ldd,
+                                            _stream(stream))

@@ -501,6 +501,105 @@ fn_status fn_dequant_mxfp8(const void* q, const void* scales, int64_t d, int64_t
              : FN_ERR_CUDA;
 }
 
+namespace {
+// Rows of a strided matrix: [rows, cols] elements of `size` bytes, ld apart.
+size_t span_bytes(int64_t rows, int64_t cols, int64_t ld, int size) {
+  return rows <= 0 ? 0 : (static_cast<size_t>(rows - 1) * ld + cols) * size;
+}
+int type_bytes(fn_dtype t) { return t == FN_T_FP32 ? 4 : 2; }
+bool misaligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
+}  // namespace
+
+fn_status fn_token_logprobs(const void* logits, fn_dtype type, int64_t M, int64_t V, int64_t ld, const int32_t* targets,
+                            float scale, int top_k, float* logprob, float* entropy, float* lse, int32_t* top_ids,
+                            float* top_logprobs, fn_stream_t stream) {
+  if (M < 0 || V <= 0 || ld < V || top_k < 0 || top_k > V) return FN_ERR_INVALID_ARG;
+  if (type != FN_T_BF16 && type != FN_T_FP16 && type != FN_T_FP32) return FN_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || scale <= 0.0f) return FN_ERR_INVALID_ARG;
+  if (top_k > kMaxTopAlternatives || V > kMaxDim || M > kMaxDim / 8) return FN_ERR_UNSUPPORTED_SHAPE;
+  if (M == 0) return FN_OK;
+  if (!logits || (logprob && !targets)) return FN_ERR_INVALID_ARG;
+  if (top_k > 0 ? (!top_ids || !top_logprobs) : (top_ids || top_logprobs)) return FN_ERR_INVALID_ARG;
+  if (!logprob && !entropy && !lse && top_k == 0) return FN_ERR_INVALID_ARG;
+  if (misaligned(logits, type_bytes(type)) || misaligned(targets, 4) || misaligned(logprob, 4) ||
+      misaligned(entropy, 4) || misaligned(lse, 4) || misaligned(top_ids, 4) || misaligned(top_logprobs, 4))
+    return FN_ERR_ALIGNMENT;
+  const size_t rows = static_cast<size_t>(M) * 4, tops = rows * top_k;
+  const struct { const void* p; size_t n; } outs[5] = {
+      {logprob, rows}, {entropy, rows}, {lse, rows}, {top_ids, tops}, {top_logprobs, tops}};
+  const size_t in = span_bytes(M, V, ld, type_bytes(type));
+  for (int i = 0; i < 5; ++i) {
+    if (overlaps(outs[i].p, outs[i].n, logits, in) || overlaps(outs[i].p, outs[i].n, targets, rows))
+      return FN_ERR_ALIAS;
+    for (int j = i + 1; j < 5; ++j)
+      if (overlaps(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return FN_ERR_ALIAS;
+  }
+  int sms = 0;
+  const fn_status st = check_device(sms);
+  if (st != FN_OK) return st;
+  LogprobArgs a;
+  a.logits = logits;
+  a.type = static_cast<int>(type);
+  a.M = M;
+  a.V = V;
+  a.ld = ld;
+  a.targets = targets;
+  a.scale = scale;
+  a.top_k = top_k;
+  a.logprob = logprob;
+  a.entropy = entropy;
+  a.lse = lse;
+  a.top_ids = top_ids;
+  a.top_logprobs = top_logprobs;
+  a.stream = reinterpret_cast<cudaStream_t>(stream);
+  a.num_sms = sms;
+  return launch_logprobs(a) == cudaSuccess ? FN_OK : FN_ERR_CUDA;
+}
+
+fn_status fn_token_logprobs_backward(const void* logits, fn_dtype type, int64_t M, int64_t V, int64_t ld,
+                                     const int32_t* targets, const float* lse, const float* entropy,
+                                     const float* grad_logprob, const float* grad_entropy, float scale, void* dlogits,
+                                     int64_t ldd, fn_stream_t stream) {
+  if (M < 0 || V <= 0 || ld < V || ldd < V) return FN_ERR_INVALID_ARG;
+  if (type != FN_T_BF16 && type != FN_T_FP16 && type != FN_T_FP32) return FN_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || scale <= 0.0f) return FN_ERR_INVALID_ARG;
+  if (V > kMaxDim || M > kMaxDim || logprobs_bwd_blocks(M, V, type_bytes(type)) > kMaxDim)
+    return FN_ERR_UNSUPPORTED_SHAPE;
+  if (M == 0) return FN_OK;
+  if (!logits || !lse || !dlogits || (!grad_logprob && !grad_entropy)) return FN_ERR_INVALID_ARG;
+  if ((grad_logprob && !targets) || (grad_entropy && !entropy)) return FN_ERR_INVALID_ARG;
+  if (misaligned(logits, type_bytes(type)) || misaligned(dlogits, type_bytes(type)) || misaligned(targets, 4) ||
+      misaligned(lse, 4) || misaligned(entropy, 4) || misaligned(grad_logprob, 4) || misaligned(grad_entropy, 4))
+    return FN_ERR_ALIGNMENT;
+  const size_t rows = static_cast<size_t>(M) * 4;
+  const size_t out = span_bytes(M, V, ldd, type_bytes(type));
+  // the gradient may overwrite the logits in place, not overlap them otherwise
+  if ((logits != dlogits || ld != ldd) && overlaps(dlogits, out, logits, span_bytes(M, V, ld, type_bytes(type))))
+    return FN_ERR_ALIAS;
+  const void* ins[5] = {targets, lse, entropy, grad_logprob, grad_entropy};
+  for (const void* p : ins)
+    if (overlaps(dlogits, out, p, rows)) return FN_ERR_ALIAS;
+  int sms = 0;
+  const fn_status st = check_device(sms);
+  if (st != FN_OK) return st;
+  LogprobBwdArgs a;
+  a.logits = logits;
+  a.type = static_cast<int>(type);
+  a.M = M;
+  a.V = V;
+  a.ld = ld;
+  a.targets = targets;
+  a.lse = lse;
+  a.entropy = entropy;
+  a.grad_logprob = grad_logprob;
+  a.grad_entropy = grad_entropy;
+  a.scale = scale;
+  a.dlogits = dlogits;
+  a.ldd = ldd;
+  a.stream = reinterpret_cast<cudaStream_t>(stream);
+  return launch_logprobs_bwd(a) == cudaSuccess ? FN_OK : FN_ERR_CUDA;
+}
+
 const char* fn_status_string(fn_status s) {
   switch (s) {
     case FN_OK: return "FN_OK";

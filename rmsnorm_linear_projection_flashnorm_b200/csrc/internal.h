@@ -130,6 +130,36 @@ cudaError_t launch_dequant_fp8(const void* q, const float* scales, int64_t d, in
 cudaError_t launch_adaln_shift_bias(const float* shift, int64_t n_cond, const void* W0, const void* W1, int64_t d,
                                     int64_t N, float* B, cudaStream_t s);
 
+// Token log probabilities (logprobs.cu), validated by the ABI layer.
+constexpr int kMaxTopAlternatives = 32;
+struct LogprobArgs {
+  const void* logits;     // [M, V], row stride ld elements
+  int type;               // 0 bf16, 1 fp16, 2 fp32
+  int64_t M, V, ld;
+  const int* targets;     // [M], or null (then logprob is null)
+  float scale;
+  int top_k;              // 0..kMaxTopAlternatives
+  float *logprob, *entropy, *lse;   // fp32 [M], each may be null
+  int* top_ids;           // int32 [M, top_k]
+  float* top_logprobs;    // fp32 [M, top_k]
+  cudaStream_t stream;
+  int num_sms;
+};
+struct LogprobBwdArgs {
+  const void* logits;
+  int type;
+  int64_t M, V, ld;
+  const int* targets;
+  const float *lse, *entropy, *grad_logprob, *grad_entropy;
+  float scale;
+  void* dlogits;
+  int64_t ldd;
+  cudaStream_t stream;
+};
+cudaError_t launch_logprobs(const LogprobArgs& a);
+cudaError_t launch_logprobs_bwd(const LogprobBwdArgs& a);
+int64_t logprobs_bwd_blocks(int64_t M, int64_t V, int elem_bytes);   // grid size of the gradient
+
 // Raise a kernel's dynamic shared-memory limit once per device (a host-only
 // call, done on the first launch so later launches can be graph-captured).
 // One flag set per kernel: the kernel itself is the template argument.

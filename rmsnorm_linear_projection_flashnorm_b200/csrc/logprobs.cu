@@ -1,0 +1,629 @@
+// Log probabilities of given tokens, entropies and top alternatives from the
+// logits of a head projection, and their gradient, sm_100a.
+//
+// With z = scale * logits, m = max z, d_v = z_v - m, over a row of V logits:
+//   s = sum_v e^{d_v},  t = sum_v d_v e^{d_v}
+//   lse = m + ln s,  logprob = d_target - ln s,  entropy = ln s - t / s
+// all from ONE pass over the logits with running (m, s, t): when the maximum
+// grows by D the sums become s' = s e^{-D}, t' = e^{-D} (t - s D).  The
+// products run in the base-2 exponent domain (d log2 e), 32-bit floats.
+//
+// The pass is bound by HBM (2 or 4 bytes per logit, read once).  The SM side
+// stays below it: about 6 issue slots and one ex2 per 16-bit logit, packed
+// fp32 pairs where the arithmetic allows.
+//
+// Top alternatives in the same pass: a logit becomes a 64-bit key, its ordered
+// bit pattern above the complement of its index, so keys are unique, ties go
+// to the lower index and the order of arrival does not matter.  A threshold
+// key, never above the true k-th largest, filters the stream: one comparison
+// per 16-byte vector.  The first tile sets it from the threads' own maxima
+// (the k-th largest of 256 disjoint groups' maxima is a lower bound of the
+// k-th largest element, and at most k groups hold anything above it, which
+// bounds the survivors by k * 32); survivors go to a small buffer that is
+// reduced to its top k by warp bitonic sorts when it fills.  Rows that grow
+// steadily overflow the buffer in a tile; that tile is filtered again under a
+// threshold from its own maxima, so the buffer bound always holds.
+//
+// Work split: one thread-block cluster per row; C = 1, 2, 4 or 8 CTAs, more
+// when there are few rows, so one decoded token still uses 8 SMs.  The CTAs'
+// (m, s, t) and top lists meet in distributed shared memory in rank order:
+// one launch, no workspace, no atomics on results, bit-identical repeats.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace fn {
+namespace lp {
+
+constexpr int THREADS = 256;
+constexpr int WARPS = THREADS / 32;
+constexpr int VECS = 4;                       // 16-byte vectors per thread and tile
+constexpr int MAX_K = kMaxTopAlternatives;    // 32: one key per lane
+constexpr int SOFT = 256;                     // survivors kept before they are reduced
+constexpr int CAP = 1024 + SOFT;              // k * 32 elements of one tile + what was kept
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LN2 = 0.6931471805599453f;
+static_assert(MAX_K == 32, "one list entry per lane");
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either is
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
+// Element types: 16-byte vectors as packed words, the NaN-propagating maximum
+// of a vector, and the unpacked fp32 values.
+template <typename T>
+struct Elem;
+template <>
+struct Elem<__nv_bfloat16> {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ float vmax(const uint4& v) {
+    uint32_t a, b;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(v.x), "r"(v.y));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(v.z), "r"(v.w));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(b));
+    return max_nan(bf16lo_to_f32(a), bf16hi_to_f32(a));
+  }
+  static __device__ __forceinline__ void unpack(const uint4& v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = bf16lo_to_f32(w[i]);
+      f[2 * i + 1] = bf16hi_to_f32(w[i]);
+    }
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                      pack_bf16x2(f[6], f[7]));
+  }
+  static __device__ __forceinline__ float load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+  static __device__ __forceinline__ __nv_bfloat16 from(float f) { return __float2bfloat16_rn(f); }
+};
+template <>
+struct Elem<__half> {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ float vmax(const uint4& v) {
+    uint32_t a, b;
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(a) : "r"(v.x), "r"(v.y));
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(b) : "r"(v.z), "r"(v.w));
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(b));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&a));
+    return max_nan(f.x, f.y);
+  }
+  static __device__ __forceinline__ void unpack(const uint4& v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      f[2 * i] = p.x;
+      f[2 * i + 1] = p.y;
+    }
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  static __device__ __forceinline__ float load(const __half* p) { return __half2float(*p); }
+  static __device__ __forceinline__ __half from(float f) { return __float2half_rn(f); }
+};
+template <>
+struct Elem<float> {
+  static constexpr int N = 4;
+  static __device__ __forceinline__ float vmax(const uint4& v) {
+    return max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)),
+                   max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
+  }
+  static __device__ __forceinline__ void unpack(const uint4& v, float (&f)[4]) {
+    f[0] = __uint_as_float(v.x);
+    f[1] = __uint_as_float(v.y);
+    f[2] = __uint_as_float(v.z);
+    f[3] = __uint_as_float(v.w);
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  }
+  static __device__ __forceinline__ float load(const float* p) { return *p; }
+  static __device__ __forceinline__ float from(float f) { return f; }
+};
+
+// ---------------------------------------------------------------------------
+// keys: (ordered value, complement of the index); 0 is below every real key
+// ---------------------------------------------------------------------------
+using Key = unsigned long long;
+
+__device__ __forceinline__ Key make_key(float v, uint32_t idx) {
+  v += 0.0f;                                        // -0 ties with +0
+  const uint32_t u = __float_as_uint(v);
+  uint32_t o = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  if (v != v) o = 0xFFFFFFFFu;                      // NaN ranks first
+  return (static_cast<Key>(o) << 32) | (0xFFFFFFFFu - idx);
+}
+__device__ __forceinline__ float key_value(Key k) {
+  const uint32_t o = static_cast<uint32_t>(k >> 32);
+  if (o == 0xFFFFFFFFu) return __uint_as_float(0x7FC00000u);
+  return __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
+}
+__device__ __forceinline__ int key_index(Key k) {
+  return static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(k));
+}
+
+// One step of a bitonic network over the lanes: keep the larger key where
+// `keep_max`, else the smaller.
+__device__ __forceinline__ Key cmp_xchg(Key k, int mask, bool keep_max) {
+  const Key o = __shfl_xor_sync(0xffffffffu, k, mask);
+  return (k > o) == keep_max ? k : o;
+}
+// Sort 32 keys over the lanes, largest in lane 0.
+__device__ __forceinline__ Key warp_sort(Key k, int lane) {
+#pragma unroll
+  for (int size = 2; size <= 32; size <<= 1) {
+#pragma unroll
+    for (int j = size >> 1; j > 0; j >>= 1) {
+      const bool down = (lane & size) == 0;          // this run is sorted downwards
+      k = cmp_xchg(k, j, ((lane & j) == 0) == down);
+    }
+  }
+  return k;
+}
+// The 32 largest of two sorted runs, sorted: the larger of a[i] and b[31 - i]
+// is a bitonic run that holds them.
+__device__ __forceinline__ Key warp_merge(Key a, Key b, int lane) {
+  const Key r = __shfl_sync(0xffffffffu, b, 31 - lane);
+  Key k = a > r ? a : r;
+#pragma unroll
+  for (int j = 16; j > 0; j >>= 1) k = cmp_xchg(k, j, (lane & j) == 0);
+  return k;
+}
+
+struct Stat {
+  float m, s, t;   // maximum (raw logits), sum of 2^d, sum of d 2^d, d = (x - m) c
+};
+__device__ __forceinline__ Stat merge_stat(const Stat& a, const Stat& b, float c) {
+  Stat r;
+  r.m = max_nan(a.m, b.m);
+  const float da = a.m == r.m ? 0.f : max_nan((a.m - r.m) * c, -200.f);
+  const float db = b.m == r.m ? 0.f : max_nan((b.m - r.m) * c, -200.f);
+  const float fa = ex2(da), fb = ex2(db);
+  r.s = fa * a.s + fb * b.s;
+  r.t = fa * fmaf(a.s, da, a.t) + fb * fmaf(b.s, db, b.t);
+  return r;
+}
+
+struct Smem {
+  Key buf[CAP];
+  Key lists[WARPS][32];
+  Key top[32];          // this CTA's result, read by rank 0 of the cluster
+  Stat wstat[WARPS];
+  Stat stat;            // this CTA's (m, s, t), read by rank 0
+  int count;
+};
+
+// Reduce n keys (shared memory, or one per thread when buf is null) to the 32
+// largest, sorted, in sm.top.  All threads call; ends with a barrier.
+__device__ __forceinline__ void block_top32(Smem& sm, const Key* buf, int n, Key own, int warp, int lane) {
+  Key best;
+  if (buf) {
+    best = 0;
+    for (int i = warp * 32; i < n; i += THREADS) {
+      const Key k = warp_sort(i + lane < n ? buf[i + lane] : 0, lane);
+      best = i < THREADS ? k : warp_merge(best, k, lane);
+    }
+  } else {
+    best = warp_sort(own, lane);
+  }
+  sm.lists[warp][lane] = best;
+#pragma unroll
+  for (int w = WARPS / 2; w > 0; w >>= 1) {
+    __syncthreads();
+    if (warp < w) {
+      best = warp_merge(best, sm.lists[warp + w][lane], lane);
+      sm.lists[warp][lane] = best;
+    }
+  }
+  if (warp == 0) sm.top[lane] = best;
+  __syncthreads();
+}
+
+struct Params {
+  const void* logits;
+  int64_t ld;
+  int V, C, k;
+  const int* targets;
+  float scale;
+  float *logprob, *entropy, *lse, *top_logprobs;
+  int* top_ids;
+};
+
+template <typename T, bool TOPK>
+__global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const Params p) {
+  using E = Elem<T>;
+  constexpr int N = E::N;
+  __shared__ Smem sm;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = blockIdx.x % p.C;
+  const int64_t row = blockIdx.x / p.C;
+  const T* x = static_cast<const T*>(p.logits) + row * p.ld;
+  const float c = p.scale * LOG2E;
+  grid_dependency_wait();
+  grid_launch_dependents();
+
+  // Scalars up to the first 16-byte boundary, whole vectors, scalars behind
+  // them.  Each rank takes a contiguous share of the vectors, rank 0 the (at
+  // most 2 N - 2) scalars too.
+  const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
+  const int head = min(mis ? N - mis : 0, p.V);
+  const int nv = (p.V - head) / N;
+  const int tail0 = head + nv * N;
+  const int v0 = static_cast<int>(static_cast<int64_t>(nv) * rank / p.C);
+  const int v1 = static_cast<int>(static_cast<int64_t>(nv) * (rank + 1) / p.C);
+  const uint4* xv = reinterpret_cast<const uint4*>(x + head);
+
+  Stat st{-INFINITY, 0.f, 0.f};
+  float thr_v = -INFINITY;
+  Key thr = 0;
+
+  const int nscal = rank == 0 ? head + p.V - tail0 : 0;
+  if (rank == 0) {
+    if (static_cast<int>(threadIdx.x) < nscal) {
+      const int i = static_cast<int>(threadIdx.x);
+      const int idx = i < head ? i : tail0 + i - head;
+      const float v = E::load(x + idx);
+      st.m = v;
+      st.s = v == -INFINITY ? 0.f : (isinf(v) ? NAN : v - v + 1.f);   // NaN for NaN and +inf
+      if (TOPK) sm.buf[i] = make_key(v, idx);
+    }
+  }
+  if (TOPK && threadIdx.x == 0) sm.count = nscal;
+
+  bool first = true;
+  int kept = nscal;                            // keys in the buffer, the same in every thread
+  for (int base = v0; base < v1; base += THREADS * VECS) {
+    uint4 q[VECS];
+    bool have[VECS];
+#pragma unroll
+    for (int j = 0; j < VECS; ++j) {
+      const int i = base + j * THREADS + static_cast<int>(threadIdx.x);
+      have[j] = i < v1;
+      if (have[j]) q[j] = __ldcs(xv + i);
+    }
+    float vm[VECS];
+    float bm = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < VECS; ++j) {
+      vm[j] = have[j] ? E::vmax(q[j]) : -INFINITY;
+      bm = max_nan(bm, vm[j]);
+    }
+    // running softmax statistics
+    if (!(bm <= st.m)) {                       // grows, or NaN
+      if (st.s > 0.f) {
+        const float D = max_nan((st.m - bm) * c, -200.f);
+        const float f = ex2(D);
+        st.t = f * fmaf(st.s, D, st.t);
+        st.s *= f;
+      }
+      st.m = bm;
+    }
+    const float mu = st.m == -INFINITY ? 0.f : st.m;
+    const uint64_t nm2 = f2_pack(-mu, -mu), c2 = f2_pack(c, c);
+    uint64_t s2 = f2_pack(st.s, 0.f), t2 = f2_pack(st.t, 0.f);
+#pragma unroll
+    for (int j = 0; j < VECS; ++j) {
+      if (have[j]) {
+        float f[N];
+        E::unpack(q[j], f);
+#pragma unroll
+        for (int e = 0; e < N; e += 2) {
+          const uint64_t d2 = f2_mul(f2_add(f2_pack(f[e], f[e + 1]), nm2), c2);
+          // masked logits (d = -inf) contribute 0 to both sums, not 0 * inf
+          const float d0 = max_nan(f2_lo(d2), -200.f), d1 = max_nan(f2_hi(d2), -200.f);
+          const uint64_t e2 = f2_pack(ex2(d0), ex2(d1));
+          s2 = f2_add(s2, e2);
+          t2 = f2_fma(f2_pack(d0, d1), e2, t2);
+        }
+      }
+    }
+    st.s = f2_lo(s2) + f2_hi(s2);
+    st.t = f2_lo(t2) + f2_hi(t2);
+
+    if constexpr (TOPK) {
+      auto survivors = [&]() {
+#pragma unroll
+        for (int j = 0; j < VECS; ++j) {
+          if (have[j] && !(vm[j] < thr_v)) {
+            float f[N];
+            E::unpack(q[j], f);
+            const uint32_t i0 = static_cast<uint32_t>(head) + static_cast<uint32_t>(base + j * THREADS + threadIdx.x) * N;
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+              const Key k = make_key(f[e], i0 + e);
+              if (k > thr) {
+                const int pos = atomicAdd(&sm.count, 1);
+                if (pos < CAP) sm.buf[pos] = k;
+              }
+            }
+          }
+        }
+      };
+      __syncthreads();                                  // every thread has read the last count
+      bool again = first;
+      if (!first) {
+        survivors();
+        __syncthreads();
+        again = sm.count > CAP;
+      }
+      if (again) {
+        // threshold from this tile's own maxima: the k-th largest of the
+        // threads' largest keys
+        Key own = 0;
+#pragma unroll
+        for (int j = 0; j < VECS; ++j) {
+          if (have[j]) {
+            float f[N];
+            E::unpack(q[j], f);
+            const uint32_t i0 = static_cast<uint32_t>(head) + static_cast<uint32_t>(base + j * THREADS + threadIdx.x) * N;
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+              const Key k = make_key(f[e], i0 + e);
+              own = k > own ? k : own;
+            }
+          }
+        }
+        block_top32(sm, nullptr, 0, own, warp, lane);
+        const Key kth = sm.top[p.k - 1];
+        if (kth != 0 && kth - 1 > thr) thr = kth - 1;   // keys >= kth survive
+        thr_v = thr ? key_value(thr + 1) : -INFINITY;
+        if (threadIdx.x == 0) sm.count = kept;
+        __syncthreads();
+        survivors();
+        __syncthreads();
+      }
+      first = false;
+      kept = sm.count;                                  // <= CAP: k * 32 + SOFT
+      if (kept > SOFT) {
+        block_top32(sm, sm.buf, kept, 0, warp, lane);
+        thr = sm.top[p.k - 1];                          // kept > SOFT >= k: a real key, already there
+        thr_v = key_value(thr);
+        if (warp == 0) sm.buf[lane] = sm.top[lane];
+        kept = p.k;
+        if (threadIdx.x == 0) sm.count = kept;
+      }
+    }
+  }
+
+  // this CTA's statistics, fixed order
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    Stat b;
+    b.m = __shfl_down_sync(0xffffffffu, st.m, o);
+    b.s = __shfl_down_sync(0xffffffffu, st.s, o);
+    b.t = __shfl_down_sync(0xffffffffu, st.t, o);
+    st = merge_stat(st, b, c);
+  }
+  if (lane == 0) sm.wstat[warp] = st;
+  __syncthreads();
+  if (TOPK) block_top32(sm, sm.buf, kept, 0, warp, lane);
+  if (threadIdx.x == 0) {
+    Stat a = sm.wstat[0];
+    for (int w = 1; w < WARPS; ++w) a = merge_stat(a, sm.wstat[w], c);
+    sm.stat = a;
+  }
+  Key best = TOPK && warp == 0 ? sm.top[lane] : 0;
+  if (p.C > 1) {
+    cluster_sync_all();
+    if (rank == 0 && warp == 0) {
+      Stat a = sm.stat;
+      for (int r = 1; r < p.C; ++r) {
+        const uint32_t sa = dsmem_addr(&sm.stat, r);
+        Stat b;
+        b.m = dsmem_ld_f32(sa);
+        b.s = dsmem_ld_f32(sa + 4);
+        b.t = dsmem_ld_f32(sa + 8);
+        a = merge_stat(a, b, c);
+        if (TOPK) best = warp_merge(best, dsmem_ld_u64(dsmem_addr(&sm.top[lane], r)), lane);
+      }
+      if (lane == 0) sm.stat = a;
+      __syncwarp();
+    }
+    cluster_sync_all();          // peers stay until rank 0 has read them
+  } else {
+    __syncthreads();
+  }
+  if (rank != 0 || warp != 0) return;
+
+  const Stat a = sm.stat;
+  const float zmax = a.m * p.scale;
+  const bool empty = zmax == -INFINITY;      // the mask leaves nothing
+  const float ls = logf(a.s);
+  if (TOPK && lane < p.k) {
+    p.top_ids[row * p.k + lane] = key_index(best);
+    p.top_logprobs[row * p.k + lane] = empty ? -INFINITY : (key_value(best) - a.m) * p.scale - ls;
+  }
+  if (lane == 0) {
+    if (p.lse) p.lse[row] = empty ? -INFINITY : zmax + ls;
+    if (p.entropy) {
+      const float h = ls - a.t / a.s * LN2;
+      p.entropy[row] = empty || h < 0.f ? 0.f : h;
+    }
+    if (p.logprob) {
+      const int t = p.targets[row];
+      float v = 0.f;                         // no token
+      if (t >= p.V) v = NAN;                 // nothing is read out of range
+      else if (t >= 0) v = empty ? -INFINITY : (E::load(x + t) - a.m) * p.scale - ls;
+      p.logprob[row] = v;
+    }
+  }
+}
+
+template <typename T>
+cudaError_t launch_fwd(const LogprobArgs& a) {
+  Params p;
+  p.logits = a.logits;
+  p.ld = a.ld;
+  p.V = static_cast<int>(a.V);
+  p.k = a.top_k;
+  p.targets = a.targets;
+  p.scale = a.scale;
+  p.logprob = a.logprob;
+  p.entropy = a.entropy;
+  p.lse = a.lse;
+  p.top_ids = a.top_ids;
+  p.top_logprobs = a.top_logprobs;
+  // CTAs per row: as many as keep every CTA at least one full tile and the
+  // grid within two waves of the 4 CTAs an SM holds
+  constexpr int64_t TILE = static_cast<int64_t>(THREADS) * VECS * Elem<T>::N;
+  int C = 1;
+  while (C < 8 && a.M * C * 2 <= 8LL * a.num_sms && a.V >= TILE * C * 2) C *= 2;
+  p.C = C;
+  const unsigned grid = static_cast<unsigned>(a.M * C);
+  if (a.top_k > 0) {
+    return C > 1 ? launch_pdl_cluster(logprobs_kernel<T, true>, grid, C, THREADS, 0, a.stream, p)
+                 : launch_pdl(logprobs_kernel<T, true>, grid, THREADS, 0, a.stream, p);
+  }
+  return C > 1 ? launch_pdl_cluster(logprobs_kernel<T, false>, grid, C, THREADS, 0, a.stream, p)
+               : launch_pdl(logprobs_kernel<T, false>, grid, THREADS, 0, a.stream, p);
+}
+
+// ---------------------------------------------------------------------------
+// gradient
+// ---------------------------------------------------------------------------
+// dlogits_v = scale * (gl (1[v = target] - p_v) - gh p_v (log p_v + H)) with
+// p_v = e^{z_v - lse}: one read and one write of the row, bound by HBM.  A
+// thread reads and writes the same elements, so the gradient may overwrite
+// the logits.
+constexpr int BWD_VECS = 4;
+
+struct BwdParams {
+  const void* logits;
+  void* dlogits;
+  int64_t ld, ldd;
+  int V, chunks;
+  const int* targets;
+  const float *lse, *entropy, *gl, *gh;
+  float scale;
+};
+
+template <bool FAST>
+__device__ __forceinline__ float grad_of(float x, float scale, float lse, float gl, float gh, float H) {
+  const float lp = fmaf(x, scale, -lse);
+  const float pv = FAST ? ex2(lp * LOG2E) : expf(lp);
+  // masked: p = 0 and log p = -inf, no gradient
+  return pv == 0.f ? 0.f : -scale * pv * fmaf(gh, lp + H, gl);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(THREADS) logprobs_bwd_kernel(const BwdParams p) {
+  using E = Elem<T>;
+  constexpr int N = E::N;
+  constexpr bool FAST = sizeof(T) == 2;      // the result is rounded to 8 or 11 bits anyway
+  const int64_t row = blockIdx.x / p.chunks;
+  const int chunk = static_cast<int>(blockIdx.x % p.chunks);
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const T* x = static_cast<const T*>(p.logits) + row * p.ld;
+  T* dx = static_cast<T*>(p.dlogits) + row * p.ldd;
+  const int t = p.gl ? __ldg(p.targets + row) : -1;
+  const float gl = t < 0 ? 0.f : t >= p.V ? NAN : __ldg(p.gl + row);
+  const float gh = p.gh ? __ldg(p.gh + row) : 0.f;
+  const float H = p.gh ? __ldg(p.entropy + row) : 0.f;
+  const float lse = __ldg(p.lse + row);
+  const float hot = gl * p.scale;
+  const bool empty = lse == -INFINITY;
+  const int lo = static_cast<int>(static_cast<int64_t>(p.V) * chunk / p.chunks);
+  const int hi = static_cast<int>(static_cast<int64_t>(p.V) * (chunk + 1) / p.chunks);
+  auto one = [&](int i) {
+    float g = empty ? 0.f : grad_of<FAST>(E::load(x + i), p.scale, lse, gl, gh, H);
+    if (i == t && !empty) g += hot;
+    dx[i] = E::from(g);
+  };
+  const uintptr_t ax = reinterpret_cast<uintptr_t>(x + lo), ad = reinterpret_cast<uintptr_t>(dx + lo);
+  if (((ax ^ ad) & 15u) != 0) {              // the rows lie differently to 16-byte boundaries
+    for (int i = lo + static_cast<int>(threadIdx.x); i < hi; i += THREADS) one(i);
+    return;
+  }
+  const int mis = static_cast<int>((ax & 15u) / sizeof(T));
+  const int b = min(lo + (mis ? N - mis : 0), hi);
+  const int nv = (hi - b) / N;
+  const int e0 = b + nv * N;
+  if (lo + static_cast<int>(threadIdx.x) < b) one(lo + static_cast<int>(threadIdx.x));
+  if (e0 + static_cast<int>(threadIdx.x) < hi) one(e0 + static_cast<int>(threadIdx.x));
+  const uint4* xv = reinterpret_cast<const uint4*>(x + b);
+  uint4* dv = reinterpret_cast<uint4*>(dx + b);
+  for (int base = 0; base < nv; base += THREADS * BWD_VECS) {
+    uint4 q[BWD_VECS];
+#pragma unroll
+    for (int j = 0; j < BWD_VECS; ++j) {
+      const int i = base + j * THREADS + static_cast<int>(threadIdx.x);
+      if (i < nv) q[j] = __ldcs(xv + i);
+    }
+#pragma unroll
+    for (int j = 0; j < BWD_VECS; ++j) {
+      const int i = base + j * THREADS + static_cast<int>(threadIdx.x);
+      if (i < nv) {
+        float f[N];
+        E::unpack(q[j], f);
+        const int rel = t - (b + i * N);       // the target's place in this vector
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          float g = grad_of<FAST>(f[e], p.scale, lse, gl, gh, H);
+          if (rel == e) g += hot;
+          f[e] = empty ? 0.f : g;
+        }
+        __stcs(dv + i, E::pack(f));
+      }
+    }
+  }
+}
+
+template <typename T>
+cudaError_t launch_bwd(const LogprobBwdArgs& a) {
+  BwdParams p;
+  p.logits = a.logits;
+  p.dlogits = a.dlogits;
+  p.ld = a.ld;
+  p.ldd = a.ldd;
+  p.V = static_cast<int>(a.V);
+  constexpr int64_t TILE = static_cast<int64_t>(THREADS) * BWD_VECS * Elem<T>::N;
+  p.chunks = static_cast<int>((a.V + TILE - 1) / TILE);
+  p.targets = a.targets;
+  p.lse = a.lse;
+  p.entropy = a.entropy;
+  p.gl = a.grad_logprob;
+  p.gh = a.grad_entropy;
+  p.scale = a.scale;
+  return launch_pdl(logprobs_bwd_kernel<T>, static_cast<unsigned>(a.M * p.chunks), THREADS, 0, a.stream, p);
+}
+
+}  // namespace lp
+
+int64_t logprobs_bwd_blocks(int64_t M, int64_t V, int elem_bytes) {
+  const int64_t tile = static_cast<int64_t>(lp::THREADS) * lp::BWD_VECS * (16 / elem_bytes);
+  return M * ((V + tile - 1) / tile);
+}
+
+cudaError_t launch_logprobs(const LogprobArgs& a) {
+  if (a.type == 0) return lp::launch_fwd<__nv_bfloat16>(a);
+  if (a.type == 1) return lp::launch_fwd<__half>(a);
+  return lp::launch_fwd<float>(a);
+}
+
+cudaError_t launch_logprobs_bwd(const LogprobBwdArgs& a) {
+  if (a.type == 0) return lp::launch_bwd<__nv_bfloat16>(a);
+  if (a.type == 1) return lp::launch_bwd<__half>(a);
+  return lp::launch_bwd<float>(a);
+}
+
+}  // namespace fn

@@ -3,14 +3,14 @@ with torch (device memory is torch's job here) and call the library.  No
 arithmetic of the method happens in Python."""
 from __future__ import annotations
 
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 
-from . import (FN_W_BF16, FN_W_FP8_E4M3_B128, FN_W_MXFP8_E4M3, check, fn_adaln_shift_bias, fn_norm_proj_adaln,
+from . import (FN_T_BF16, FN_T_FP16, FN_T_FP32, FN_W_BF16, FN_W_FP8_E4M3_B128, FN_W_MXFP8_E4M3, check, fn_adaln_shift_bias, fn_norm_proj_adaln,
                fn_norm_proj_swiglu_nvfp4_swizzled, fn_workspace_size_adaln, fn_fold_weights, fn_norm_proj, fn_norm_proj_swiglu,
                fn_norm_proj_partial, fn_norm_proj_swiglu_nvfp4, fn_post_scale, fn_query_device_status,
-               fn_workspace_size)
+               fn_token_logprobs, fn_token_logprobs_backward, fn_workspace_size)
 
 
 def weight_type(Wp: torch.Tensor, scales: Optional[torch.Tensor]) -> int:
@@ -163,4 +163,106 @@ def norm_proj_adaln(x: torch.Tensor, Wp: torch.Tensor, N: int, eps: float, adaln
         out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
     check(fn_norm_proj_adaln(x, M, d, Wp, scales, wt, N, int(swiglu), eps, adaln_scale, shift_bias, adaln_index,
                              adaln_scale.shape[0], out, ws.buf, ws.buf.numel(), stream), "fn_norm_proj_adaln")
+    return out
+
+
+# --------------------------------------------------------------------------
+# operators next to the fused projections
+# --------------------------------------------------------------------------
+_DTYPE = {torch.bfloat16: FN_T_BF16, torch.float16: FN_T_FP16, torch.float32: FN_T_FP32}
+
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _rows(t: torch.Tensor, name: str, dtypes, shape=None) -> int:
+    """Check a matrix with contiguous rows; returns its row stride."""
+    _need(t.dim() == 2 and t.dtype in dtypes, f"{name}: a matrix of {[str(d) for d in dtypes]} is needed")
+    _need(shape is None or tuple(t.shape) == tuple(shape), f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    _need(t.stride(1) == 1 or t.shape[1] == 1, f"{name}: rows must be contiguous")
+    # a single row has no stride of its own; overlapping rows are refused by the library
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _vec(t: Optional[torch.Tensor], name: str, dtype, n: int, dev) -> None:
+    if t is not None:
+        _need(t.dtype == dtype and t.shape == (n,) and t.is_contiguous() and t.device == dev,
+              f"{name}: a contiguous {dtype} vector of {n} on {dev} is needed")
+
+
+class _on:
+    """Run on the device that holds the tensors, whatever the current one is;
+    gives the stream to launch on (the device's current one by default)."""
+
+    def __init__(self, dev: torch.device, stream):
+        _need(dev.type == "cuda", f"tensors on {dev}: a CUDA device is needed")
+        self.guard = torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else None
+        self.stream = torch.cuda.current_stream(dev) if stream is None else stream
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self.stream
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+class TokenLogprobs(NamedTuple):
+    logprob: Optional[torch.Tensor]      # fp32 [M] (None without targets)
+    entropy: torch.Tensor                # fp32 [M]
+    lse: torch.Tensor                    # fp32 [M]
+    top_ids: torch.Tensor                # int32 [M, top_k]
+    top_logprobs: torch.Tensor           # fp32 [M, top_k]
+
+
+def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None, top_k: int = 0, scale: float = 1.0,
+                   out: Optional[TokenLogprobs] = None, stream=None) -> TokenLogprobs:
+    """Log probabilities of the int32 `targets` [M] under softmax(scale * logits),
+    the rows' entropies and log sums, and the top_k alternatives (see
+    fn_token_logprobs).  logits: bf16, fp16 or fp32 [M, V], rows contiguous."""
+    ld = _rows(logits, "logits", _DTYPE)
+    M, V = logits.shape
+    dev = logits.device
+    _vec(targets, "targets", torch.int32, M, dev)
+    if out is None:
+        f = torch.empty((3, M), dtype=torch.float32, device=dev)
+        out = TokenLogprobs(f[0] if targets is not None else None, f[1], f[2],
+                            torch.empty((M, top_k), dtype=torch.int32, device=dev),
+                            torch.empty((M, top_k), dtype=torch.float32, device=dev))
+    else:
+        for t, n in ((out.logprob, "logprob"), (out.entropy, "entropy"), (out.lse, "lse")):
+            _vec(t, n, torch.float32, M, dev)
+        for t, d in ((out.top_ids, torch.int32), (out.top_logprobs, torch.float32)):
+            _need(t.dtype == d and t.shape == (M, top_k) and t.is_contiguous() and t.device == dev,
+                  f"top alternatives: contiguous [{M}, {top_k}] outputs on {dev} are needed")
+    with _on(dev, stream) as s:
+        check(fn_token_logprobs(logits, _DTYPE[logits.dtype], M, V, ld, targets, scale, top_k, out.logprob,
+                                out.entropy, out.lse, out.top_ids if top_k else None,
+                                out.top_logprobs if top_k else None, s), "fn_token_logprobs")
+    return out
+
+
+def token_logprobs_backward(logits: torch.Tensor, targets: Optional[torch.Tensor], lse: torch.Tensor,
+                            entropy: Optional[torch.Tensor], grad_logprob: Optional[torch.Tensor],
+                            grad_entropy: Optional[torch.Tensor] = None, scale: float = 1.0,
+                            out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Gradient of token_logprobs' logprob and entropy with respect to the
+    logits (see fn_token_logprobs_backward); `out` may be the logits."""
+    ld = _rows(logits, "logits", _DTYPE)
+    M, V = logits.shape
+    dev = logits.device
+    _vec(targets, "targets", torch.int32, M, dev)
+    for t, n in ((lse, "lse"), (entropy, "entropy"), (grad_logprob, "grad_logprob"), (grad_entropy, "grad_entropy")):
+        _vec(t, n, torch.float32, M, dev)
+    if out is None:
+        out = torch.empty((M, V), dtype=logits.dtype, device=dev)
+    ldd = _rows(out, "out", (logits.dtype,), (M, V))
+    _need(out.device == dev, f"out on {out.device}, logits on {dev}")
+    with _on(dev, stream) as s:
+        check(fn_token_logprobs_backward(logits, _DTYPE[logits.dtype], M, V, ld, targets, lse, entropy, grad_logprob,
+                                         grad_entropy, scale, out, ldd, s), "fn_token_logprobs_backward")
     return out

@@ -1,0 +1,410 @@
+"""Token log probabilities, entropies, top alternatives and their gradient:
+refusals and the oracle on the CPU, parity on the GPU.
+
+Tolerances, with u = 2^-24 (half a step of fp32).  Forward: d = (z - max) is
+rounded a few times (relative 4 u), which moves s = sum e^d by at most
+4 u sum |d| e^d <= 4 u s (ln V + 1); ex2.approx adds 2^-22 = 4 u per term; a
+thread adds at most V / 256 + 64 terms one after another (u each).  So ln s is
+off by at most (4 (ln V + 1) + 4 + V / 256 + 64 + 1) u, and a difference or
+product on the way out adds 4 u of its value and of the largest |z| (lse).
+t / s is a mean of d under p, with the same relative error per term.
+Gradient: log p = z scale - lse carries u (|z| + 2 |lse|) from lse's own
+rounding and the fused multiply-add, ex2 its argument's rounding u |log p| and
+4 u; then one round to the output type, eps / 2 of the value.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+import rmsnorm_linear_projection_flashnorm_b200 as fnb
+from rmsnorm_linear_projection_flashnorm_b200 import torch_api as T
+
+U = 2.0 ** -24
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+A, B, C, D, E = (1 << 30), (1 << 34), (1 << 35), (1 << 36), (1 << 37)
+
+
+# ------------------------------------------------------------------ CPU: refusals
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    fnb.build()
+    fnb.lib()
+
+
+def fwd_(logits=A, type=0, M=4, V=1000, ld=1000, t=B, scale=1.0, k=5, lp=C, H=C + 64, lse=C + 128, ids=D, top=E):
+    return fnb.fn_token_logprobs(logits, type, M, V, ld, t, scale, k, lp, H, lse, ids, top, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(M=-1), fnb.FN_ERR_INVALID_ARG),
+    (dict(V=0), fnb.FN_ERR_INVALID_ARG),
+    (dict(ld=999), fnb.FN_ERR_INVALID_ARG),
+    (dict(type=3), fnb.FN_ERR_INVALID_ARG),
+    (dict(scale=0.0), fnb.FN_ERR_INVALID_ARG),
+    (dict(scale=float("nan")), fnb.FN_ERR_INVALID_ARG),
+    (dict(scale=float("inf")), fnb.FN_ERR_INVALID_ARG),
+    (dict(k=-1), fnb.FN_ERR_INVALID_ARG),
+    (dict(k=4, V=3, ld=3), fnb.FN_ERR_INVALID_ARG),
+    (dict(k=33), fnb.FN_ERR_UNSUPPORTED_SHAPE),
+    (dict(M=1 << 28), fnb.FN_ERR_UNSUPPORTED_SHAPE),
+    (dict(V=1 << 31, ld=1 << 31), fnb.FN_ERR_UNSUPPORTED_SHAPE),
+    (dict(logits=None), fnb.FN_ERR_INVALID_ARG),
+    (dict(t=None), fnb.FN_ERR_INVALID_ARG),
+    (dict(ids=None), fnb.FN_ERR_INVALID_ARG),
+    (dict(top=None), fnb.FN_ERR_INVALID_ARG),
+    (dict(k=0), fnb.FN_ERR_INVALID_ARG),                       # top outputs without a top_k
+    (dict(k=0, ids=None, top=None, lp=None, H=None, lse=None), fnb.FN_ERR_INVALID_ARG),
+    (dict(logits=A + 1), fnb.FN_ERR_ALIGNMENT),
+    (dict(type=2, logits=A + 2), fnb.FN_ERR_ALIGNMENT),
+    (dict(t=B + 2), fnb.FN_ERR_ALIGNMENT),
+    (dict(lse=C + 130), fnb.FN_ERR_ALIGNMENT),
+    (dict(lp=A + 4), fnb.FN_ERR_ALIAS),
+    (dict(H=C + 8), fnb.FN_ERR_ALIAS),                         # entropy overlaps logprob
+    (dict(top=D + 40), fnb.FN_ERR_ALIAS),                      # 4 x 5 ids: 80 bytes
+    (dict(ids=B + 12), fnb.FN_ERR_ALIAS),
+])
+def test_forward_refusals(kw, code):
+    assert fwd_(**kw) == code
+
+
+def bwd_(logits=A, type=0, M=4, V=1000, ld=1000, t=B, lse=C, H=C + 64, gl=C + 128, gh=C + 192, scale=1.0, d=D, ldd=1000):
+    return fnb.fn_token_logprobs_backward(logits, type, M, V, ld, t, lse, H, gl, gh, scale, d, ldd, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(M=-1), fnb.FN_ERR_INVALID_ARG),
+    (dict(ldd=999), fnb.FN_ERR_INVALID_ARG),
+    (dict(type=-1), fnb.FN_ERR_INVALID_ARG),
+    (dict(scale=-1.0), fnb.FN_ERR_INVALID_ARG),
+    (dict(lse=None), fnb.FN_ERR_INVALID_ARG),
+    (dict(d=None), fnb.FN_ERR_INVALID_ARG),
+    (dict(t=None), fnb.FN_ERR_INVALID_ARG),
+    (dict(H=None), fnb.FN_ERR_INVALID_ARG),
+    (dict(gl=None, gh=None), fnb.FN_ERR_INVALID_ARG),
+    (dict(M=(1 << 31) - 1, V=100000, ld=100000, ldd=100000), fnb.FN_ERR_UNSUPPORTED_SHAPE),
+    (dict(d=D + 1), fnb.FN_ERR_ALIGNMENT),
+    (dict(gl=C + 129), fnb.FN_ERR_ALIGNMENT),
+    (dict(d=A + 2), fnb.FN_ERR_ALIAS),                         # overlaps the logits, not in place
+    (dict(d=A, ldd=1001), fnb.FN_ERR_ALIAS),                   # in place with another row stride
+    (dict(d=C - 4000), fnb.FN_ERR_ALIAS),                      # overlaps lse
+])
+def test_backward_refusals(kw, code):
+    assert bwd_(**kw) == code
+
+
+def test_empty_batch_is_a_noop():
+    assert fwd_(M=0, logits=None, t=None) == fnb.FN_OK
+    assert bwd_(M=0, logits=None, lse=None, d=None) == fnb.FN_OK
+
+
+def test_torch_api_refuses_what_the_library_cannot_see():
+    x = torch.zeros(2, 8)
+    t = torch.zeros(2, dtype=torch.int32)
+    for bad in (lambda: T.token_logprobs(x, t),                                # not on a GPU
+                lambda: T.token_logprobs(x.double(), t),
+                lambda: T.token_logprobs(x[0], t),
+                lambda: T.token_logprobs(x, t.long()),
+                lambda: T.token_logprobs(x, t[:1]),
+                lambda: T.token_logprobs(x.t().contiguous().t(), t),
+                lambda: T.token_logprobs_backward(x, t, torch.zeros(3), None, torch.zeros(2)),
+                lambda: T.token_logprobs_backward(x, t, torch.zeros(2), None, torch.zeros(2).double()),
+                lambda: T.token_logprobs_backward(x, t, torch.zeros(2), None, torch.zeros(2), out=x.half())):
+        with pytest.raises(ValueError):
+            bad()
+
+
+# ------------------------------------------------------------------ CPU: the oracle
+def test_oracle_against_brute_force_and_differences():
+    rng = np.random.default_rng(0)
+    x = rng.standard_normal((3, 7))
+    x[1, 2] = -np.inf
+    t = np.array([3, 0, -1])
+    lp, H, lse, ids, top = O.token_logprobs(x, t, 3, 0.5)
+    p = np.exp(0.5 * x) / np.exp(0.5 * x).sum(1, keepdims=True)
+    assert np.allclose(lp, [math.log(p[0, 3]), math.log(p[1, 0]), 0.0], atol=1e-13)
+    assert np.allclose(H, [-sum(v * math.log(v) for v in r if v > 0) for r in p], atol=1e-13)
+    assert np.allclose(np.exp(lse), np.exp(0.5 * x).sum(1))
+    assert np.array_equal(ids[0], np.argsort(-x[0])[:3]) and np.allclose(np.exp(top[0]), np.sort(p[0])[::-1][:3])
+    gl, gh = rng.standard_normal(3), rng.standard_normal(3)
+    g = O.token_logprobs_grad(x, t, gl, gh, 0.5)
+    f = lambda z: (lambda r: np.sum(gl * r[0]) + np.sum(gh * r[1]))(O.token_logprobs(z, t, 0, 0.5))
+    for i in range(3):
+        for j in range(7):
+            if np.isfinite(x[i, j]):
+                e = np.zeros_like(x)
+                e[i, j] = 1e-6
+                assert abs((f(x + e) - f(x - e)) / 2e-6 - g[i, j]) < 1e-8
+
+
+def test_oracle_order_of_ties_and_nan():
+    x = np.array([[1.0, 2.0, 2.0, 0.0, -0.0, 1.0]])
+    assert O.token_logprobs(x, None, 6)[3].tolist() == [[1, 2, 0, 5, 3, 4]]
+    x = np.array([[1.0, np.nan, np.inf, np.nan, -np.inf]])
+    assert O.token_logprobs(x, None, 5)[3].tolist() == [[1, 3, 2, 0, 4]]
+
+
+# ------------------------------------------------------------------ GPU: parity
+def logits_(M, V, ld, dtype, seed, spread=3.0, masked=0.0, offset=0):
+    gen = torch.Generator().manual_seed(seed)
+    buf = torch.randn(M * ld + offset, generator=gen) * spread
+    if masked:
+        buf[torch.rand(buf.shape, generator=gen) < masked] = -math.inf
+    buf = buf.to(DT[dtype]).cuda()
+    return buf[offset:].view(M, ld)[:, :V]
+
+
+def targets_(M, V, seed):
+    rng = np.random.default_rng(seed)
+    t = rng.integers(0, V, M).astype(np.int32)
+    if M > 2:
+        t[1] = -1
+    return t
+
+
+def check_fwd(x, t, k, scale):
+    r = T.token_logprobs(x, torch.from_numpy(t).cuda(), top_k=k, scale=scale)
+    torch.cuda.synchronize()
+    xc = x.float().cpu()
+    lp, H, lse, ids, top = O.token_logprobs(xc, t, k, scale)
+    V = x.shape[1]
+    ls = (4 * (math.log(V) + 1) + V / 256 + 69) * U
+    with np.errstate(all="ignore"):
+        big = np.nan_to_num(np.abs(np.where(np.isfinite(xc.numpy()), xc.numpy(), 0.0)).max(1) * scale)
+    assert np.array_equal(r.top_ids.cpu().numpy(), ids)
+
+    def close(got, ref, tol):
+        got, ref = got.cpu().double().numpy(), np.asarray(ref)
+        assert np.array_equal(np.isnan(got), np.isnan(ref))
+        fin = np.isfinite(ref)
+        assert np.array_equal(got[~fin & ~np.isnan(ref)], ref[~fin & ~np.isnan(ref)])
+        tol = np.broadcast_to(tol, ref.shape)
+        assert np.all(np.abs(got[fin] - ref[fin]) <= tol[fin]), np.max(np.abs(got[fin] - ref[fin]) - tol[fin])
+
+    fin = lambda a: np.where(np.isfinite(a), np.abs(a), 0.0)
+    close(r.logprob, lp, ls + 4 * U * (fin(lp) + 1) + 4 * U * fin(lp))
+    close(r.lse, lse, ls + 4 * U * (fin(lse) + big))
+    close(r.entropy, H, 2 * ls * (1 + math.log(V)) + 4 * U * (fin(H) + 1))
+    close(r.top_logprobs, top, ls + 8 * U * (fin(top) + 1))
+    return r
+
+
+SHAPES = [(1, 1), (1, 2), (3, 5), (2, 31), (5, 257), (4, 1000), (1, 8192), (3, 8193), (2, 16384 + 9), (1, 50021),
+          (1, 131072), (40, 32003), (700, 4099)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("M,V", SHAPES)
+def test_forward(M, V, dtype):
+    x = logits_(M, V, V + (M > 1) * (V % 3), dtype, seed=M * 1000 + V, offset=V % 5)
+    check_fwd(x, targets_(M, V, V), min(V, 20), 1.0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("k", [0, 1, 2, 31, 32])
+def test_forward_top_k(k):
+    check_fwd(logits_(3, 40000, 40000, "bf16", seed=k), targets_(3, 40000, k), k, 0.7)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scale", [0.25, 3.0])
+@pytest.mark.parametrize("masked", [0.3, 0.999])
+def test_forward_masked(masked, scale):
+    x = logits_(5, 30011, 30011, "fp32", seed=1, masked=masked)
+    x[3] = -math.inf                       # nothing left
+    x[4, 1:] = -math.inf                   # one token left
+    x[4, 0] = 2.0
+    t = targets_(5, 30011, 2)
+    t[4] = 0
+    check_fwd(x, t, 32, scale)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("order", ["up", "down", "flat", "steps", "saw"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_forward_orders(order, dtype):
+    """Rows that grow steadily (every tile overflows the survivor buffer), fall,
+    are constant (ties everywhere), or tie in long runs."""
+    V = 70001
+    i = torch.arange(V, dtype=torch.float32)
+    row = {"up": i / V * 20 - 10, "down": 10 - i / V * 20, "flat": torch.full((V,), 0.5),
+           "steps": torch.floor(i / 5000) - 7, "saw": (i % 64) / 8}[order]
+    x = row.to(DT[dtype]).expand(3, V).contiguous().cuda()
+    check_fwd(x, targets_(3, V, 0), 32, 1.0)
+
+
+@pytest.mark.gpu
+def test_forward_signed_zeros_infinities_and_nan():
+    x = torch.zeros(6, 9000)
+    x[0, ::2] = -0.0                       # -0 ties with +0
+    x[1, 17] = math.nan
+    x[2, 8999] = math.inf
+    x[3, 5] = math.nan
+    x[3, 8000] = math.inf
+    x[4] = torch.finfo(torch.float32).min  # masked by the type's lowest value: uniform
+    x[5, 1:] = torch.finfo(torch.float32).min
+    t = np.array([1, 2, 3, 4, 5, 0], dtype=np.int32)
+    x = x.cuda()
+    r = T.token_logprobs(x, torch.from_numpy(t).cuda(), top_k=4)
+    torch.cuda.synchronize()
+    lp, H, lse, ids, top = O.token_logprobs(x.cpu(), t, 4)
+    assert np.array_equal(r.top_ids.cpu().numpy(), ids)
+    for got, ref in ((r.logprob, lp), (r.entropy, H), (r.lse, lse), (r.top_logprobs, top)):
+        got = got.cpu().double().numpy()
+        assert np.array_equal(np.isnan(got), np.isnan(ref))
+        ok = ~np.isnan(ref)
+        assert np.allclose(got[ok], ref[ok], rtol=1e-5, atol=1e-5)
+
+
+@pytest.mark.gpu
+def test_forward_target_out_of_range_and_optional_outputs():
+    x = logits_(3, 100, 100, "bf16", seed=3)
+    t = torch.tensor([100, 2**31 - 1, -2**31], dtype=torch.int32, device="cuda")
+    lp = T.token_logprobs(x, t).logprob.cpu()
+    assert torch.isnan(lp[:2]).all() and lp[2] == 0
+    r = T.token_logprobs(x)
+    assert r.logprob is None and r.top_ids.shape == (3, 0)
+    # each output alone
+    for i in range(4):
+        o = [torch.full((3,), 7.0, device="cuda") if j == i else None for j in range(3)]
+        ids = torch.empty((3, 2), dtype=torch.int32, device="cuda") if i == 3 else None
+        top = torch.empty((3, 2), device="cuda") if i == 3 else None
+        fnb.check(fnb.fn_token_logprobs(x, 0, 3, 100, 100, t, 1.0, 2 if i == 3 else 0, *o, ids, top))
+    torch.cuda.synchronize()
+
+
+@pytest.mark.gpu
+def test_rows_behind_the_outputs_stay_and_repeats_are_equal():
+    x = logits_(9, 20011, 20011, "bf16", seed=5)
+    t = torch.from_numpy(targets_(9, 20011, 1)).cuda()
+    f = torch.full((4, 12), 9.0, device="cuda")
+    ids = torch.full((12, 8), 9, dtype=torch.int32, device="cuda")
+    top = torch.full((12, 8), 9.0, device="cuda")
+    runs = []
+    for _ in range(3):
+        out = T.TokenLogprobs(f[0, :9], f[1, :9], f[2, :9], ids[:9], top[:9])
+        T.token_logprobs(x, t, top_k=8, out=out)
+        torch.cuda.synchronize()
+        runs.append([v.clone() for v in out])
+    assert all(torch.equal(a, b) for r in runs[1:] for a, b in zip(runs[0], r))
+    assert (f[:3, 9:] == 9).all() and (f[3] == 9).all() and (ids[9:] == 9).all() and (top[9:] == 9).all()
+
+
+def check_bwd(x, t, gl, gh, scale, out=None):
+    tg = torch.from_numpy(t).cuda()
+    ref = O.token_logprobs_grad(x.float().cpu(), t, gl, gh, scale)
+    xc = np.abs(np.where(np.isfinite(x.float().cpu().numpy()), x.float().cpu().numpy(), 0.0)) * scale
+    r = T.token_logprobs(x, tg, scale=scale)
+    cu = lambda a: None if a is None else torch.from_numpy(a).cuda()
+    lse = np.nan_to_num(r.lse.cpu().numpy().astype(np.float64), neginf=0.0)
+    Hn = r.entropy.cpu().numpy().astype(np.float64)
+    g = T.token_logprobs_backward(x, tg, r.lse, r.entropy, cu(gl), cu(gh), scale=scale, out=out)
+    torch.cuda.synchronize()
+    got = g.double().cpu().numpy()
+    V = x.shape[1]
+    ls = (4 * (math.log(V) + 1) + V / 256 + 69) * U            # lse's own error
+    eh = 2 * ls * (1 + math.log(V)) + 4 * U * (Hn[:, None] + 1)
+    elp = ls + U * (2 * xc + 4 * np.abs(lse)[:, None])         # error of log p
+    lp = xc + np.abs(lse)[:, None]
+    rel_p = elp + 4 * U + 2 * U * lp
+    agl = np.abs(gl)[:, None] if gl is not None else 0.0
+    agh = np.abs(gh)[:, None] if gh is not None else 0.0
+    p = np.minimum(1.0, np.exp(np.minimum(0.0, np.where(np.isfinite(x.float().cpu().numpy()),
+                                                       x.float().cpu().numpy() * scale - lse[:, None], -np.inf))))
+    tol = scale * p * (agl * (rel_p + 4 * U) + agh * ((lp + Hn[:, None]) * (rel_p + 4 * U) + elp + eh))
+    tol = tol + scale * agl * 4 * U + torch.finfo(x.dtype).eps / 2 * np.abs(ref) * (1 + 2 ** -10)
+    tol = tol + {torch.float16: 2.0 ** -25}.get(x.dtype, 0.0)  # fp16 subnormals: half a step
+    tol = tol + 2.0 ** -126                                    # ex2 flushes subnormal results
+    assert np.all(np.abs(got - ref) <= tol), np.max(np.abs(got - ref) - tol)
+    return g
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("M,V", [(1, 1), (3, 5), (2, 33), (4, 1000), (3, 8193), (2, 50021), (61, 3203)])
+def test_backward(M, V, dtype):
+    rng = np.random.default_rng(V)
+    x = logits_(M, V, V + V % 3, dtype, seed=V, masked=0.2 if V > 30 else 0.0, offset=V % 4)
+    gl, gh = rng.standard_normal(M).astype(np.float32), rng.standard_normal(M).astype(np.float32)
+    check_bwd(x, targets_(M, V, V), gl, gh, 1.0)
+    check_bwd(x, targets_(M, V, V), gl, None, 0.7)
+    check_bwd(x, targets_(M, V, V), None, gh, 1.6)
+
+
+@pytest.mark.gpu
+def test_backward_in_place_strided_and_empty_rows():
+    rng = np.random.default_rng(0)
+    M, V = 6, 9001
+    x = logits_(M, V, V + 3, "bf16", seed=4, masked=0.3)
+    x[2] = -math.inf
+    gl, gh = rng.standard_normal(M).astype(np.float32), rng.standard_normal(M).astype(np.float32)
+    t = targets_(M, V, 0)
+    # an output whose rows lie differently to 16-byte boundaries; what lies between its rows stays
+    buf = torch.full((M, V + 8), 5.0, dtype=torch.bfloat16, device="cuda")
+    a = check_bwd(x, t, gl, gh, 1.0, out=buf[:, 1:V + 1])
+    assert (buf[:, 0] == 5).all() and (buf[:, V + 1:] == 5).all()
+    assert (a[2] == 0).all()
+    inplace = x.clone(memory_format=torch.preserve_format)
+    y = torch.empty(M, V + 3, dtype=torch.bfloat16, device="cuda")[:, :V]
+    y.copy_(x)
+    r = T.token_logprobs(x, torch.from_numpy(t).cuda())
+    T.token_logprobs_backward(y, torch.from_numpy(t).cuda(), r.lse, r.entropy, torch.from_numpy(gl).cuda(),
+                              torch.from_numpy(gh).cuda(), out=y)
+    torch.cuda.synchronize()
+    assert torch.equal(y, a) and torch.equal(inplace, x)
+
+
+@pytest.mark.gpu
+def test_gradient_against_differences():
+    """Along a random direction the measured change of the forward's own
+    outputs agrees with the gradient: step h, fp32 outputs off by about 1e-5,
+    curvature h^2: 1e-5 / h + h^2 with h = 0.02 stays under 5e-3 of the scale."""
+    rng = np.random.default_rng(1)
+    M, V, h = 4, 501, 0.02
+    x = torch.from_numpy(rng.standard_normal((M, V)).astype(np.float32) * 2).cuda()
+    u = torch.from_numpy(rng.standard_normal((M, V)).astype(np.float32)).cuda()
+    t = torch.from_numpy(rng.integers(0, V, M).astype(np.int32)).cuda()
+    gl, gh = (torch.from_numpy(rng.standard_normal(M).astype(np.float32)).cuda() for _ in range(2))
+    r = T.token_logprobs(x, t)
+    g = T.token_logprobs_backward(x, t, r.lse, r.entropy, gl, gh)
+    f = lambda z: (lambda q: (gl * q.logprob + gh * q.entropy).double())(T.token_logprobs(z.contiguous(), t))
+    num = (f(x + h * u) - f(x - h * u)) / (2 * h)
+    ana = (g.double() * u.double()).sum(1)
+    assert torch.all((num - ana).abs() <= 5e-3 * (1 + ana.abs()))
+
+
+@pytest.mark.gpu
+def test_capture_streams_and_concurrent_calls():
+    """A captured call replays on new contents; two streams at once do not
+    disturb each other (no workspace is shared)."""
+    M, V = 7, 33333
+    x = logits_(M, V, V, "bf16", seed=8)
+    t = torch.from_numpy(targets_(M, V, 3)).cuda()
+    gl = torch.ones(M, device="cuda")
+    T.token_logprobs(x, t, top_k=5)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        r = T.token_logprobs(x, t, top_k=5)
+        d = T.token_logprobs_backward(x, t, r.lse, r.entropy, gl, gl)
+    x.copy_(logits_(M, V, V, "bf16", seed=9))
+    g.replay()
+    torch.cuda.synchronize()
+    e = T.token_logprobs(x, t, top_k=5)
+    d2 = T.token_logprobs_backward(x, t, e.lse, e.entropy, gl, gl)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(r, e)) and torch.equal(d, d2)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    y = logits_(M, V, V, "bf16", seed=10)
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(5):
+        outs.append((T.token_logprobs(x, t, top_k=5, stream=s1), T.token_logprobs(y, t, top_k=5, stream=s2)))
+    torch.cuda.synchronize()
+    ref = T.token_logprobs(y, t, top_k=5)
+    torch.cuda.synchronize()
+    for a, b in outs:
+        assert all(torch.equal(p, q) for p, q in zip(a, e)) and all(torch.equal(p, q) for p, q in zip(b, ref))
