@@ -372,11 +372,57 @@ fn_status fn_dequant_fp8(const void* q, const float* scales, int64_t d, int64_t 
 fn_status fn_dequant_mxfp8(const void* q, const void* scales, int64_t d, int64_t ncols, void* W,
                            fn_stream_t stream);
 
+/*
+ * Operators next to the fused projections: the projection back into the
+ * residual stream, the mixture-of-experts layer for a few tokens, and token
+ * log probabilities.  Conventions as above, with these differences: matrices
+ * may have padded rows (a row stride in elements beside each), and a
+ * workspace whose call ran out of time (FN_ERR_TIMEOUT) must be zeroed again.
+ */
 typedef enum {
   FN_T_BF16 = 0,
   FN_T_FP16 = 1,
   FN_T_FP32 = 2
 } fn_dtype;
+
+typedef enum {
+  FN_ACT_NONE = 0,
+  FN_ACT_RELU = 1,
+  FN_ACT_GELU = 2,        /* z Phi(z) */
+  FN_ACT_GELU_TANH = 3,   /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+  FN_ACT_SILU = 4         /* z / (1 + e^-z) */
+} fn_act;
+
+/*
+ * fn_proj — y = act(x @ W + bias) + residual: the projection that takes an
+ * attention or feed-forward result back into the residual stream (no norm).
+ * fp32 accumulation; one round at the store, after the residual.
+ *   x        bf16 [M, K], rows ldx >= K elements apart
+ *   W        bf16 [K, N], rows ldw >= N elements apart
+ *   bias     fp32 [N] or NULL
+ *   residual [M, N] of out_type, rows ldr >= N apart, or NULL
+ *   out_type FN_T_BF16 or FN_T_FP32
+ *   y        [M, N] of out_type, rows ldy >= N apart; may be the residual
+ *            itself (same address and row stride), may not overlap any input
+ *            otherwise (FN_ERR_ALIAS)
+ *   Any M, K, N up to 2^30.  x, W and workspace 16-byte aligned and ldx, ldw
+ *   multiples of 8 (FN_ERR_UNSUPPORTED_SHAPE): pad the rows of an odd K or N;
+ *   the padding is not read.  y, residual and bias need element alignment.
+ *   workspace, ws_bytes  >= fn_workspace_size_proj(M, K, N), zeroed before
+ *            first use; the calls leave what they need zero at zero
+ * M == 0 is a no-op.  M <= 64 runs a split-K kernel that streams the weight
+ * over all SMs, larger M a tensor-core tile kernel on pairs of SMs; one launch
+ * each, deterministic.
+ */
+fn_status fn_proj(const void* x, int64_t ldx, int64_t M, int64_t K, const void* W, int64_t ldw, int64_t N,
+                  const float* bias, fn_act act, const void* residual, int64_t ldr, fn_dtype out_type, void* y,
+                  int64_t ldy, void* workspace, size_t ws_bytes, fn_stream_t stream);
+
+/* fn_workspace_size_proj — workspace bytes of fn_proj: the 256-byte header
+ * (status word, counters) and the fp32 partial sums of the tiles whose k range
+ * several SMs share.  One workspace serves any of this library's calls, one
+ * after another.  Depends on the SM count of the current device. */
+size_t fn_workspace_size_proj(int64_t M, int64_t K, int64_t N);
 
 /*
  * fn_token_logprobs — log probabilities of given tokens, entropies and the

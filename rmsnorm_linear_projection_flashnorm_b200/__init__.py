@@ -34,6 +34,12 @@ FN_T_BF16 = 0
 FN_T_FP16 = 1
 FN_T_FP32 = 2
 
+FN_ACT_NONE = 0
+FN_ACT_RELU = 1
+FN_ACT_GELU = 2
+FN_ACT_GELU_TANH = 3
+FN_ACT_SILU = 4
+
 FN_DEBUG_WAIT_BUDGET_NS = 1
 FN_DEBUG_WITHHOLD_ARRIVE = 2
 FN_DEBUG_FORCE_PATH = 3
@@ -65,6 +71,8 @@ _SIGNATURES = {
     "fn_rmsnorm": (_int, [_vp, _i64, _i64, _vp, _f32, _vp, _vp]),
     "fn_dequant_fp8": (_int, [_vp, _vp, _i64, _i64, _vp, _vp]),
     "fn_dequant_mxfp8": (_int, [_vp, _vp, _i64, _i64, _vp, _vp]),
+    "fn_workspace_size_proj": (_sz, [_i64, _i64, _i64]),
+    "fn_proj": (_int, [_vp, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _int, _vp, _i64, _int, _vp, _i64, _vp, _sz, _vp]),
     "fn_token_logprobs": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _f32, _int, _vp, _vp, _vp, _vp, _vp, _vp]),
     "fn_token_logprobs_backward": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _f32, _vp, _i64,
                                           _vp]),
@@ -228,6 +236,16 @@ def fn_norm_proj_swiglu_nvfp4_swizzled(x, M: int, d: int, Wp, scales, wt: int, N
     return lib().fn_norm_proj_swiglu_nvfp4_swizzled(_ptr(x), M, d, _ptr(Wp), _ptr(scales), wt, N, eps,
                                                     _ptr(global_scale), _ptr(out_q), _ptr(out_sf), _ptr(workspace),
                                                     ws_bytes, _stream(stream))
+
+
+def fn_workspace_size_proj(M: int, K: int, N: int) -> int:
+    return lib().fn_workspace_size_proj(M, K, N)
+
+
+def fn_proj(x, ldx: int, M: int, K: int, W, ldw: int, N: int, bias, act: int, residual, ldr: int, out_type: int, y,
+            ldy: int, workspace, ws_bytes: int, stream=None) -> int:
+    return lib().fn_proj(_ptr(x), ldx, M, K, _ptr(W), ldw, N, _ptr(bias), act, _ptr(residual), ldr, out_type,
+                         _ptr(y), ldy, _ptr(workspace), ws_bytes, _stream(stream))
 
 
 def fn_token_logprobs(logits, type: int, M: int, V: int, ld: int, targets, scale: float, top_k: int, logprob, entropy,

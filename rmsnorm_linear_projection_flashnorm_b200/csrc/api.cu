@@ -73,6 +73,7 @@ bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
 bool eps_ok(float eps) { return std::isfinite(eps) && eps >= 0.0f; }
 
 constexpr int64_t kMaxDim = (int64_t{1} << 31) - 1;
+constexpr int64_t kMaxProjDim = int64_t{1} << 30;
 std::atomic<unsigned long long> g_launches{0};
 }  // namespace
 
@@ -95,10 +96,16 @@ EncodeTiledFn encode_fn() {
 
 bool make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int elem_bytes, uint64_t rows,
                   uint64_t cols, uint32_t box_rows, uint32_t box_cols, bool swizzle128) {
+  return make_tmap_2d_ld(map, base, dt, elem_bytes, rows, cols, cols, box_rows, box_cols, swizzle128);
+}
+
+// Rows `ld` elements apart (ld * elem_bytes a multiple of 16).
+bool make_tmap_2d_ld(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int elem_bytes, uint64_t rows,
+                     uint64_t cols, uint64_t ld, uint32_t box_rows, uint32_t box_cols, bool swizzle128) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
   const cuuint64_t dims[2] = {cols, rows};
-  const cuuint64_t strides[1] = {cols * static_cast<uint64_t>(elem_bytes)};
+  const cuuint64_t strides[1] = {ld * static_cast<uint64_t>(elem_bytes)};
   const cuuint32_t box[2] = {box_cols, box_rows};
   const cuuint32_t estr[2] = {1, 1};
   std::memset(map, 0, sizeof(*map));
@@ -509,6 +516,68 @@ size_t span_bytes(int64_t rows, int64_t cols, int64_t ld, int size) {
 int type_bytes(fn_dtype t) { return t == FN_T_FP32 ? 4 : 2; }
 bool misaligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
 }  // namespace
+
+size_t fn_workspace_size_proj(int64_t M, int64_t K, int64_t N) {
+  if (M <= 0 || K <= 0 || N <= 0 || M > kMaxProjDim || K > kMaxProjDim || N > kMaxProjDim) return kWsHeaderBytes;
+  const int sms = current_sms_or_default();
+  return M <= 64 ? proj_stream_workspace_bytes(M, sms) : proj_tile_workspace_bytes(M, K, N, sms);
+}
+
+fn_status fn_proj(const void* x, int64_t ldx, int64_t M, int64_t K, const void* W, int64_t ldw, int64_t N,
+                  const float* bias, fn_act act, const void* residual, int64_t ldr, fn_dtype out_type, void* y,
+                  int64_t ldy, void* workspace, size_t ws_bytes, fn_stream_t stream) {
+  if (M < 0 || K <= 0 || N <= 0 || ldx < K || ldw < N || ldy < N || (residual && ldr < N)) return FN_ERR_INVALID_ARG;
+  if (act < FN_ACT_NONE || act > FN_ACT_SILU) return FN_ERR_INVALID_ARG;
+  if (out_type != FN_T_BF16 && out_type != FN_T_FP32) return FN_ERR_INVALID_ARG;
+  if (M > kMaxProjDim || K > kMaxProjDim || N > kMaxProjDim) return FN_ERR_UNSUPPORTED_SHAPE;
+  if (ldx % 8 != 0 || ldw % 8 != 0 || ldx > kMaxDim || ldw > kMaxDim || proj_tile_count(M, N) > kMaxDim)
+    return FN_ERR_UNSUPPORTED_SHAPE;
+  if (M == 0) return FN_OK;
+  if (!x || !W || !y) return FN_ERR_INVALID_ARG;
+  if (!workspace) return FN_ERR_WORKSPACE;
+  const int ob = type_bytes(out_type);
+  if (!aligned16(x) || !aligned16(W) || !aligned16(workspace) || misaligned(bias, 4) || misaligned(y, ob) ||
+      misaligned(residual, ob))
+    return FN_ERR_ALIGNMENT;
+  const size_t yb = span_bytes(M, N, ldy, ob), rb = residual ? span_bytes(M, N, ldr, ob) : 0;
+  const struct { const void* p; size_t n; } ins[4] = {{x, span_bytes(M, K, ldx, 2)}, {W, span_bytes(K, N, ldw, 2)},
+                                                      {bias, static_cast<size_t>(N) * 4}, {residual, rb}};
+  if (overlaps(y, yb, workspace, ws_bytes)) return FN_ERR_ALIAS;
+  for (int i = 0; i < 4; ++i) {
+    if (overlaps(workspace, ws_bytes, ins[i].p, ins[i].n)) return FN_ERR_ALIAS;
+    // y may be the residual itself: each element is read and written by one thread
+    const bool in_place = i == 3 && residual == y && ldr == ldy;
+    if (!in_place && overlaps(y, yb, ins[i].p, ins[i].n)) return FN_ERR_ALIAS;
+  }
+  int sms = 0;
+  const fn_status st = check_device(sms);
+  if (st != FN_OK) return st;
+  const bool stream_path = M <= 64;
+  if (ws_bytes < (stream_path ? proj_stream_workspace_bytes(M, sms) : proj_tile_workspace_bytes(M, K, N, sms)))
+    return FN_ERR_WORKSPACE;
+  ProjArgs a;
+  a.x = x;
+  a.M = M;
+  a.K = K;
+  a.ldx = ldx;
+  a.W = W;
+  a.N = N;
+  a.ldw = ldw;
+  a.epi.bias = bias;
+  a.epi.act = static_cast<int>(act);
+  a.epi.residual = residual;
+  a.epi.ldr = ldr;
+  a.epi.y = y;
+  a.epi.ldy = ldy;
+  a.epi.out_fp32 = out_type == FN_T_FP32;
+  a.ws = workspace;
+  a.stream = reinterpret_cast<cudaStream_t>(stream);
+  a.num_sms = sms;
+  a.budget_ns = static_cast<uint64_t>(g_budget_ns.load());
+  a.withhold = g_withhold.load();
+  a.prefetch_iters = g_prefetch_mode.load() ? g_prefetch_iters.load() : 0;
+  return (stream_path ? launch_proj_stream(a) : launch_proj_tile(a)) == cudaSuccess ? FN_OK : FN_ERR_CUDA;
+}
 
 fn_status fn_token_logprobs(const void* logits, fn_dtype type, int64_t M, int64_t V, int64_t ld, const int32_t* targets,
                             float scale, int top_k, float* logprob, float* entropy, float* lse, int32_t* top_ids,

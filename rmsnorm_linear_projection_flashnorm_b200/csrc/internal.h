@@ -64,6 +64,8 @@ EncodeTiledFn encode_fn();
 
 // 2D row-major tensor map with 128-byte swizzle: rows x cols elements of
 // `elem_bytes`, box of box_rows x box_cols (box_cols * elem_bytes <= 128).
+bool make_tmap_2d_ld(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int elem_bytes, uint64_t rows,
+                     uint64_t cols, uint64_t ld, uint32_t box_rows, uint32_t box_cols, bool swizzle128 = true);
 bool make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int elem_bytes, uint64_t rows,
                   uint64_t cols, uint32_t box_rows, uint32_t box_cols, bool swizzle128 = true);
 
@@ -129,6 +131,46 @@ cudaError_t launch_dequant_fp8(const void* q, const float* scales, int64_t d, in
 // AdaLN shift bias B[c, n] = sum_k shift[c, k] W[k, n] in stored column order (fp32 accumulation).
 cudaError_t launch_adaln_shift_bias(const float* shift, int64_t n_cond, const void* W0, const void* W1, int64_t d,
                                     int64_t N, float* B, cudaStream_t s);
+
+// fn_proj: y = act(x W + bias) + residual (stream.cu up to 64 rows, proj_tile.cu above).
+struct Epilogue {
+  const float* bias;      // [N] or null
+  int act;                // fn_act
+  const void* residual;   // [M, N] of the output's type, row stride ldr, or null
+  int64_t ldr;
+  void* y;                // [M, N] bf16, or fp32 with out_fp32, row stride ldy
+  int64_t ldy;
+  int out_fp32;
+};
+struct ProjArgs {
+  const void* x;          // bf16 [M, K], row stride ldx
+  int64_t M, K, ldx;
+  const void* W;          // bf16 [K, N], row stride ldw
+  int64_t N, ldw;
+  Epilogue epi;
+  void* ws;
+  cudaStream_t stream;
+  int num_sms;
+  uint64_t budget_ns;
+  int withhold;
+  int prefetch_iters;
+};
+size_t proj_stream_workspace_bytes(int64_t M, int num_sms);
+size_t proj_tile_workspace_bytes(int64_t M, int64_t K, int64_t N, int num_sms);
+int64_t proj_tile_count(int64_t M, int64_t N);
+cudaError_t launch_proj_stream(const ProjArgs& a);
+cudaError_t launch_proj_tile(const ProjArgs& a);
+
+// fn_moe_swiglu: what the router writes for the expert kernels.
+constexpr int kMoeMaxRows = 64;
+constexpr int kMoeMaxExperts = 512;
+constexpr int kMoeMaxTopK = 16;
+struct MoeRoute {
+  const int* ids;         // [M][k] chosen experts
+  const float* weight;    // [E][kMoeMaxRows] routing weight, 0 where the row did not choose the expert
+  const float* rinv;      // [M] 1 / rms
+  int E, k;
+};
 
 // Token log probabilities (logprobs.cu), validated by the ABI layer.
 constexpr int kMaxTopAlternatives = 32;

@@ -1,0 +1,487 @@
+// fn_proj above 64 rows: y = act(x W + b) + residual on pairs of SMs, sm_100a.
+//
+// Each 2-CTA cluster computes 256 weight columns x NB rows with
+// tcgen05.mma.cta_group::2 (swap-AB: the weight columns on the MMA's M side,
+// 128 in each CTA, the rows of x on its N side).  N may be any multiple of 32
+// up to 256, so a batch is cut into equal row blocks padded by less than 32
+// rows each: 300 rows run as 2 x 160, not as 2 x 256.  Both operands are
+// staged by TMA with 128-byte swizzle: the CTA's 128 weight columns (16 KB per
+// 64-deep k step, N-major) and its half of the rows (NB / 2, K-major).
+// Ragged K and N read zeros past the edge (TMA fill), the epilogue stores
+// what exists.
+//
+// Bound by the tensor cores at large M, by the weight stream from HBM at a
+// few hundred rows.  Tiles run whole, one after another per pair, in as many
+// rounds as fill every pair; the k ranges of the tiles that are left over
+// (fewer than pairs) are cut into equal shares over all pairs where that
+// saves more than the exchange costs.  Sharing CTAs write fp32 partials to
+// the workspace and count themselves; the one that counts last adds them in
+// ascending k order and finishes the tile (no CTA waits for another, no
+// floating-point atomics, bit-identical repeats).
+//
+// Layout per CTA: 10 warps.
+//   warp 0      TMA producer (own weight columns, own rows)
+//   warp 1      TMEM owner; in CTA 0 the pair-MMA issuer
+//   warps 2-9   epilogue, two warps per TMEM lane quarter, alternating
+//               32-row chunks; two accumulator buffers, so a tile's epilogue
+//               overlaps the next tile's MMAs
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "decode_common.cuh"
+#include "epilogue.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace fn {
+namespace ptile {
+
+constexpr int BK = 64;
+constexpr int BN = 256;                        // weight columns per pair
+constexpr int MAX_NB = 256;                    // rows per tile
+constexpr int W_BOX_BYTES = 64 * BK * 2;       // 64 columns x 64 k rows
+constexpr int W_BYTES = 2 * W_BOX_BYTES;       // a CTA's 128 columns
+constexpr int NUM_THREADS = 320;
+constexpr int EPI_THREADS = 256;
+constexpr int MAX_STAGES = 11;
+constexpr int RING_BYTES = 7 * 32 * 1024;      // 7 stages at 256 rows
+constexpr int TMEM_COLS = 512;
+
+enum : unsigned { kSiteProdEmpty = 1, kSiteMmaAccEmpty, kSiteMmaFull, kSiteEpiAccFull };
+
+struct Params {
+  int M, N;
+  int nb, num_m, num_n, kblocks;
+  int group_m;                     // tile raster: bands of group_m row blocks
+  int full;                        // tiles that run whole
+  int rest;                        // tiles whose k blocks are shared between pairs
+  int sharers;                     // pairs that take a share of them (each at least one k block)
+  int stages;
+  Epilogue epi;
+  unsigned int* status;            // workspace header: status word and counters
+  float* part;                     // [grid][2][MAX_NB x 128]
+  unsigned long long budget_ns;
+  int withhold;
+};
+
+struct alignas(8) Bars {
+  uint64_t full[MAX_STAGES], empty[MAX_STAGES];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t drain;                  // the last pair MMA completed (both CTAs)
+  uint64_t exit_bar;               // the partner is done with this CTA's memory
+  uint32_t tmem_base;
+  int abort_flag;
+  int epi_ok[2];
+  int last;
+};
+constexpr size_t SMEM = 1024 + RING_BYTES + sizeof(Bars);
+static_assert(SMEM <= 232448, "shared memory budget");
+constexpr int SLOT_FLOATS = MAX_NB * 128;
+
+// First of the shared tiles' k blocks that pair c takes.
+__device__ __forceinline__ long long share_begin(const Params& p, int c) {
+  return c * (static_cast<long long>(p.rest) * p.kblocks) / p.sharers;
+}
+
+// Segment i of a pair: a whole tile, or its part of the shared tiles.
+struct Seg {
+  int tile, kb0, kb1;
+  bool shared;
+};
+struct SegIter {
+  int npairs, full, kblocks, next_tile;
+  long long it, end;
+  __device__ SegIter(const Params& p, int pair, int npairs_)
+      : npairs(npairs_), full(p.full), kblocks(p.kblocks), next_tile(pair), it(0), end(0) {
+    if (pair < p.sharers) {
+      it = share_begin(p, pair);
+      end = share_begin(p, pair + 1);
+    }
+  }
+  __device__ __forceinline__ bool next(Seg& s) {
+    if (next_tile < full) {
+      s.tile = next_tile;
+      s.kb0 = 0;
+      s.kb1 = kblocks;
+      s.shared = false;
+      next_tile += npairs;
+      return true;
+    }
+    if (it >= end) return false;
+    const int r = static_cast<int>(it / kblocks);
+    s.tile = full + r;
+    s.kb0 = static_cast<int>(it - static_cast<long long>(r) * kblocks);
+    s.kb1 = static_cast<int>(min(static_cast<long long>(kblocks), s.kb0 + (end - it)));
+    s.shared = s.kb0 != 0 || s.kb1 != kblocks;
+    it += s.kb1 - s.kb0;
+    return true;
+  }
+};
+
+__device__ __forceinline__ void tile_coords(int t, const Params& p, int& mb, int& nb) {
+  const int per_group = p.group_m * p.num_n;
+  const int group = t / per_group;
+  const int first_m = group * p.group_m;
+  const int gm = min(p.num_m - first_m, p.group_m);
+  const int r = t - group * per_group;
+  mb = first_m + r % gm;
+  nb = r / gm;
+}
+
+// Bounded wait that polls without suspending (the pair's critical path).
+__device__ __forceinline__ bool mbar_wait_spin(uint64_t* bar, uint32_t parity, const WaitCtl& c, unsigned site) {
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*c.abort_flag) return false;
+    if (globaltimer_ns() - t0 > c.budget_ns) {
+      raise_timeout(c, site);
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, unsigned long long budget) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait_cluster(bar, parity)) {
+    if (globaltimer_ns() - t0 > budget) return;
+  }
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
+    proj_tile_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
+                     const Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Bars& bars = *reinterpret_cast<Bars*>(smem + RING_BYTES);
+  const int x_bytes = p.nb * (BK * 2 / 2);           // this CTA's nb / 2 rows
+  const int stage_bytes = W_BYTES + x_bytes;
+  const int stages = p.stages;
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();           // 0: MMA issuer of the pair
+  const int pair = blockIdx.x >> 1;
+  const int npairs = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(&bars.full[s], 1);
+      mbar_init(&bars.empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&bars.acc_full[b], 1);
+      mbar_init(&bars.acc_empty[b], EPI_THREADS + 1);   // CTA 0's epilogue threads + CTA 1's epilogue
+    }
+    mbar_init(&bars.drain, 1);
+    mbar_init(&bars.exit_bar, 1);
+    bars.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmap_x);
+    tma_prefetch_desc(&tmap_w);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(&bars.tmem_base, TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync_all();                                 // both CTAs' barriers are initialised
+  tc_fence_after();
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const uint32_t tmem_base = bars.tmem_base;
+  WaitCtl ctl{&bars.abort_flag, p.status, p.budget_ns};
+  ctl.peer_abort = dsmem_addr(&bars.abort_flag, rank ^ 1u);
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer (own halves)
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0, issued = 0, last_ph = 0;
+      bool ok = true;
+      const uint32_t full0 = dsmem_addr(&bars.full[0], 0);   // CTA 0's barriers count both CTAs' bytes
+      SegIter segs(p, pair, npairs);
+      Seg g;
+      while (ok && segs.next(g)) {
+        int mb, nb;
+        tile_coords(g.tile, p, mb, nb);
+        const int row0 = mb * p.nb + static_cast<int>(rank) * (p.nb / 2);
+        const int col0 = nb * BN + static_cast<int>(rank) * 128;
+        for (int kb = g.kb0; kb < g.kb1; ++kb) {
+          if (!mbar_wait_spin(&bars.empty[s], ph ^ 1, ctl, kSiteProdEmpty)) { ok = false; break; }
+          if (rank == 0) mbar_arrive_expect_tx(&bars.full[s], 2 * stage_bytes);
+          const uint32_t fb = full0 + s * 8;
+          uint8_t* st = smem + s * stage_bytes;
+          tma_load_2d_pair(st, &tmap_w, fb, col0, kb * BK);
+          tma_load_2d_pair(st + W_BOX_BYTES, &tmap_w, fb, col0 + 64, kb * BK);
+          tma_load_2d_pair(st + W_BYTES, &tmap_x, fb, kb * BK, row0);
+          issued |= 1u << s;
+          last_ph = (last_ph & ~(1u << s)) | (ph << s);
+          if (++s == stages) { s = 0; ph ^= 1; }
+        }
+      }
+      // No copy may still be landing in shared memory when a CTA exits.  CTA
+      // 0's stage barriers count both CTAs' copies, and CTA 1 leaves after
+      // CTA 0 (exit_bar below).  After an abort the partner may not have
+      // announced a stage's bytes, so the barriers cannot tell: leave the
+      // copies a millisecond.
+      if (ok) {
+        if (rank == 0)
+          for (int i = 0; i < stages; ++i)
+            if (issued & (1u << i)) drain_wait(&bars.full[i], (last_ph >> i) & 1u, p.budget_ns);
+      } else {
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 1000000ull) {
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      if (rank == 0) {
+        // -------------------------------------------------------- pair-MMA issuer
+        const uint32_t idesc = idesc_bf16_f32(2 * 128, p.nb, /*a MN-major*/ true, /*b MN-major*/ false);
+        int s = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        int i = 0;
+        SegIter segs(p, pair, npairs);
+        Seg g;
+        for (; ok && segs.next(g); ++i) {
+          const int b = i & 1;
+          const uint32_t aph = (i >> 1) & 1;
+          if (!mbar_wait_spin(&bars.acc_empty[b], aph ^ 1, ctl, kSiteMmaAccEmpty)) break;
+          tc_fence_after();
+          const uint32_t d_tmem = tmem_base + b * MAX_NB;
+          for (int kb = g.kb0; kb < g.kb1; ++kb) {
+            if (!mbar_wait_spin(&bars.full[s], ph, ctl, kSiteMmaFull)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t w0 = smem_u32(smem + s * stage_bytes);
+#pragma unroll
+            for (int kk = 0; kk < BK / 16; ++kk) {
+              // A: 128 weight columns of each CTA, N-major; B: nb / 2 rows of x of each CTA, K-major
+              const uint64_t adesc = sdesc_sw128(w0 + kk * 2048, W_BOX_BYTES, 1024);
+              const uint64_t bdesc = sdesc_sw128(w0 + W_BYTES + kk * 32, 16, 1024);
+              umma_bf16_pair(d_tmem, adesc, bdesc, idesc, (kb != g.kb0 || kk != 0) ? 1u : 0u);
+            }
+            umma_commit_pair(&bars.empty[s], 0x3);
+            if (++s == stages) { s = 0; ph ^= 1; }
+          }
+          if (!ok) break;
+          if (!(p.withhold && i == 0)) umma_commit_pair(&bars.acc_full[b], 0x3);
+        }
+        umma_commit_pair(&bars.drain, 0x3);
+        drain_wait(&bars.drain, 0, p.budget_ns);
+      } else {
+        drain_wait(&bars.drain, 0, p.budget_ns);   // the pair's last MMA no longer reads this CTA
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue (own columns)
+    const int q = warp & 3;                        // TMEM lane quarter this warp may access
+    const int half = (warp - 2) >> 2;              // which of the quarter's two warps
+    const int et = threadIdx.x - 64;               // 0..255
+    const uint32_t acc_empty0 = dsmem_addr(&bars.acc_empty[0], 0);
+    const int chunks = p.nb / 32;
+    int i = 0;
+    SegIter segs(p, pair, npairs);
+    Seg g;
+    for (; segs.next(g); ++i) {
+      int mb, nb;
+      tile_coords(g.tile, p, mb, nb);
+      const int b = i & 1;
+      const uint32_t aph = (i >> 1) & 1;
+      // One thread waits and the whole epilogue follows its decision, so the
+      // group never splits at the named barriers or the .sync.aligned loads.
+      if (et == 0) bars.epi_ok[b] = mbar_wait_spin(&bars.acc_full[b], aph, ctl, kSiteEpiAccFull) ? 1 : 0;
+      named_bar_sync(1, EPI_THREADS);
+      if (!bars.epi_ok[b]) break;
+      tc_fence_after();
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + b * MAX_NB;
+      const int n = q * 32 + lane;                 // column within this CTA's 128
+      const int64_t col = static_cast<int64_t>(nb) * BN + rank * 128 + n;
+      const bool col_ok = col < p.N;
+      const float bias = p.epi.bias && col_ok ? __ldg(p.epi.bias + col) : 0.f;
+      const int row0 = mb * p.nb;
+      auto release = [&]() {
+        // this CTA's epilogue has read TMEM buffer b
+        tc_fence_before();
+        if (rank == 0) {
+          mbar_arrive(&bars.acc_empty[b]);
+        } else {
+          named_bar_sync(1, EPI_THREADS);
+          if (et == 0) mbar_arrive_remote(acc_empty0 + b * 8);
+        }
+      };
+      auto finish = [&](int c, const float(&v)[32]) {
+        // rows row0 + 32 c + j of column col
+        if (!col_ok) return;
+        const int r0 = row0 + 32 * c;
+        const int nr = min(p.M - r0, 32);
+        float res[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) res[j] = j < nr ? epi_residual(p.epi, r0 + j, col) : 0.f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (j < nr) epi_store(p.epi, r0 + j, col, epi_act(p.epi.act, v[j] + bias) + res[j]);
+      };
+      if (!g.shared) {
+#pragma unroll 1
+        for (int c = half; c < chunks; c += 2) {
+          float v[32];
+          dec::tmem_ld_cols<32>(taddr + c * 32, v);
+          finish(c, v);
+        }
+        release();
+        continue;
+      }
+      // Shared tile: publish the partial (float4 groups [row / 4][column]) and
+      // count; the CTA that counts last adds all of them and finishes.
+      const long long total = static_cast<long long>(p.rest) * p.kblocks;
+      const int r = g.tile - p.full;
+      const long long t0 = static_cast<long long>(r) * p.kblocks;
+      const int slot = static_cast<int>(blockIdx.x) * 2 + (share_begin(p, pair) >= t0 ? 0 : 1);
+      float4* mine = reinterpret_cast<float4*>(p.part + static_cast<int64_t>(slot) * SLOT_FLOATS);
+#pragma unroll 1
+      for (int c = half; c < chunks; c += 2) {
+        float v[32];
+        dec::tmem_ld_cols<32>(taddr + c * 32, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          __stcg(mine + (c * 8 + j) * 128 + n, make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
+      }
+      release();
+      const int c_first = static_cast<int>(((t0 + 1) * p.sharers - 1) / total);
+      const int c_last = static_cast<int>(((t0 + p.kblocks) * p.sharers - 1) / total);
+      __threadfence();
+      named_bar_sync(1, EPI_THREADS);
+      if (et == 0) {
+        bars.last = count_partial(p.status, c_first * 2 + static_cast<int>(rank), c_last - c_first + 1);
+        __threadfence();
+      }
+      named_bar_sync(1, EPI_THREADS);
+      if (!bars.last) continue;
+#pragma unroll 1
+      for (int c = half; c < chunks; c += 2) {
+        float v[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = 0.f;
+#pragma unroll 2
+        for (int o = c_first; o <= c_last; ++o) {
+          // a pair's first shared segment is slot 0; this tile is not its first when its share begins before it
+          const int sl = (o * 2 + static_cast<int>(rank)) * 2 + (share_begin(p, o) >= t0 ? 0 : 1);
+          const float4* src = reinterpret_cast<const float4*>(p.part + static_cast<int64_t>(sl) * SLOT_FLOATS);
+          float4 t[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) t[j] = __ldcg(src + (c * 8 + j) * 128 + n);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            v[4 * j] += t[j].x;
+            v[4 * j + 1] += t[j].y;
+            v[4 * j + 2] += t[j].z;
+            v[4 * j + 3] += t[j].w;
+          }
+        }
+        finish(c, v);
+      }
+    }
+  }
+
+  // Teardown: every role of this CTA is done; wait (bounded) until the partner
+  // is done with this CTA's memory too, then release TMEM in both CTAs.
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    mbar_arrive_remote(dsmem_addr(&bars.exit_bar, rank ^ 1u));
+    drain_wait(&bars.exit_bar, 0, p.budget_ns);
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, TMEM_COLS);
+  }
+}
+
+// How a call is cut into tiles and shares.
+struct Plan {
+  int nb, num_m, num_n, kblocks, pairs, full, rest, sharers;
+};
+
+Plan make_plan(int64_t M, int64_t K, int64_t N, int num_sms) {
+  Plan q;
+  const int64_t blocks = (M + MAX_NB - 1) / MAX_NB;
+  q.num_m = static_cast<int>(blocks);
+  q.nb = static_cast<int>(((M + blocks - 1) / blocks + 31) / 32 * 32);
+  q.num_n = static_cast<int>((N + BN - 1) / BN);
+  q.kblocks = static_cast<int>((K + BK - 1) / BK);
+  const int64_t tiles = static_cast<int64_t>(q.num_m) * q.num_n;
+  const int pairs = (num_sms < kMaxCounters ? num_sms : kMaxCounters) / 2;
+  const int64_t rest = tiles % pairs;
+  // At most 8 pairs to a tile (the last one reads all partials), at least 4 k
+  // blocks to a share.
+  const int64_t total = rest * q.kblocks;
+  int64_t sharers = pairs < rest * 8 ? pairs : rest * 8;
+  if (sharers > total / 4) sharers = total / 4;
+  // Sharing saves (1 - rest / sharers) of a tile's time, about 0.37 us per k
+  // block at 256 rows, and costs about 5 us.
+  const bool share = sharers > rest && q.kblocks * (sharers - rest) * q.nb > 14 * sharers * MAX_NB;
+  q.full = static_cast<int>(share ? tiles - rest : tiles);
+  q.rest = static_cast<int>(share ? rest : 0);
+  q.sharers = static_cast<int>(share ? sharers : 0);
+  q.pairs = tiles >= pairs ? pairs : share ? q.sharers : static_cast<int>(tiles);
+  return q;
+}
+
+}  // namespace ptile
+
+size_t proj_tile_workspace_bytes(int64_t M, int64_t K, int64_t N, int num_sms) {
+  const ptile::Plan q = ptile::make_plan(M, K, N, num_sms);
+  if (q.rest == 0) return kWsHeaderBytes;
+  return kWsHeaderBytes + static_cast<size_t>(q.pairs) * 2 * 2 * ptile::SLOT_FLOATS * 4;
+}
+
+int64_t proj_tile_count(int64_t M, int64_t N) {
+  return ((M + ptile::MAX_NB - 1) / ptile::MAX_NB) * ((N + ptile::BN - 1) / ptile::BN);
+}
+
+cudaError_t launch_proj_tile(const ProjArgs& a) {
+  using namespace ptile;
+  const Plan q = make_plan(a.M, a.K, a.N, a.num_sms);
+  CUtensorMap tx, tw;
+  if (!make_tmap_2d_ld(&tx, a.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.M, a.K, a.ldx, q.nb / 2, BK))
+    return cudaErrorInvalidValue;
+  if (!make_tmap_2d_ld(&tw, a.W, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.K, a.N, a.ldw, BK, 64))
+    return cudaErrorInvalidValue;
+  Params p = {};
+  p.M = static_cast<int>(a.M);
+  p.N = static_cast<int>(a.N);
+  p.nb = q.nb;
+  p.num_m = q.num_m;
+  p.num_n = q.num_n;
+  p.kblocks = q.kblocks;
+  // Raster band: as many row blocks as keep the band's x within about 40 MB
+  // of L2 (at most 16), so the weight is fetched once per band.
+  const int64_t band_rows = (40ll << 20) / (a.K * 2);
+  p.group_m = static_cast<int>(band_rows / q.nb);
+  if (p.group_m < 1) p.group_m = 1;
+  if (p.group_m > 16) p.group_m = 16;
+  p.full = q.full;
+  p.rest = q.rest;
+  p.sharers = q.sharers;
+  const int stage_bytes = W_BYTES + q.nb * BK;
+  p.stages = RING_BYTES / stage_bytes;
+  if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;
+  p.epi = a.epi;
+  uint8_t* ws = static_cast<uint8_t*>(a.ws);
+  p.status = reinterpret_cast<unsigned int*>(ws);
+  p.part = reinterpret_cast<float*>(ws + kWsHeaderBytes);
+  p.budget_ns = a.budget_ns;
+  p.withhold = a.withhold;
+  const cudaError_t e = ensure_smem_limit<proj_tile_kernel>(static_cast<int>(SMEM));
+  if (e != cudaSuccess) return e;
+  return launch_pdl(proj_tile_kernel, static_cast<unsigned>(2 * q.pairs), NUM_THREADS, SMEM, a.stream, tx, tw, p);
+}
+
+}  // namespace fn

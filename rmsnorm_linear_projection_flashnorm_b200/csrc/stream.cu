@@ -1,0 +1,464 @@
+// Projections of at most 64 rows whose cost is the weight stream, sm_100a:
+//   kProj  y = act(x W + b) + residual (fn_proj)
+//   kUp    the chosen experts' SwiGLU, act = w silu(r x G') (r x U') (fn_moe_swiglu)
+//   kDown  y = residual + sum over the chosen experts of act D  (fn_moe_swiglu)
+//
+// Swap-AB as in the norm-fused decode kernel: D[n, m] += W^T[n, k] x^T[k, m],
+// 128 weight columns on the MMA's M side, the rows padded to 16, 32 or 64 on
+// its N side (tcgen05.mma kind::f16, fp32 accumulators in TMEM), both operands
+// staged by TMA with 128-byte swizzle.  Bound by HBM: every weight byte is
+// read once, the MMAs hide under the stream.
+//
+// All three run on one (column tile, 64-deep k block) iteration space that is
+// cut into equal contiguous shares, one per SM.  For the experts the space is
+// only known on the device (how many experts were chosen), so each CTA derives
+// it from the router's list:
+//   kUp    tile -> (expert slot, 128 intermediate columns); k runs over d
+//   kDown  k block -> (expert slot, 64 intermediate values): the sum over
+//          experts is one long contraction accumulated in TMEM
+// Every row goes through every chosen expert's MMA: the weights are the cost,
+// the flops are not (64 rows x all weights is under a tenth of the tensor
+// rate at the HBM rate).  kUp stores zeros for the rows that did not choose an
+// expert, scaled by the routing weight for those that did, so kDown needs no
+// masks.
+//
+// A tile whose k range falls to one CTA is finished by it.  The CTAs that
+// share a tile write fp32 partials to the workspace and count themselves; the
+// one that counts last adds all partials in ascending k order (a fixed order,
+// so repeats are bit-identical) and finishes.  No CTA waits for another.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "decode_common.cuh"
+#include "epilogue.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace fn {
+namespace strm {
+
+constexpr int BK = 64;
+constexpr int NUM_THREADS = 192;           // producer, MMA issuer, 4 epilogue warps
+constexpr int W_BOX_BYTES = 64 * BK * 2;   // 64 columns x 64 k rows
+constexpr int SMEM_BUDGET = 200 * 1024;
+constexpr int MAX_SHARE = 16;              // CTAs to a tile: the last one reads all their partials
+
+enum Mode : int { kProj = 0, kUp = 1, kDown = 2 };
+enum : unsigned { kSiteProdEmpty = 1, kSiteMmaAccEmpty, kSiteMmaFull, kSiteEpiAccFull };
+
+struct Params {
+  int M, ncols;                  // rows; output columns (kProj: N, kUp: I, kDown: d)
+  int tiles, kblocks;            // kProj: the whole space; kUp: tiles per expert, k blocks of d;
+                                 // kDown: tiles of d, k blocks per expert
+  int wrows;                     // weight rows per expert (kUp: d, kDown: I)
+  unsigned int* status;          // workspace header: status word and counters
+  float* part;                   // [grid][2][slot floats]
+  unsigned long long budget_ns;
+  int withhold;
+  const uint8_t* w;              // weight base and row bytes (L2 prefetch addresses, kProj)
+  int64_t w_row_bytes;
+  int prefetch_iters;
+  Epilogue epi;                  // kProj, kDown
+  MoeRoute route;                // kUp, kDown
+  __nv_bfloat16* act;            // kUp writes [slot][MPAD][I]
+};
+
+template <int MPAD, int HALVES>
+struct Cfg {
+  static constexpr int W_BYTES = HALVES * 2 * W_BOX_BYTES;
+  static constexpr int X_BYTES = MPAD * BK * 2;
+  static constexpr int STAGE_BYTES = W_BYTES + X_BYTES;
+  static constexpr int STAGES_RAW = SMEM_BUDGET / STAGE_BYTES;
+  static constexpr int STAGES = STAGES_RAW > 10 ? 10 : STAGES_RAW;
+  static constexpr int ACC_COLS = HALVES * MPAD;
+  static constexpr int TMEM_COLS = 2 * ACC_COLS;                    // two buffers: 32..256
+  static constexpr int SLOT_FLOATS = HALVES * MPAD * 128;
+};
+
+template <int STAGES>
+struct alignas(16) Bars {
+  uint64_t full[STAGES], empty[STAGES];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort_flag;
+  int epi_ok[2];
+  int last;                        // the count of the tile's contributors is complete
+  int n_active;
+  uint32_t active[kMoeMaxExperts / 32];
+  int experts[kMoeMaxExperts];     // chosen experts in ascending order
+};
+
+template <int MPAD, int HALVES>
+constexpr size_t smem_bytes() {
+  using C = Cfg<MPAD, HALVES>;
+  return 1024 + C::STAGES * C::STAGE_BYTES + sizeof(Bars<C::STAGES>);
+}
+static_assert(smem_bytes<16, 1>() <= 232448 && smem_bytes<64, 2>() <= 232448, "shared memory budget");
+
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, unsigned long long budget) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (globaltimer_ns() - t0 > budget) return;
+  }
+}
+
+template <int MPAD, int HALVES, int MODE>
+__global__ void __launch_bounds__(NUM_THREADS, 1)
+    stream_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
+                  const Params p) {
+  using C = Cfg<MPAD, HALVES>;
+  constexpr int STAGES = C::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Bars<STAGES>& bars = *reinterpret_cast<Bars<STAGES>*>(smem + STAGES * C::STAGE_BYTES);
+  auto stage_w = [&](int s) { return smem + s * C::STAGE_BYTES; };
+  auto stage_x = [&](int s) { return smem + s * C::STAGE_BYTES + C::W_BYTES; };
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int cta = blockIdx.x;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&bars.full[s], 1);
+      mbar_init(&bars.empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&bars.acc_full[b], 1);
+      mbar_init(&bars.acc_empty[b], 128);
+    }
+    mbar_init(&bars.drain, 1);
+    bars.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmap_x);
+    tma_prefetch_desc(&tmap_w);
+  }
+  if (warp == 1) {
+    tmem_alloc(&bars.tmem_base, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  if (MODE != kProj)
+    for (int i = threadIdx.x; i < kMoeMaxExperts / 32; i += NUM_THREADS) bars.active[i] = 0;
+
+  // The iteration space: tiles x kblocks, cut into one contiguous share per CTA.
+  int tiles = p.tiles, kblocks = p.kblocks;
+  long long total = static_cast<long long>(tiles) * kblocks;
+  auto shares = [&]() {
+    const long long most = min(total, static_cast<long long>(tiles) * MAX_SHARE);
+    return static_cast<int>(min(most, static_cast<long long>(gridDim.x)));
+  };
+  int grid = shares();
+  if (MODE == kProj) {
+    // This overlaps the previous kernel in the stream: an L2 prefetch cannot
+    // return stale data, whoever wrote the weight.  One 128-byte line per
+    // thread and step.
+    // (the first k blocks of the share)
+    const long long b0 = cta < grid ? cta * total / grid : 0;
+    const long long b1 = cta < grid ? (cta + 1LL) * total / grid : 0;
+    const int n_it = static_cast<int>(min(static_cast<long long>(p.prefetch_iters), b1 - b0));
+    for (int i = threadIdx.x; i < n_it * BK * 2; i += NUM_THREADS) {
+      const long long it = b0 + i / (BK * 2);
+      const int tile = static_cast<int>(it / kblocks);
+      const int64_t k = (it - static_cast<long long>(tile) * kblocks) * BK + (i >> 1) % BK;
+      const int64_t col = static_cast<int64_t>(tile) * 128 + (i & 1) * 64;
+      if (k < p.wrows && col < p.ncols)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(p.w + k * p.w_row_bytes + col * 2));
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (MODE != kProj) {
+    // the chosen experts in ascending order, from the router's ids
+    for (int i = threadIdx.x; i < p.M * p.route.k; i += NUM_THREADS) {
+      const int e = __ldcg(p.route.ids + i);
+      atomicOr(&bars.active[e >> 5], 1u << (e & 31));
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < p.route.E; e += NUM_THREADS) {
+      int slot = 0;
+      for (int w = 0; w < (e >> 5); ++w) slot += __popc(bars.active[w]);
+      slot += __popc(bars.active[e >> 5] & ((1u << (e & 31)) - 1u));
+      const bool on = (bars.active[e >> 5] >> (e & 31)) & 1u;
+      if (on) bars.experts[slot] = e;
+      if (e == p.route.E - 1) bars.n_active = slot + (on ? 1 : 0);
+    }
+    __syncthreads();
+    const int n = bars.n_active;
+    if (MODE == kUp) tiles *= n;
+    else kblocks *= n;
+    total = static_cast<long long>(tiles) * kblocks;
+    grid = shares();
+  }
+  const long long it0 = cta < grid ? cta * total / grid : 0;
+  const long long it1 = cta < grid ? (cta + 1LL) * total / grid : 0;
+  // the CTA whose share holds iteration `it`
+  auto owner_of = [&](long long it) { return static_cast<int>(((it + 1) * grid - 1) / total); };
+
+  const uint32_t tmem_base = bars.tmem_base;
+  const WaitCtl ctl{&bars.abort_flag, p.status, p.budget_ns};
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      const uint64_t w_policy = l2_policy_evict_first();   // the weight is streamed once
+      int s = 0;
+      uint32_t ph = 0, issued = 0, last_ph = 0;
+      bool ok = true;
+      for (long long it = it0; it < it1 && ok;) {
+        const int tile = static_cast<int>(it / kblocks);
+        const int kb0 = static_cast<int>(it - static_cast<long long>(tile) * kblocks);
+        const int kb1 = static_cast<int>(min(static_cast<long long>(kblocks), kb0 + (it1 - it)));
+        int wcol = tile * 128, wrow = 0;                    // kProj, kDown: this tile's columns
+        if (MODE == kUp) {
+          wcol = tile % p.tiles * 256;                      // gate | up, 128 columns each
+          wrow = bars.experts[tile / p.tiles] * p.wrows;
+        }
+        int slot = MODE == kDown ? kb0 / p.kblocks : 0;
+        int kk = MODE == kDown ? kb0 - slot * p.kblocks : kb0;
+        if (MODE == kDown) wrow = bars.experts[slot] * p.wrows;
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!mbar_wait(&bars.empty[s], ph ^ 1, ctl, kSiteProdEmpty)) { ok = false; break; }
+          mbar_arrive_expect_tx(&bars.full[s], C::X_BYTES + C::W_BYTES);
+          tma_load_2d(stage_x(s), &tmap_x, &bars.full[s], kk * BK, slot * MPAD);
+#pragma unroll
+          for (int bx = 0; bx < 2 * HALVES; ++bx)
+            tma_load_2d_hint(stage_w(s) + bx * W_BOX_BYTES, &tmap_w, &bars.full[s], wcol + bx * 64, wrow + kk * BK,
+                             w_policy);
+          issued |= 1u << s;
+          last_ph = (last_ph & ~(1u << s)) | (ph << s);
+          if (++s == STAGES) { s = 0; ph ^= 1; }
+          ++kk;
+          if (MODE == kDown && kk == p.kblocks && kb + 1 < kb1) {
+            kk = 0;
+            wrow = bars.experts[++slot] * p.wrows;
+          }
+        }
+        it += kb1 - kb0;
+      }
+      for (int i = 0; i < STAGES; ++i)
+        if (issued & (1u << i)) drain_wait(&bars.full[i], (last_ph >> i) & 1u, p.budget_ns);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t IDESC = idesc_bf16_f32(128, MPAD, /*a MN-major*/ true, /*b MN-major*/ false);
+      int s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      int seg = 0;
+      for (long long it = it0; it < it1 && ok; ++seg) {
+        const int tile = static_cast<int>(it / kblocks);
+        const int kb0 = static_cast<int>(it - static_cast<long long>(tile) * kblocks);
+        const int kb1 = static_cast<int>(min(static_cast<long long>(kblocks), kb0 + (it1 - it)));
+        const int b = seg & 1;
+        const uint32_t aph = (seg >> 1) & 1;
+        if (!mbar_wait(&bars.acc_empty[b], aph ^ 1, ctl, kSiteMmaAccEmpty)) break;
+        tc_fence_after();
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!mbar_wait(&bars.full[s], ph, ctl, kSiteMmaFull)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t w0 = smem_u32(stage_w(s));
+          const uint32_t x0 = smem_u32(stage_x(s));
+#pragma unroll
+          for (int h = 0; h < HALVES; ++h) {
+            const uint32_t d_tmem = tmem_base + (b * HALVES + h) * MPAD;
+#pragma unroll
+            for (int kk = 0; kk < BK / 16; ++kk) {
+              // A = W^T: 128 weight columns, N-major, two 64-column boxes; B = x^T: K-major rows
+              const uint64_t adesc = sdesc_sw128(w0 + h * 2 * W_BOX_BYTES + kk * 2048, W_BOX_BYTES, 1024);
+              const uint64_t bdesc = sdesc_sw128(x0 + kk * 32, 16, 1024);
+              umma_bf16(d_tmem, adesc, bdesc, IDESC, (kb != kb0 || kk != 0) ? 1u : 0u);
+            }
+          }
+          umma_commit(&bars.empty[s]);
+          if (++s == STAGES) { s = 0; ph ^= 1; }
+        }
+        if (!ok) break;
+        if (!(p.withhold && seg == 0)) umma_commit(&bars.acc_full[b]);
+        it += kb1 - kb0;
+      }
+      umma_commit(&bars.drain);
+      drain_wait(&bars.drain, 0, p.budget_ns);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3;                       // TMEM lane quarter this warp may access
+    const int n = q * 32 + lane;                  // column within the tile
+    const int et = threadIdx.x - 64;              // 0..127
+    const int Q = (p.M + 3) >> 2;
+    int seg = 0;
+    for (long long it = it0; it < it1; ++seg) {
+      const int tile = static_cast<int>(it / kblocks);
+      const int kb0 = static_cast<int>(it - static_cast<long long>(tile) * kblocks);
+      const int kb1 = static_cast<int>(min(static_cast<long long>(kblocks), kb0 + (it1 - it)));
+      it += kb1 - kb0;
+      const int b = seg & 1;
+      const uint32_t aph = (seg >> 1) & 1;
+      // One thread waits and the whole group follows its decision, so the
+      // group never splits at the named barriers or the .sync.aligned loads.
+      if (et == 0) bars.epi_ok[b] = mbar_wait(&bars.acc_full[b], aph, ctl, kSiteEpiAccFull) ? 1 : 0;
+      named_bar_sync(1, 128);
+      if (!bars.epi_ok[b]) break;
+      tc_fence_after();
+      float acc[HALVES][MPAD];
+#pragma unroll
+      for (int h = 0; h < HALVES; ++h)
+        dec::tmem_ld_cols<MPAD>(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + (b * HALVES + h) * MPAD, acc[h]);
+      tc_fence_before();
+      mbar_arrive(&bars.acc_empty[b]);
+      if (kb0 != 0 || kb1 != kblocks) {
+        // Shared tile: publish the partial (float4 groups [half][row / 4][column],
+        // rows below M only), count, and go on unless this was the last one.
+        const int slot = cta * 2 + (seg == 0 ? 0 : 1);
+        float4* mine = reinterpret_cast<float4*>(p.part + static_cast<int64_t>(slot) * C::SLOT_FLOATS);
+#pragma unroll
+        for (int h = 0; h < HALVES; ++h)
+#pragma unroll
+          for (int g = 0; g < MPAD / 4; ++g)
+            if (g < Q)
+              __stcg(mine + (h * (MPAD / 4) + g) * 128 + n,
+                     make_float4(acc[h][4 * g], acc[h][4 * g + 1], acc[h][4 * g + 2], acc[h][4 * g + 3]));
+        const long long t0 = static_cast<long long>(tile) * kblocks;
+        const int c_first = owner_of(t0), c_last = owner_of(t0 + kblocks - 1);
+        __threadfence();
+        named_bar_sync(1, 128);
+        if (et == 0) {
+          bars.last = count_partial(p.status, c_first, c_last - c_first + 1);
+          __threadfence();
+        }
+        named_bar_sync(1, 128);
+        if (!bars.last) continue;
+        // every partial of the tile is visible: add them in ascending k order
+#pragma unroll
+        for (int h = 0; h < HALVES; ++h)
+#pragma unroll
+          for (int m = 0; m < MPAD; ++m) acc[h][m] = 0.f;
+        constexpr int GROUPS = HALVES * MPAD / 4;
+        constexpr int CB = GROUPS >= 16 ? 1 : 16 / GROUPS;       // contributors in flight
+        for (int c0 = c_first; c0 <= c_last; c0 += CB) {
+          float4 v[CB][GROUPS];
+#pragma unroll
+          for (int j = 0; j < CB; ++j) {
+            const int c = c0 + j;
+            if (c <= c_last) {
+              // a CTA's first segment is slot 0; this tile is not its first when its share begins before it
+              const int sl = c * 2 + (c * total / grid >= t0 ? 0 : 1);
+              const float4* src = reinterpret_cast<const float4*>(p.part + static_cast<int64_t>(sl) * C::SLOT_FLOATS);
+#pragma unroll
+              for (int g = 0; g < GROUPS; ++g)
+                if (g % (MPAD / 4) < Q) v[j][g] = __ldcg(src + g * 128 + n);
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < CB; ++j) {
+            if (c0 + j <= c_last) {
+#pragma unroll
+              for (int g = 0; g < GROUPS; ++g) {
+                if (g % (MPAD / 4) < Q) {
+                  float* a = &acc[g / (MPAD / 4)][g % (MPAD / 4) * 4];
+                  a[0] += v[j][g].x;
+                  a[1] += v[j][g].y;
+                  a[2] += v[j][g].z;
+                  a[3] += v[j][g].w;
+                }
+              }
+            }
+          }
+        }
+      }
+      if constexpr (MODE == kUp) {
+        // act = w silu(r gate) (r up), one round to bf16; 0 for rows that did not choose the expert
+        const int slot = tile / p.tiles;
+        const float* wt = p.route.weight + bars.experts[slot] * kMoeMaxRows;
+        __nv_bfloat16* dst = p.act + (static_cast<int64_t>(slot) * MPAD) * p.ncols + tile % p.tiles * 128 + n;
+#pragma unroll
+        for (int m = 0; m < MPAD; ++m) {
+          const float w = m < p.M ? __ldcg(wt + m) : 0.f;
+          float v = 0.f;
+          if (w != 0.f) {
+            const float r = __ldcg(p.route.rinv + m);
+            v = w * (silu_f32(acc[0][m] * r) * (acc[HALVES - 1][m] * r));
+          }
+          dst[static_cast<int64_t>(m) * p.ncols] = __float2bfloat16_rn(v);
+        }
+      } else {
+        const int64_t col = static_cast<int64_t>(tile) * 128 + n;
+        if (col < p.ncols) {
+          const float bias = p.epi.bias ? __ldg(p.epi.bias + col) : 0.f;
+          float res[MPAD];
+#pragma unroll
+          for (int m = 0; m < MPAD; ++m) res[m] = m < p.M ? epi_residual(p.epi, m, col) : 0.f;
+#pragma unroll
+          for (int m = 0; m < MPAD; ++m)
+            if (m < p.M) epi_store(p.epi, m, col, epi_act(p.epi.act, acc[0][m] + bias) + res[m]);
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, C::TMEM_COLS);
+  }
+}
+
+template <int MPAD, int HALVES, int MODE>
+cudaError_t launch(Params& p, const CUtensorMap& tx, const CUtensorMap& tw, int num_sms, cudaStream_t stream) {
+  constexpr size_t SMEM = smem_bytes<MPAD, HALVES>();
+  const cudaError_t e = ensure_smem_limit<stream_kernel<MPAD, HALVES, MODE>>(static_cast<int>(SMEM));
+  if (e != cudaSuccess) return e;
+  // the experts' space is at least tiles x kblocks (one expert): known to the kernel only
+  const long long total = static_cast<long long>(p.tiles) * p.kblocks;
+  if (num_sms > kMaxCounters) num_sms = kMaxCounters;
+  const long long most = total < static_cast<long long>(p.tiles) * MAX_SHARE ? total : static_cast<long long>(p.tiles) * MAX_SHARE;
+  const unsigned grid = static_cast<unsigned>(MODE == kProj && most < num_sms ? most : num_sms);
+  return launch_pdl(stream_kernel<MPAD, HALVES, MODE>, grid, NUM_THREADS, SMEM, stream, tx, tw, p);
+}
+
+// Partials: two slots per CTA.
+inline size_t part_bytes(int mpad, int halves, int num_sms) {
+  return static_cast<size_t>(num_sms) * 2 * halves * mpad * 128 * 4;
+}
+
+}  // namespace strm
+
+size_t proj_stream_workspace_bytes(int64_t M, int num_sms) {
+  return kWsHeaderBytes + strm::part_bytes(decode_mpad(M), 1, num_sms);
+}
+
+cudaError_t launch_proj_stream(const ProjArgs& a) {
+  using namespace strm;
+  const int mp = decode_mpad(a.M);
+  CUtensorMap tx, tw;
+  if (!make_tmap_2d_ld(&tx, a.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.M, a.K, a.ldx, mp, BK)) return cudaErrorInvalidValue;
+  if (!make_tmap_2d_ld(&tw, a.W, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.K, a.N, a.ldw, BK, 64)) return cudaErrorInvalidValue;
+  Params p = {};
+  p.M = static_cast<int>(a.M);
+  p.ncols = static_cast<int>(a.N);
+  p.tiles = static_cast<int>((a.N + 127) / 128);
+  p.kblocks = static_cast<int>((a.K + BK - 1) / BK);
+  p.wrows = static_cast<int>(a.K);
+  uint8_t* ws = static_cast<uint8_t*>(a.ws);
+  p.status = reinterpret_cast<unsigned int*>(ws);
+  p.part = reinterpret_cast<float*>(ws + kWsHeaderBytes);
+  p.budget_ns = a.budget_ns;
+  p.withhold = a.withhold;
+  p.w = static_cast<const uint8_t*>(a.W);
+  p.w_row_bytes = a.ldw * 2;
+  p.prefetch_iters = a.prefetch_iters;
+  p.epi = a.epi;
+  if (mp == 16) return strm::launch<16, 1, kProj>(p, tx, tw, a.num_sms, a.stream);
+  if (mp == 32) return strm::launch<32, 1, kProj>(p, tx, tw, a.num_sms, a.stream);
+  return strm::launch<64, 1, kProj>(p, tx, tw, a.num_sms, a.stream);
+}
+
+}  // namespace fn

@@ -10,7 +10,7 @@ import torch
 from . import (FN_T_BF16, FN_T_FP16, FN_T_FP32, FN_W_BF16, FN_W_FP8_E4M3_B128, FN_W_MXFP8_E4M3, check, fn_adaln_shift_bias, fn_norm_proj_adaln,
                fn_norm_proj_swiglu_nvfp4_swizzled, fn_workspace_size_adaln, fn_fold_weights, fn_norm_proj, fn_norm_proj_swiglu,
                fn_norm_proj_partial, fn_norm_proj_swiglu_nvfp4, fn_post_scale, fn_query_device_status,
-               fn_token_logprobs, fn_token_logprobs_backward, fn_workspace_size)
+               fn_proj, fn_workspace_size_proj, fn_token_logprobs, fn_token_logprobs_backward, fn_workspace_size)
 
 
 def weight_type(Wp: torch.Tensor, scales: Optional[torch.Tensor]) -> int:
@@ -49,6 +49,11 @@ class Workspace:
 
     def get(self, M: int, d: int, N: int, wt: int, swiglu: bool) -> torch.Tensor:
         need = fn_workspace_size(M, d, N, wt, int(swiglu))
+        if self.buf.numel() < need:
+            self.buf = torch.zeros(need, dtype=torch.uint8, device=self.device)
+        return self.buf
+
+    def reserve(self, need: int) -> torch.Tensor:
         if self.buf.numel() < need:
             self.buf = torch.zeros(need, dtype=torch.uint8, device=self.device)
         return self.buf
@@ -209,6 +214,43 @@ class _on:
     def __exit__(self, *exc):
         if self.guard is not None:
             self.guard.__exit__(*exc)
+
+
+_ACT = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+
+
+def proj(x: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None, act: str = "none",
+         residual: Optional[torch.Tensor] = None, ws: Optional[Workspace] = None, out: Optional[torch.Tensor] = None,
+         out_dtype: Optional[torch.dtype] = None, stream=None) -> torch.Tensor:
+    """act(x @ W + bias) + residual (see fn_proj): x bf16 [M, K], W bf16 [K, N],
+    bias fp32 [N]; the output is bf16 or fp32, the type of `out`, else
+    `out_dtype`, else the residual's, else bf16.  `out` may be the residual."""
+    ldx = _rows(x, "x", (torch.bfloat16,))
+    M, K = x.shape
+    _need(W.dim() == 2 and W.shape[0] == K, f"W: {K} rows are needed")
+    ldw = _rows(W, "W", (torch.bfloat16,))
+    N = W.shape[1]
+    dev = x.device
+    _need(act in _ACT, f"act: one of {list(_ACT)}")
+    _vec(bias, "bias", torch.float32, N, dev)
+    if out is None:
+        dt = out_dtype or (residual.dtype if residual is not None else torch.bfloat16)
+        out = torch.empty((M, N), dtype=dt, device=dev)
+    ldy = _rows(out, "out", (torch.bfloat16, torch.float32), (M, N))
+    ldr = 0 if residual is None else _rows(residual, "residual", (out.dtype,), (M, N))
+    _need(W.device == dev and out.device == dev and (residual is None or residual.device == dev),
+          f"every tensor must be on {dev}")
+    # a single row's stride is free: the library wants multiples of 8
+    ldx, ldw = (ldx + 7) // 8 * 8 if M <= 1 else ldx, (ldw + 7) // 8 * 8 if K == 1 else ldw
+    if out is residual:
+        ldr = ldy
+    with _on(dev, stream) as s:
+        if ws is None:
+            ws = Workspace(dev)
+        buf = ws.reserve(fn_workspace_size_proj(M, K, N))
+        check(fn_proj(x, ldx, M, K, W, ldw, N, bias, _ACT[act], residual, ldr, _DTYPE[out.dtype], out, ldy, buf,
+                      buf.numel(), s), "fn_proj")
+    return out
 
 
 class TokenLogprobs(NamedTuple):

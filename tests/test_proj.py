@@ -1,0 +1,261 @@
+"""fn_proj: refusals on the CPU, parity with the oracle on the GPU.
+
+Tolerance, per element, with u = 2^-24: products of bf16 values are exact in
+fp32; the tensor cores and the partial sums add K of them in fp32, so the sum
+is off by at most K u sum |x W| in the worst order, and by a small multiple of
+sqrt(K) u (sum of squares)^(1/2) in practice: the bound used is
+(8 + sqrt(K)) 2^-23 * sum_k |x_k W_k| (truncating adders: 2 u per add), times
+the activation's slope, at most 1.2.  The activation itself carries 16 u of
+its value (ex2-based exponentials, erfc), of |z| for the tanh form's argument
+(its exponential's relative error is the argument's absolute one, 2 u |u2|,
+damped by the logistic factor).  The bias and residual add u each, and the
+store eps / 2 of the value.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+import rmsnorm_linear_projection_flashnorm_b200 as fnb
+from rmsnorm_linear_projection_flashnorm_b200 import torch_api as T
+
+U = 2.0 ** -24
+X, W, Y, R, B, WS = 1 << 30, 1 << 34, 1 << 36, 1 << 37, 1 << 38, 1 << 39
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    fnb.build()
+    fnb.lib()
+
+
+# ------------------------------------------------------------------ CPU: refusals
+def proj_(x=X, ldx=256, M=4, K=256, w=W, ldw=512, N=512, bias=B, act=0, res=R, ldr=512, dt=0, y=Y, ldy=512, ws=WS,
+          ws_bytes=1 << 30):
+    return fnb.fn_proj(x, ldx, M, K, w, ldw, N, bias, act, res, ldr, dt, y, ldy, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(M=-1), fnb.FN_ERR_INVALID_ARG),
+    (dict(K=0), fnb.FN_ERR_INVALID_ARG),
+    (dict(N=0), fnb.FN_ERR_INVALID_ARG),
+    (dict(ldx=248), fnb.FN_ERR_INVALID_ARG),
+    (dict(ldw=504), fnb.FN_ERR_INVALID_ARG),
+    (dict(ldy=511), fnb.FN_ERR_INVALID_ARG),
+    (dict(ldr=511), fnb.FN_ERR_INVALID_ARG),
+    (dict(act=5), fnb.FN_ERR_INVALID_ARG),
+    (dict(act=-1), fnb.FN_ERR_INVALID_ARG),
+    (dict(dt=1), fnb.FN_ERR_INVALID_ARG),                  # fp16 output
+    (dict(x=None), fnb.FN_ERR_INVALID_ARG),
+    (dict(w=None), fnb.FN_ERR_INVALID_ARG),
+    (dict(y=None), fnb.FN_ERR_INVALID_ARG),
+    (dict(ws=None), fnb.FN_ERR_WORKSPACE),
+    (dict(ldx=260), fnb.FN_ERR_UNSUPPORTED_SHAPE),
+    (dict(ldw=513), fnb.FN_ERR_UNSUPPORTED_SHAPE),
+    (dict(M=(1 << 30) + 1), fnb.FN_ERR_UNSUPPORTED_SHAPE),
+    (dict(x=X + 8), fnb.FN_ERR_ALIGNMENT),
+    (dict(w=W + 2), fnb.FN_ERR_ALIGNMENT),
+    (dict(y=Y + 1), fnb.FN_ERR_ALIGNMENT),
+    (dict(dt=2, y=Y + 2), fnb.FN_ERR_ALIGNMENT),
+    (dict(dt=2, res=R + 2), fnb.FN_ERR_ALIGNMENT),
+    (dict(bias=B + 2), fnb.FN_ERR_ALIGNMENT),
+    (dict(ws=WS + 8), fnb.FN_ERR_ALIGNMENT),
+    (dict(y=X + 64), fnb.FN_ERR_ALIAS),
+    (dict(y=W + 64), fnb.FN_ERR_ALIAS),
+    (dict(y=R + 2), fnb.FN_ERR_ALIAS),                     # overlaps the residual, not in place
+    (dict(y=R, ldy=520), fnb.FN_ERR_ALIAS),                # in place with another row stride
+    (dict(y=B + 16), fnb.FN_ERR_ALIAS),
+    (dict(y=WS + 512), fnb.FN_ERR_ALIAS),
+    (dict(ws=R + 1024), fnb.FN_ERR_ALIAS),
+])
+def test_refusals(kw, code):
+    assert proj_(**kw) == code
+
+
+def test_empty_batch_and_workspace_size():
+    assert proj_(M=0, x=None, w=None, y=None, ws=None) == fnb.FN_OK
+    assert fnb.fn_workspace_size_proj(0, 64, 64) == 256
+    sizes = [fnb.fn_workspace_size_proj(m, 4096, 4096) for m in (1, 16, 17, 32, 33, 64)]
+    assert sizes[0] == sizes[1] < sizes[2] == sizes[3] < sizes[4] == sizes[5]
+
+
+def test_torch_api_refuses_what_the_library_cannot_see():
+    x, w = torch.zeros(2, 8, dtype=torch.bfloat16), torch.zeros(8, 16, dtype=torch.bfloat16)
+    for bad in (lambda: T.proj(x, w), lambda: T.proj(x.float(), w), lambda: T.proj(x, w[:7]), lambda: T.proj(x, w.t()),
+                lambda: T.proj(x, w, act="tanh"), lambda: T.proj(x, w, bias=torch.zeros(15)),
+                lambda: T.proj(x, w, residual=torch.zeros(2, 15)),
+                lambda: T.proj(x, w, residual=torch.zeros(2, 16), out=torch.zeros(2, 16, dtype=torch.bfloat16))):
+        with pytest.raises(ValueError):
+            bad()
+
+
+# ------------------------------------------------------------------ GPU: parity
+def padded(rows, cols, ld, seed, std=1.0):
+    """bf16 [rows, cols] in rows of ld; what lies between the rows is NaN."""
+    g = torch.Generator().manual_seed(seed)
+    buf = torch.full((rows, ld), math.nan, dtype=torch.bfloat16)
+    buf[:, :cols] = (torch.randn(rows, cols, generator=g) * std).bfloat16()
+    return buf.cuda()[:, :cols]
+
+
+def up8(n):
+    return (n + 7) // 8 * 8
+
+
+def case(M, K, N, bias=False, act="none", residual=False, fp32=False, pad=0, seed=0, ws=None, alias=False):
+    x = padded(M, K, up8(K) + pad, seed)
+    w = padded(K, N, up8(N) + pad, seed + 1, K ** -0.5)
+    g = torch.Generator().manual_seed(seed + 2)
+    b = torch.randn(N, generator=g).cuda() if bias else None
+    dt = torch.float32 if fp32 else torch.bfloat16
+    r = torch.randn(M, N + 3, generator=g).to(dt).cuda()[:, 1:N + 1] if residual else None
+    buf = torch.full((M + 2, N + 5), 7.0, dtype=dt, device="cuda")
+    out = buf[1:M + 1, 2:N + 2]
+    rc = None if r is None else r.clone()
+    if alias:
+        out.copy_(r)
+        r = out
+    y = T.proj(x, w, bias=b, act=act, residual=r, ws=ws, out=out)
+    torch.cuda.synchronize()
+    assert y is out
+    buf[1:M + 1, 2:N + 2], got = 7.0, y.double().cpu().numpy()
+    assert (buf == 7).all(), "wrote outside the output"
+    xd, wd = x.double().cpu().numpy(), w.double().cpu().numpy()
+    ref = O.project(xd, wd, None if b is None else b.cpu().numpy(), act, None if rc is None else rc.double().cpu())
+    mag = np.abs(xd) @ np.abs(wd)
+    z = np.abs(O.project(xd, wd, None if b is None else b.cpu().numpy()))
+    tol = 1.2 * ((8 + math.sqrt(K)) * 2 * U * mag + U * z) + 16 * U * z * (1 + (z if act == "gelu_tanh" else 0))
+    if residual:
+        tol = tol + U * (np.abs(ref) + np.abs(rc.double().cpu().numpy()))
+    tol = tol + torch.finfo(dt).eps / 2 * np.abs(ref) * (1 + 2 ** -7) + 1e-30
+    bad = np.abs(got - ref) - tol
+    assert not np.isnan(got).any() and bad.max() <= 0, (bad.max(), np.unravel_index(bad.argmax(), bad.shape))
+
+
+MS = [1, 2, 15, 16, 17, 31, 33, 64, 65, 96, 97, 129, 256, 257, 300, 513]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", MS)
+@pytest.mark.parametrize("K,N", [(64, 128), (1, 1), (7, 3), (200, 130), (1000, 257), (4096, 72)])
+def test_sizes(M, K, N):
+    case(M, K, N, residual=True, bias=True, seed=M + K)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("M", [3, 70])
+@pytest.mark.parametrize("fp32", [False, True])
+def test_activations(M, act, fp32):
+    case(M, 333, 259, bias=True, act=act, residual=False, fp32=fp32, pad=8, seed=5)
+    case(M, 333, 259, bias=True, act=act, residual=True, fp32=fp32, pad=16, seed=6)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,K,N", [(1, 4096, 4096), (16, 2048, 4096), (64, 4096, 2048), (45, 2051, 4099),
+                                   (8, 16384, 100), (64, 16000, 640), (3, 64, 30000), (1, 14336, 4096)])
+def test_few_rows_split_k(M, K, N):
+    case(M, K, N, residual=True, seed=1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,K,N", [(300, 14336, 1024), (65, 8192, 4096), (128, 16384, 256), (1000, 4096, 2048),
+                                   (4096, 512, 1024), (700, 2000, 6144), (2048, 4096, 2560), (257, 1024, 20000)])
+def test_many_rows(M, K, N):
+    case(M, K, N, residual=True, bias=True, seed=2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [5, 64, 200])
+@pytest.mark.parametrize("fp32", [False, True])
+def test_residual_in_place(M, fp32):
+    case(M, 1024, 520, residual=True, fp32=fp32, seed=3, alias=True)
+
+
+@pytest.mark.gpu
+def test_one_workspace_for_every_call_in_turn():
+    """Calls of other sizes and of the fused projections in between leave the
+    counters of the shared tiles at zero."""
+    import workloads as WL
+    ws = T.Workspace("cuda")
+    inp = WL.case(8, 512, 1024, False, seed=3)
+    Wp, _ = T.fold(inp["W"].cuda(), inp["g"].cuda())
+    for i, (M, K, N) in enumerate([(1, 4096, 512), (300, 8192, 512), (40, 1000, 3000), (1, 4096, 512), (300, 8192, 512)]):
+        case(M, K, N, seed=i, ws=ws)
+        T.norm_proj(inp["x"].cuda(), Wp, 1024, 1e-6, ws=ws)
+    assert ws.status()[0] == fnb.FN_OK
+    assert (ws.buf[:256] == 0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,K,N", [(7, 4096, 1000), (200, 8192, 1024)])
+def test_repeats_capture_and_streams(M, K, N):
+    x, w = padded(M, K, up8(K), 1), padded(K, N, up8(N), 2, K ** -0.5)
+    ws = T.Workspace("cuda")
+    ref = T.proj(x, w, ws=ws)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        y = T.proj(x, w, ws=ws)
+        torch.cuda.synchronize()
+        assert torch.equal(y, ref)
+    out = torch.empty_like(ref)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        T.proj(x, w, ws=ws, out=out)
+        T.proj(x, w, ws=ws, out=out, residual=out)
+    x.copy_(padded(M, K, up8(K), 9))
+    g.replay()
+    torch.cuda.synchronize()
+    a = T.proj(x, w, ws=ws)
+    b = T.proj(x, w, ws=ws, residual=a)
+    torch.cuda.synchronize()
+    assert torch.equal(out, b)
+    # two calls at once, each with its own workspace
+    s = [torch.cuda.Stream(), torch.cuda.Stream()]
+    wss = [T.Workspace("cuda") for _ in s]
+    for q in wss:
+        q.reserve(fnb.fn_workspace_size_proj(M, K, N))
+    outs = [[torch.empty_like(ref) for _ in range(8)] for _ in s]
+    torch.cuda.synchronize()
+    for i in range(8):
+        for j in range(2):
+            T.proj(x, w, ws=wss[j], out=outs[j][i], stream=s[j])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, a) for os_ in outs for o in os_)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [4, 100])
+def test_non_finite_rows_stay_in_their_rows(M):
+    x, w = padded(M, 512, 512, 1), padded(512, 384, 384, 2)
+    clean = T.proj(x, w)
+    x[1, 5], x[2, 7] = math.nan, math.inf
+    y = T.proj(x, w)
+    torch.cuda.synchronize()
+    assert torch.isnan(y[1]).all() and not torch.isfinite(y[2]).any()
+    keep = [i for i in range(M) if i not in (1, 2)]
+    assert torch.equal(y[keep], clean[keep])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [4, 100])
+def test_timeout_is_reported(M):
+    """A commit that never comes: the epilogue's wait runs out, the call ends
+    and the status word says so."""
+    x, w = padded(M, 512, 512, 1), padded(512, 384, 384, 2)
+    ws = T.Workspace("cuda")
+    fnb.fn_set_debug(fnb.FN_DEBUG_WAIT_BUDGET_NS, 20_000_000)
+    fnb.fn_set_debug(fnb.FN_DEBUG_WITHHOLD_ARRIVE, 1)
+    try:
+        T.proj(x, w, ws=ws)
+        torch.cuda.synchronize()
+        assert ws.status()[0] == fnb.FN_ERR_TIMEOUT
+    finally:
+        fnb.fn_set_debug(fnb.FN_DEBUG_WITHHOLD_ARRIVE, 0)
+        fnb.fn_set_debug(fnb.FN_DEBUG_WAIT_BUDGET_NS, 2_000_000_000)
+    ws.buf.zero_()
+    y = T.proj(x, w, ws=ws)
+    torch.cuda.synchronize()
+    assert ws.status()[0] == fnb.FN_OK and torch.isfinite(y).all()
