@@ -424,6 +424,54 @@ fn_status fn_proj(const void* x, int64_t ldx, int64_t M, int64_t K, const void* 
  * after another.  Depends on the SM count of the current device. */
 size_t fn_workspace_size_proj(int64_t M, int64_t K, int64_t N);
 
+typedef enum {
+  FN_SCORE_SOFTMAX = 0,   /* softmax over all experts' logits */
+  FN_SCORE_SIGMOID = 1    /* each logit's sigmoid */
+} fn_score;
+
+/*
+ * fn_moe_swiglu — a whole mixture-of-experts feed-forward layer for a few
+ * tokens (M <= 64): the RMSNorm, the router, the chosen experts' SwiGLU and
+ * the weighted sum, in the deferred form of fn_norm_proj_swiglu.  With
+ * h = RMSNorm(x; g, eps):
+ *   l[m, e]  = h[m, :] . router[e, :]          (fp64: a choice between close values)
+ *   s        = softmax_e(l) or sigmoid(l)
+ *   ids[m]   = the top_k experts by l, or by s + select_bias where that is
+ *              given; ties to the lower index, NaN below every number
+ *   w[m, j]  = s[ids] (renorm != 0: divided by their sum) * route_scale
+ *   y[m]     = residual[m] + sum_j w[m, j] (silu(h G_e) * (h U_e)) D_e
+ *   x        bf16 [M, d] raw activations
+ *   g        fp32 [d], 16-byte aligned: the norm gain, for the router; NULL
+ *            where the router weight holds it already
+ *   router   bf16 [E, d], not folded
+ *   Wgu      bf16 [E, d, 2I]: per expert the interleaved fold of (G_e, U_e)
+ *            by fn_fold_weights; must be finite, Wd too (the rows that did not
+ *            choose an expert meet it with zeros)
+ *   Wd       bf16 [E, I, d]
+ *   select_bias  fp32 [E] or NULL: added to the scores for the choice only
+ *   residual bf16 [M, d] or NULL
+ *   y        bf16 [M, d]; may be x or the residual themselves (same address)
+ *   ids      int32 [M, top_k] or NULL, largest key first; weights fp32
+ *            [M, top_k] or NULL
+ *   d % 64 == 0, I % 128 == 0, M <= 64, E <= 512, top_k <= 16
+ *   (FN_ERR_UNSUPPORTED_SHAPE); E d and E I below 2^31
+ *   workspace, ws_bytes  >= fn_workspace_size_moe(M, d, I, E, top_k), zeroed
+ *            before first use
+ * fp32 sums; the expert activations are rounded to bf16 once, after the
+ * routing weight, and the result once, after the residual.  Only the chosen
+ * experts' weights are read.  A row with a non-finite activation has NaN or
+ * infinite outputs in its own row only.  M == 0 is a no-op.  Deterministic.
+ */
+fn_status fn_moe_swiglu(const void* x, int64_t M, int64_t d, const float* g, const void* router, int64_t E,
+                        const void* Wgu, const void* Wd, int64_t I, int top_k, fn_score score,
+                        const float* select_bias, int renorm, float route_scale, float eps, const void* residual,
+                        void* y, int32_t* ids, float* weights, void* workspace, size_t ws_bytes, fn_stream_t stream);
+
+/* fn_workspace_size_moe — workspace bytes of fn_moe_swiglu: the header, the
+ * routing table (256 E bytes), fp32 partial sums, and the chosen experts'
+ * activations (at most min(E, M top_k) x 64 x I bf16 values). */
+size_t fn_workspace_size_moe(int64_t M, int64_t d, int64_t I, int64_t E, int top_k);
+
 /*
  * fn_token_logprobs — log probabilities of given tokens, entropies and the
  * top alternatives, from the logits of a head projection (fn_norm_proj with

@@ -40,6 +40,9 @@ FN_ACT_GELU = 2
 FN_ACT_GELU_TANH = 3
 FN_ACT_SILU = 4
 
+FN_SCORE_SOFTMAX = 0
+FN_SCORE_SIGMOID = 1
+
 FN_DEBUG_WAIT_BUDGET_NS = 1
 FN_DEBUG_WITHHOLD_ARRIVE = 2
 FN_DEBUG_FORCE_PATH = 3
@@ -73,6 +76,9 @@ _SIGNATURES = {
     "fn_dequant_mxfp8": (_int, [_vp, _vp, _i64, _i64, _vp, _vp]),
     "fn_workspace_size_proj": (_sz, [_i64, _i64, _i64]),
     "fn_proj": (_int, [_vp, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _int, _vp, _i64, _int, _vp, _i64, _vp, _sz, _vp]),
+    "fn_workspace_size_moe": (_sz, [_i64, _i64, _i64, _i64, _int]),
+    "fn_moe_swiglu": (_int, [_vp, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _i64, _int, _int, _vp, _int, _f32, _f32, _vp,
+                             _vp, _vp, _vp, _vp, _sz, _vp]),
     "fn_token_logprobs": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _f32, _int, _vp, _vp, _vp, _vp, _vp, _vp]),
     "fn_token_logprobs_backward": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _f32, _vp, _i64,
                                           _vp]),
@@ -246,6 +252,18 @@ def fn_proj(x, ldx: int, M: int, K: int, W, ldw: int, N: int, bias, act: int, re
             ldy: int, workspace, ws_bytes: int, stream=None) -> int:
     return lib().fn_proj(_ptr(x), ldx, M, K, _ptr(W), ldw, N, _ptr(bias), act, _ptr(residual), ldr, out_type,
                          _ptr(y), ldy, _ptr(workspace), ws_bytes, _stream(stream))
+
+
+def fn_workspace_size_moe(M: int, d: int, I: int, E: int, top_k: int) -> int:
+    return lib().fn_workspace_size_moe(M, d, I, E, top_k)
+
+
+def fn_moe_swiglu(x, M: int, d: int, g, router, E: int, Wgu, Wd, I: int, top_k: int, score: int, select_bias,
+                  renorm: int, route_scale: float, eps: float, residual, y, ids, weights, workspace, ws_bytes: int,
+                  stream=None) -> int:
+    return lib().fn_moe_swiglu(_ptr(x), M, d, _ptr(g), _ptr(router), E, _ptr(Wgu), _ptr(Wd), I, top_k, score,
+                               _ptr(select_bias), int(renorm), route_scale, eps, _ptr(residual), _ptr(y), _ptr(ids),
+                               _ptr(weights), _ptr(workspace), ws_bytes, _stream(stream))
 
 
 def fn_token_logprobs(logits, type: int, M: int, V: int, ld: int, targets, scale: float, top_k: int, logprob, entropy,

@@ -579,6 +579,77 @@ fn_status fn_proj(const void* x, int64_t ldx, int64_t M, int64_t K, const void* 
   return (stream_path ? launch_proj_stream(a) : launch_proj_tile(a)) == cudaSuccess ? FN_OK : FN_ERR_CUDA;
 }
 
+size_t fn_workspace_size_moe(int64_t M, int64_t d, int64_t I, int64_t E, int top_k) {
+  if (M <= 0 || d <= 0 || I <= 0 || E <= 0 || top_k <= 0 || M > kMoeMaxRows || E > kMoeMaxExperts ||
+      top_k > kMoeMaxTopK || I > kMaxProjDim)
+    return kWsHeaderBytes;
+  return moe_workspace_bytes(M, I, E, top_k, current_sms_or_default());
+}
+
+fn_status fn_moe_swiglu(const void* x, int64_t M, int64_t d, const float* g, const void* router, int64_t E,
+                        const void* Wgu, const void* Wd, int64_t I, int top_k, fn_score score,
+                        const float* select_bias, int renorm, float route_scale, float eps, const void* residual,
+                        void* y, int32_t* ids, float* weights, void* workspace, size_t ws_bytes, fn_stream_t stream) {
+  if (M < 0 || d <= 0 || E <= 0 || I <= 0 || top_k <= 0 || top_k > E) return FN_ERR_INVALID_ARG;
+  if (score != FN_SCORE_SOFTMAX && score != FN_SCORE_SIGMOID) return FN_ERR_INVALID_ARG;
+  if (!eps_ok(eps) || !std::isfinite(route_scale)) return FN_ERR_INVALID_ARG;
+  if (M > kMoeMaxRows || E > kMoeMaxExperts || top_k > kMoeMaxTopK || d % 64 != 0 || I % 128 != 0)
+    return FN_ERR_UNSUPPORTED_SHAPE;
+  if (d > kMaxProjDim || I > kMaxProjDim / 2 || E * d > kMaxDim || E * I > kMaxDim) return FN_ERR_UNSUPPORTED_SHAPE;
+  if (M == 0) return FN_OK;
+  if (!x || !router || !Wgu || !Wd || !y) return FN_ERR_INVALID_ARG;
+  if (!workspace) return FN_ERR_WORKSPACE;
+  if (!aligned16(x) || !aligned16(g) || !aligned16(router) || !aligned16(Wgu) || !aligned16(Wd) ||
+      !aligned16(workspace) || misaligned(select_bias, 4) || misaligned(residual, 2) || misaligned(y, 2) ||
+      misaligned(ids, 4) || misaligned(weights, 4))
+    return FN_ERR_ALIGNMENT;
+  const size_t xb = static_cast<size_t>(M) * d * 2, tb = static_cast<size_t>(M) * top_k * 4;
+  const struct { const void* p; size_t n; } ins[7] = {
+      {x, xb}, {residual, residual ? xb : 0}, {g, static_cast<size_t>(d) * 4}, {router, static_cast<size_t>(E) * d * 2},
+      {Wgu, static_cast<size_t>(E) * d * I * 4}, {Wd, static_cast<size_t>(E) * I * d * 2},
+      {select_bias, static_cast<size_t>(E) * 4}};
+  const struct { const void* p; size_t n; } outs[4] = {{y, xb}, {ids, tb}, {weights, tb}, {workspace, ws_bytes}};
+  for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < 7; ++j) {
+      // y may be x or the residual themselves: both have been read when it is written
+      if (i == 0 && j < 2 && ins[j].p == y) continue;
+      if (overlaps(outs[i].p, outs[i].n, ins[j].p, ins[j].n)) return FN_ERR_ALIAS;
+    }
+    for (int j = i + 1; j < 4; ++j)
+      if (overlaps(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return FN_ERR_ALIAS;
+  }
+  int sms = 0;
+  const fn_status st = check_device(sms);
+  if (st != FN_OK) return st;
+  if (ws_bytes < moe_workspace_bytes(M, I, E, top_k, sms)) return FN_ERR_WORKSPACE;
+  MoeArgs a;
+  a.x = x;
+  a.M = M;
+  a.d = d;
+  a.g = g;
+  a.router = router;
+  a.E = E;
+  a.Wgu = Wgu;
+  a.Wd = Wd;
+  a.I = I;
+  a.top_k = top_k;
+  a.sigmoid = score == FN_SCORE_SIGMOID;
+  a.renorm = renorm != 0;
+  a.select_bias = select_bias;
+  a.route_scale = route_scale;
+  a.eps = eps;
+  a.residual = residual;
+  a.y = y;
+  a.ids = ids;
+  a.weights = weights;
+  a.ws = workspace;
+  a.stream = reinterpret_cast<cudaStream_t>(stream);
+  a.num_sms = sms;
+  a.budget_ns = static_cast<uint64_t>(g_budget_ns.load());
+  a.withhold = g_withhold.load();
+  return launch_moe(a) == cudaSuccess ? FN_OK : FN_ERR_CUDA;
+}
+
 fn_status fn_token_logprobs(const void* logits, fn_dtype type, int64_t M, int64_t V, int64_t ld, const int32_t* targets,
                             float scale, int top_k, float* logprob, float* entropy, float* lse, int32_t* top_ids,
                             float* top_logprobs, fn_stream_t stream) {

@@ -172,6 +172,32 @@ struct MoeRoute {
   int E, k;
 };
 
+struct MoeArgs {
+  const void* x;          // bf16 [M, d]
+  int64_t M, d;
+  const float* g;         // fp32 [d] or null (router only; the experts' weights hold it)
+  const void* router;     // bf16 [E, d]
+  int64_t E;
+  const void* Wgu;        // bf16 [E, d, 2 I], gate and up interleaved per 128 columns
+  const void* Wd;         // bf16 [E, I, d]
+  int64_t I;
+  int top_k, sigmoid, renorm;
+  const float* select_bias;
+  float route_scale, eps;
+  const void* residual;   // bf16 [M, d] or null
+  void* y;                // bf16 [M, d]
+  int* ids;               // int32 [M, top_k] or null
+  float* weights;         // fp32 [M, top_k] or null
+  void* ws;
+  cudaStream_t stream;
+  int num_sms;
+  uint64_t budget_ns;
+  int withhold;
+};
+size_t moe_workspace_bytes(int64_t M, int64_t I, int64_t E, int top_k, int num_sms);
+cudaError_t launch_moe_router(const MoeArgs& a, int* ids, float* weight, float* rinv);
+cudaError_t launch_moe(const MoeArgs& a);
+
 // Token log probabilities (logprobs.cu), validated by the ABI layer.
 constexpr int kMaxTopAlternatives = 32;
 struct LogprobArgs {

@@ -461,4 +461,84 @@ cudaError_t launch_proj_stream(const ProjArgs& a) {
   return strm::launch<64, 1, kProj>(p, tx, tw, a.num_sms, a.stream);
 }
 
+// ---------------------------------------------------------------------------
+// fn_moe_swiglu: router, then the two expert kernels
+// ---------------------------------------------------------------------------
+namespace {
+// Workspace: header | 1/rms | weight table | ids | partials | act
+struct MoeLayout {
+  size_t rinv, weight, ids, part, act, end;
+  int64_t slots;       // most experts that can be chosen
+};
+MoeLayout moe_layout(int64_t M, int64_t I, int64_t E, int top_k, int num_sms) {
+  auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+  const int mp = decode_mpad(M);
+  MoeLayout l;
+  l.slots = E < M * top_k ? E : M * top_k;
+  l.rinv = kWsHeaderBytes;
+  l.weight = l.rinv + up(kMoeMaxRows * 4);
+  l.ids = l.weight + up(static_cast<size_t>(E) * kMoeMaxRows * 4);
+  l.part = l.ids + up(static_cast<size_t>(kMoeMaxRows) * kMoeMaxTopK * 4);
+  l.act = l.part + up(strm::part_bytes(mp, 2, num_sms));
+  l.end = l.act + static_cast<size_t>(l.slots) * mp * I * 2;
+  return l;
+}
+}  // namespace
+
+size_t moe_workspace_bytes(int64_t M, int64_t I, int64_t E, int top_k, int num_sms) {
+  return moe_layout(M, I, E, top_k, num_sms).end;
+}
+
+template <int MPAD>
+static cudaError_t launch_experts(strm::Params& p, const MoeArgs& a, const CUtensorMap (&maps)[4]) {
+  using namespace strm;
+  p.ncols = static_cast<int>(a.I);
+  p.tiles = static_cast<int>(a.I / 128);
+  p.kblocks = static_cast<int>(a.d / BK);
+  p.wrows = static_cast<int>(a.d);
+  const cudaError_t e = strm::launch<MPAD, 2, kUp>(p, maps[0], maps[1], a.num_sms, a.stream);
+  if (e != cudaSuccess) return e;
+  p.ncols = static_cast<int>(a.d);
+  p.tiles = static_cast<int>((a.d + 127) / 128);
+  p.kblocks = static_cast<int>(a.I / BK);
+  p.wrows = static_cast<int>(a.I);
+  return strm::launch<MPAD, 1, kDown>(p, maps[2], maps[3], a.num_sms, a.stream);
+}
+
+cudaError_t launch_moe(const MoeArgs& a) {
+  using namespace strm;
+  const int mp = decode_mpad(a.M);
+  const MoeLayout l = moe_layout(a.M, a.I, a.E, a.top_k, a.num_sms);
+  uint8_t* ws = static_cast<uint8_t*>(a.ws);
+  constexpr CUtensorMapDataType BF16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  CUtensorMap maps[4];   // x, gate/up weight; act, down weight
+  if (!make_tmap_2d(&maps[0], a.x, BF16, 2, a.M, a.d, mp, BK) ||
+      !make_tmap_2d(&maps[1], a.Wgu, BF16, 2, a.E * a.d, 2 * a.I, BK, 64) ||
+      !make_tmap_2d(&maps[2], ws + l.act, BF16, 2, l.slots * mp, a.I, mp, BK) ||
+      !make_tmap_2d(&maps[3], a.Wd, BF16, 2, a.E * a.I, a.d, BK, 64))
+    return cudaErrorInvalidValue;
+  Params p = {};
+  p.M = static_cast<int>(a.M);
+  p.status = reinterpret_cast<unsigned int*>(ws);
+  p.part = reinterpret_cast<float*>(ws + l.part);
+  p.budget_ns = a.budget_ns;
+  p.withhold = a.withhold;
+  p.route.ids = reinterpret_cast<const int*>(ws + l.ids);
+  p.route.weight = reinterpret_cast<const float*>(ws + l.weight);
+  p.route.rinv = reinterpret_cast<const float*>(ws + l.rinv);
+  p.route.E = static_cast<int>(a.E);
+  p.route.k = a.top_k;
+  p.act = reinterpret_cast<__nv_bfloat16*>(ws + l.act);
+  p.epi.residual = a.residual;
+  p.epi.ldr = a.d;
+  p.epi.y = a.y;
+  p.epi.ldy = a.d;
+  const cudaError_t e = launch_moe_router(a, reinterpret_cast<int*>(ws + l.ids), reinterpret_cast<float*>(ws + l.weight),
+                                          reinterpret_cast<float*>(ws + l.rinv));
+  if (e != cudaSuccess) return e;
+  if (mp == 16) return launch_experts<16>(p, a, maps);
+  if (mp == 32) return launch_experts<32>(p, a, maps);
+  return launch_experts<64>(p, a, maps);
+}
+
 }  // namespace fn

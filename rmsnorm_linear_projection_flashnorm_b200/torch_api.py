@@ -10,7 +10,7 @@ import torch
 from . import (FN_T_BF16, FN_T_FP16, FN_T_FP32, FN_W_BF16, FN_W_FP8_E4M3_B128, FN_W_MXFP8_E4M3, check, fn_adaln_shift_bias, fn_norm_proj_adaln,
                fn_norm_proj_swiglu_nvfp4_swizzled, fn_workspace_size_adaln, fn_fold_weights, fn_norm_proj, fn_norm_proj_swiglu,
                fn_norm_proj_partial, fn_norm_proj_swiglu_nvfp4, fn_post_scale, fn_query_device_status,
-               fn_proj, fn_workspace_size_proj, fn_token_logprobs, fn_token_logprobs_backward, fn_workspace_size)
+               fn_moe_swiglu, fn_proj, fn_workspace_size_moe, fn_workspace_size_proj, fn_token_logprobs, fn_token_logprobs_backward, fn_workspace_size)
 
 
 def weight_type(Wp: torch.Tensor, scales: Optional[torch.Tensor]) -> int:
@@ -198,20 +198,31 @@ def _vec(t: Optional[torch.Tensor], name: str, dtype, n: int, dev) -> None:
 
 
 class _on:
-    """Run on the device that holds the tensors, whatever the current one is;
-    gives the stream to launch on (the device's current one by default)."""
+    """Run on the device that holds the tensors, whatever the current one is,
+    and on `stream` (torch.cuda.Stream or a raw handle; the device's current
+    one by default): what is allocated or zeroed inside belongs to that
+    stream, as under torch.cuda.stream."""
 
     def __init__(self, dev: torch.device, stream):
         _need(dev.type == "cuda", f"tensors on {dev}: a CUDA device is needed")
         self.guard = torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else None
+        self.on = None
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
+        if stream is not None:
+            self.on = torch.cuda.stream(stream)
         self.stream = torch.cuda.current_stream(dev) if stream is None else stream
 
     def __enter__(self):
         if self.guard is not None:
             self.guard.__enter__()
+        if self.on is not None:
+            self.on.__enter__()
         return self.stream
 
     def __exit__(self, *exc):
+        if self.on is not None:
+            self.on.__exit__(*exc)
         if self.guard is not None:
             self.guard.__exit__(*exc)
 
@@ -235,7 +246,8 @@ def proj(x: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None, 
     _vec(bias, "bias", torch.float32, N, dev)
     if out is None:
         dt = out_dtype or (residual.dtype if residual is not None else torch.bfloat16)
-        out = torch.empty((M, N), dtype=dt, device=dev)
+        with _on(dev, stream):
+            out = torch.empty((M, N), dtype=dt, device=dev)
     ldy = _rows(out, "out", (torch.bfloat16, torch.float32), (M, N))
     ldr = 0 if residual is None else _rows(residual, "residual", (out.dtype,), (M, N))
     _need(W.device == dev and out.device == dev and (residual is None or residual.device == dev),
@@ -251,6 +263,59 @@ def proj(x: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None, 
         check(fn_proj(x, ldx, M, K, W, ldw, N, bias, _ACT[act], residual, ldr, _DTYPE[out.dtype], out, ldy, buf,
                       buf.numel(), s), "fn_proj")
     return out
+
+
+_SCORE = {"softmax": 0, "sigmoid": 1}
+
+
+def fold_experts(W_gate: torch.Tensor, g: torch.Tensor, W_up: torch.Tensor, stream=None) -> torch.Tensor:
+    """Fold the norm gain into every expert's gate and up weights [E, d, I]:
+    bf16 [E, d, 2I], per expert the interleaved layout of `fold`."""
+    E, d, N = W_gate.shape
+    dev = W_gate.device
+    for t, n in ((W_gate, "W_gate"), (W_up, "W_up")):
+        _need(t.dtype == torch.bfloat16 and tuple(t.shape) == (E, d, N) and t.is_contiguous() and t.device == dev,
+              f"{n}: contiguous bf16 {(E, d, N)} on {dev} is needed")
+    _vec(g, "g", torch.float32, d, dev)
+    with _on(dev, stream) as s:
+        out = torch.empty((E, d, 2 * N), dtype=torch.bfloat16, device=dev)
+        for e in range(E):
+            check(fn_fold_weights(W_gate[e], W_up[e], g, d, N, FN_W_BF16, out[e], None, s), "fn_fold_weights")
+    return out
+
+
+def moe_swiglu(x: torch.Tensor, g: Optional[torch.Tensor], router: torch.Tensor, Wgu: torch.Tensor, Wd: torch.Tensor,
+               top_k: int, eps: float, score: str = "softmax", select_bias: Optional[torch.Tensor] = None,
+               renorm: bool = True, route_scale: float = 1.0, residual: Optional[torch.Tensor] = None,
+               ws: Optional[Workspace] = None, out: Optional[torch.Tensor] = None,
+               stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """A mixture-of-experts layer for at most 64 tokens (see fn_moe_swiglu):
+    (y bf16 [M, d], expert ids int32 [M, top_k], routing weights fp32 [M, top_k]).
+    Wgu [E, d, 2I] from `fold_experts`; `out` may be x or the residual."""
+    dev = x.device
+    _need(x.dim() == 2 and Wgu.dim() == 3 and Wd.dim() == 3, "x [M, d], Wgu [E, d, 2I], Wd [E, I, d] are needed")
+    M, d = x.shape
+    E, I = Wd.shape[0], Wd.shape[1]
+    _need(score in _SCORE, f"score: one of {list(_SCORE)}")
+    _need(isinstance(top_k, int) and 0 < top_k <= E, f"top_k: 1..{E}")
+    if out is None:
+        with _on(dev, stream):
+            out = torch.empty((M, d), dtype=torch.bfloat16, device=dev)
+    for t, n, shape in ((x, "x", (M, d)), (router, "router", (E, d)), (Wgu, "Wgu", (E, d, 2 * I)),
+                        (Wd, "Wd", (E, I, d)), (residual, "residual", (M, d)), (out, "out", (M, d))):
+        _need(t is None or (t.dtype == torch.bfloat16 and tuple(t.shape) == shape and t.is_contiguous()
+                            and t.device == dev), f"{n}: contiguous bf16 {shape} on {dev} is needed")
+    _vec(g, "g", torch.float32, d, dev)
+    _vec(select_bias, "select_bias", torch.float32, E, dev)
+    with _on(dev, stream) as s:
+        ids = torch.empty((M, top_k), dtype=torch.int32, device=dev)
+        w = torch.empty((M, top_k), dtype=torch.float32, device=dev)
+        if ws is None:
+            ws = Workspace(dev)
+        buf = ws.reserve(fn_workspace_size_moe(M, d, I, E, top_k))
+        check(fn_moe_swiglu(x, M, d, g, router, E, Wgu, Wd, I, top_k, _SCORE[score], select_bias, renorm, route_scale,
+                            eps, residual, out, ids, w, buf, buf.numel(), s), "fn_moe_swiglu")
+    return out, ids, w
 
 
 class TokenLogprobs(NamedTuple):
@@ -271,10 +336,11 @@ def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None,
     dev = logits.device
     _vec(targets, "targets", torch.int32, M, dev)
     if out is None:
-        f = torch.empty((3, M), dtype=torch.float32, device=dev)
-        out = TokenLogprobs(f[0] if targets is not None else None, f[1], f[2],
-                            torch.empty((M, top_k), dtype=torch.int32, device=dev),
-                            torch.empty((M, top_k), dtype=torch.float32, device=dev))
+        with _on(dev, stream):
+            f = torch.empty((3, M), dtype=torch.float32, device=dev)
+            out = TokenLogprobs(f[0] if targets is not None else None, f[1], f[2],
+                                torch.empty((M, top_k), dtype=torch.int32, device=dev),
+                                torch.empty((M, top_k), dtype=torch.float32, device=dev))
     else:
         for t, n in ((out.logprob, "logprob"), (out.entropy, "entropy"), (out.lse, "lse")):
             _vec(t, n, torch.float32, M, dev)
@@ -301,7 +367,8 @@ def token_logprobs_backward(logits: torch.Tensor, targets: Optional[torch.Tensor
     for t, n in ((lse, "lse"), (entropy, "entropy"), (grad_logprob, "grad_logprob"), (grad_entropy, "grad_entropy")):
         _vec(t, n, torch.float32, M, dev)
     if out is None:
-        out = torch.empty((M, V), dtype=logits.dtype, device=dev)
+        with _on(dev, stream):
+            out = torch.empty((M, V), dtype=logits.dtype, device=dev)
     ldd = _rows(out, "out", (logits.dtype,), (M, V))
     _need(out.device == dev, f"out on {out.device}, logits on {dev}")
     with _on(dev, stream) as s:
