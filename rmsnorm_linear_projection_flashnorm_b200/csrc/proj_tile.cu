@@ -303,7 +303,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       const int n = q * 32 + lane;                 // column within this CTA's 128
       const int64_t col = static_cast<int64_t>(nb) * BN + rank * 128 + n;
       const bool col_ok = col < p.N;
-      const float bias = p.epi.bias && col_ok ? __ldg(p.epi.bias + col) : 0.f;
       const int row0 = mb * p.nb;
       auto release = [&]() {
         // this CTA's epilogue has read TMEM buffer b
@@ -315,17 +314,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
           if (et == 0) mbar_arrive_remote(acc_empty0 + b * 8);
         }
       };
-      auto finish = [&](int c, const float(&v)[32]) {
+      auto finish = [&](int c, float(&v)[32]) {
         // rows row0 + 32 c + j of column col
-        if (!col_ok) return;
         const int r0 = row0 + 32 * c;
-        const int nr = min(p.M - r0, 32);
-        float res[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) res[j] = j < nr ? epi_residual(p.epi, r0 + j, col) : 0.f;
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (j < nr) epi_store(p.epi, r0 + j, col, epi_act(p.epi.act, v[j] + bias) + res[j]);
+        if (col_ok) epi_finish<32>(p.epi, r0, min(p.M - r0, 32), col, v);
       };
       if (!g.shared) {
 #pragma unroll 1

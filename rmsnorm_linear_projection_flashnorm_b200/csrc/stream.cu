@@ -41,6 +41,7 @@ constexpr int BK = 64;
 constexpr int NUM_THREADS = 192;           // producer, MMA issuer, 4 epilogue warps
 constexpr int W_BOX_BYTES = 64 * BK * 2;   // 64 columns x 64 k rows
 constexpr int SMEM_BUDGET = 200 * 1024;
+constexpr int RC = 16;                     // rows of an epilogue chunk
 constexpr int MAX_SHARE = 16;              // CTAs to a tile: the last one reads all their partials
 
 enum Mode : int { kProj = 0, kUp = 1, kDown = 2 };
@@ -292,7 +293,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const int q = warp & 3;                       // TMEM lane quarter this warp may access
     const int n = q * 32 + lane;                  // column within the tile
     const int et = threadIdx.x - 64;              // 0..127
-    const int Q = (p.M + 3) >> 2;
     int seg = 0;
     for (long long it = it0; it < it1; ++seg) {
       const int tile = static_cast<int>(it / kblocks);
@@ -307,98 +307,125 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       named_bar_sync(1, 128);
       if (!bars.epi_ok[b]) break;
       tc_fence_after();
-      float acc[HALVES][MPAD];
+      // Chunks of 16 rows: the code of one chunk serves them all.
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + b * HALVES * MPAD;
+      auto finish = [&](int m0, float(&acc)[HALVES][RC]) {
+        if constexpr (MODE == kUp) {
+          // act = w silu(r gate) (r up), one round to bf16; 0 for rows that did not choose the expert
+          const int slot = tile / p.tiles;
+          const float* wt = p.route.weight + bars.experts[slot] * kMoeMaxRows + m0;
+          __nv_bfloat16* dst = p.act + (static_cast<int64_t>(slot) * MPAD + m0) * p.ncols + tile % p.tiles * 128 + n;
+          float w[RC], r[RC];
 #pragma unroll
-      for (int h = 0; h < HALVES; ++h)
-        dec::tmem_ld_cols<MPAD>(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + (b * HALVES + h) * MPAD, acc[h]);
-      tc_fence_before();
-      mbar_arrive(&bars.acc_empty[b]);
-      if (kb0 != 0 || kb1 != kblocks) {
-        // Shared tile: publish the partial (float4 groups [half][row / 4][column],
-        // rows below M only), count, and go on unless this was the last one.
-        const int slot = cta * 2 + (seg == 0 ? 0 : 1);
-        float4* mine = reinterpret_cast<float4*>(p.part + static_cast<int64_t>(slot) * C::SLOT_FLOATS);
-#pragma unroll
-        for (int h = 0; h < HALVES; ++h)
-#pragma unroll
-          for (int g = 0; g < MPAD / 4; ++g)
-            if (g < Q)
-              __stcg(mine + (h * (MPAD / 4) + g) * 128 + n,
-                     make_float4(acc[h][4 * g], acc[h][4 * g + 1], acc[h][4 * g + 2], acc[h][4 * g + 3]));
-        const long long t0 = static_cast<long long>(tile) * kblocks;
-        const int c_first = owner_of(t0), c_last = owner_of(t0 + kblocks - 1);
-        __threadfence();
-        named_bar_sync(1, 128);
-        if (et == 0) {
-          bars.last = count_partial(p.status, c_first, c_last - c_first + 1);
-          __threadfence();
-        }
-        named_bar_sync(1, 128);
-        if (!bars.last) continue;
-        // every partial of the tile is visible: add them in ascending k order
-#pragma unroll
-        for (int h = 0; h < HALVES; ++h)
-#pragma unroll
-          for (int m = 0; m < MPAD; ++m) acc[h][m] = 0.f;
-        constexpr int GROUPS = HALVES * MPAD / 4;
-        constexpr int CB = GROUPS >= 16 ? 1 : 16 / GROUPS;       // contributors in flight
-        for (int c0 = c_first; c0 <= c_last; c0 += CB) {
-          float4 v[CB][GROUPS];
-#pragma unroll
-          for (int j = 0; j < CB; ++j) {
-            const int c = c0 + j;
-            if (c <= c_last) {
-              // a CTA's first segment is slot 0; this tile is not its first when its share begins before it
-              const int sl = c * 2 + (c * total / grid >= t0 ? 0 : 1);
-              const float4* src = reinterpret_cast<const float4*>(p.part + static_cast<int64_t>(sl) * C::SLOT_FLOATS);
-#pragma unroll
-              for (int g = 0; g < GROUPS; ++g)
-                if (g % (MPAD / 4) < Q) v[j][g] = __ldcg(src + g * 128 + n);
-            }
+          for (int j = 0; j < RC; ++j) {
+            w[j] = m0 + j < p.M ? __ldcg(wt + j) : 0.f;
+            r[j] = m0 + j < p.M ? __ldcg(p.route.rinv + m0 + j) : 0.f;
           }
 #pragma unroll
-          for (int j = 0; j < CB; ++j) {
-            if (c0 + j <= c_last) {
+          for (int j = 0; j < RC; ++j) {
+            const float v = w[j] * (silu_f32(acc[0][j] * r[j]) * (acc[HALVES - 1][j] * r[j]));
+            dst[static_cast<int64_t>(j) * p.ncols] = __float2bfloat16_rn(w[j] != 0.f ? v : 0.f);
+          }
+        } else {
+          const int64_t col = static_cast<int64_t>(tile) * 128 + n;
+          if (col < p.ncols) epi_finish<RC>(p.epi, m0, min(p.M - m0, RC), col, acc[0]);
+        }
+      };
+      auto load = [&](int m0, float(&acc)[HALVES][RC]) {
+        uint32_t raw[HALVES][RC];
+#pragma unroll
+        for (int h = 0; h < HALVES; ++h) tmem_ld16(taddr + h * MPAD + m0, raw[h]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int h = 0; h < HALVES; ++h)
+#pragma unroll
+          for (int j = 0; j < RC; ++j) acc[h][j] = __uint_as_float(raw[h][j]);
+      };
+      // kUp stores the padding rows too (zeros, the next kernel's operand)
+      const int m_end = MODE == kUp ? MPAD : p.M;
+      if (kb0 == 0 && kb1 == kblocks) {
+#pragma unroll 1
+        for (int m0 = 0; m0 < m_end; m0 += RC) {
+          float acc[HALVES][RC];
+          load(m0, acc);
+          finish(m0, acc);
+        }
+        tc_fence_before();
+        mbar_arrive(&bars.acc_empty[b]);
+        continue;
+      }
+      // Shared tile: publish the partial (float4 groups [half][row / 4][column],
+      // rows below M only), count, and go on unless this was the last one.
+      {
+        const int slot = cta * 2 + (seg == 0 ? 0 : 1);
+        float4* mine = reinterpret_cast<float4*>(p.part + static_cast<int64_t>(slot) * C::SLOT_FLOATS);
+#pragma unroll 1
+        for (int m0 = 0; m0 < p.M; m0 += RC) {
+          float acc[HALVES][RC];
+          load(m0, acc);
+#pragma unroll
+          for (int h = 0; h < HALVES; ++h)
+#pragma unroll
+            for (int g = 0; g < RC / 4; ++g)
+              if (m0 + 4 * g < p.M)
+                __stcg(mine + (h * (MPAD / 4) + m0 / 4 + g) * 128 + n,
+                       make_float4(acc[h][4 * g], acc[h][4 * g + 1], acc[h][4 * g + 2], acc[h][4 * g + 3]));
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&bars.acc_empty[b]);
+      const long long t0 = static_cast<long long>(tile) * kblocks;
+      const int c_first = owner_of(t0), c_last = owner_of(t0 + kblocks - 1);
+      __threadfence();
+      named_bar_sync(1, 128);
+      if (et == 0) {
+        bars.last = count_partial(p.status, c_first, c_last - c_first + 1);
+        __threadfence();
+      }
+      named_bar_sync(1, 128);
+      if (!bars.last) continue;
+      // every partial of the tile is visible: add them in ascending k order
+#pragma unroll 1
+      for (int m0 = 0; m0 < m_end; m0 += RC) {
+        float acc[HALVES][RC];
+#pragma unroll
+        for (int h = 0; h < HALVES; ++h)
+#pragma unroll
+          for (int j = 0; j < RC; ++j) acc[h][j] = 0.f;
+        constexpr int GROUPS = HALVES * RC / 4;
+        constexpr int CB = 16 / GROUPS;                          // contributors in flight
+        if (m0 < p.M) {
+#pragma unroll 1
+          for (int c0 = c_first; c0 <= c_last; c0 += CB) {
+            float4 v[CB][GROUPS];
+#pragma unroll
+            for (int j = 0; j < CB; ++j) {
+              const int c = min(c0 + j, c_last);
+              // a CTA's first segment is slot 0; this tile is not its first when its share begins before it
+              const int sl = c * 2 + (c * total / grid >= t0 ? 0 : 1);
+              const float4* src =
+                  reinterpret_cast<const float4*>(p.part + static_cast<int64_t>(sl) * C::SLOT_FLOATS) + m0 / 4 * 128 + n;
 #pragma unroll
               for (int g = 0; g < GROUPS; ++g) {
-                if (g % (MPAD / 4) < Q) {
-                  float* a = &acc[g / (MPAD / 4)][g % (MPAD / 4) * 4];
-                  a[0] += v[j][g].x;
-                  a[1] += v[j][g].y;
-                  a[2] += v[j][g].z;
-                  a[3] += v[j][g].w;
-                }
+                v[j][g] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (c0 + j <= c_last && m0 + 4 * (g % (RC / 4)) < p.M)
+                  v[j][g] = __ldcg(src + (g / (RC / 4) * (MPAD / 4) + g % (RC / 4)) * 128);
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < CB; ++j) {
+#pragma unroll
+              for (int g = 0; g < GROUPS; ++g) {
+                float* a = &acc[g / (RC / 4)][g % (RC / 4) * 4];
+                a[0] += v[j][g].x;
+                a[1] += v[j][g].y;
+                a[2] += v[j][g].z;
+                a[3] += v[j][g].w;
               }
             }
           }
         }
-      }
-      if constexpr (MODE == kUp) {
-        // act = w silu(r gate) (r up), one round to bf16; 0 for rows that did not choose the expert
-        const int slot = tile / p.tiles;
-        const float* wt = p.route.weight + bars.experts[slot] * kMoeMaxRows;
-        __nv_bfloat16* dst = p.act + (static_cast<int64_t>(slot) * MPAD) * p.ncols + tile % p.tiles * 128 + n;
-#pragma unroll
-        for (int m = 0; m < MPAD; ++m) {
-          const float w = m < p.M ? __ldcg(wt + m) : 0.f;
-          float v = 0.f;
-          if (w != 0.f) {
-            const float r = __ldcg(p.route.rinv + m);
-            v = w * (silu_f32(acc[0][m] * r) * (acc[HALVES - 1][m] * r));
-          }
-          dst[static_cast<int64_t>(m) * p.ncols] = __float2bfloat16_rn(v);
-        }
-      } else {
-        const int64_t col = static_cast<int64_t>(tile) * 128 + n;
-        if (col < p.ncols) {
-          const float bias = p.epi.bias ? __ldg(p.epi.bias + col) : 0.f;
-          float res[MPAD];
-#pragma unroll
-          for (int m = 0; m < MPAD; ++m) res[m] = m < p.M ? epi_residual(p.epi, m, col) : 0.f;
-#pragma unroll
-          for (int m = 0; m < MPAD; ++m)
-            if (m < p.M) epi_store(p.epi, m, col, epi_act(p.epi.act, acc[0][m] + bias) + res[m]);
-        }
+        finish(m0, acc);
       }
     }
   }
