@@ -532,6 +532,8 @@ fn_status fn_proj(const void* x, int64_t ldx, int64_t M, int64_t K, const void* 
   if (M > kMaxProjDim || K > kMaxProjDim || N > kMaxProjDim) return FN_ERR_UNSUPPORTED_SHAPE;
   if (ldx % 8 != 0 || ldw % 8 != 0 || ldx > kMaxDim || ldw > kMaxDim || proj_tile_count(M, N) > kMaxDim)
     return FN_ERR_UNSUPPORTED_SHAPE;
+  // iterations of 64 k rows x 128 columns, counted in 32 bits times the CTAs (a weight of 0.27 TB)
+  if (((K + 63) / 64) * ((N + 127) / 128) > kMaxDim / 128) return FN_ERR_UNSUPPORTED_SHAPE;
   if (M == 0) return FN_OK;
   if (!x || !W || !y) return FN_ERR_INVALID_ARG;
   if (!workspace) return FN_ERR_WORKSPACE;
@@ -596,6 +598,7 @@ fn_status fn_moe_swiglu(const void* x, int64_t M, int64_t d, const float* g, con
   if (M > kMoeMaxRows || E > kMoeMaxExperts || top_k > kMoeMaxTopK || d % 64 != 0 || I % 128 != 0)
     return FN_ERR_UNSUPPORTED_SHAPE;
   if (d > kMaxProjDim || I > kMaxProjDim / 2 || E * d > kMaxDim || E * I > kMaxDim) return FN_ERR_UNSUPPORTED_SHAPE;
+  if (E * (I / 128) * (d / 64) > kMaxDim / 128) return FN_ERR_UNSUPPORTED_SHAPE;   // iterations, as in fn_proj
   if (M == 0) return FN_OK;
   if (!x || !router || !Wgu || !Wd || !y) return FN_ERR_INVALID_ARG;
   if (!workspace) return FN_ERR_WORKSPACE;

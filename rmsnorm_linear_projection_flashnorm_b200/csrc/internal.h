@@ -155,6 +155,24 @@ struct ProjArgs {
   int withhold;
   int prefetch_iters;
 };
+// Fix-up of the tiles whose k range several CTAs shared (proj_fixup.cu): the
+// partials' layout and the cut.  Sharer c (a CTA, or a pair with ranks == 2)
+// holds iterations [c total / sharers, (c + 1) total / sharers) of the tiles
+// tile0 .. tile0 + tiles - 1 in turn, kblocks to a tile; its partial of a tile
+// is in slot (c ranks + rank) 2, or the next one when another tile came first:
+// float4 groups [row / 4][128 columns].
+struct FixupArgs {
+  const float* part;
+  int64_t slot_floats;
+  int64_t total;
+  int kblocks, sharers, ranks;
+  int tile0, tiles;
+  int group_m, num_m, num_n, rows;   // raster and rows of a tile
+  int64_t M, N;
+  Epilogue epi;
+  cudaStream_t stream;
+};
+cudaError_t launch_proj_fixup(const FixupArgs& a);
 size_t proj_stream_workspace_bytes(int64_t M, int num_sms);
 size_t proj_tile_workspace_bytes(int64_t M, int64_t K, int64_t N, int num_sms);
 int64_t proj_tile_count(int64_t M, int64_t N);

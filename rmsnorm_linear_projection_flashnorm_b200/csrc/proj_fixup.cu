@@ -1,0 +1,76 @@
+// Fix-up of fn_proj: adds the fp32 partials of the tiles whose k range several
+// CTAs shared, in ascending k order, and runs the epilogue, sm_100a.
+//
+// One thread per (tile, 4 rows, column): all SMs take part, so its cost is a
+// launch and one round through L2 (about 4 us).  The CTA that happens to be
+// last doing it alone took 10 to 30 us above 16 rows.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "epilogue.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace fn {
+namespace fix {
+
+constexpr int THREADS = 256;     // 128 columns x 2 row groups
+constexpr int IN_FLIGHT = 4;     // contributors' loads in flight
+
+__device__ __forceinline__ long long div64(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
+__global__ void __launch_bounds__(THREADS) proj_fixup_kernel(const FixupArgs p) {
+  const int groups = (p.rows + 7) / 8;                 // blocks of 8 rows to a tile and rank
+  int b = static_cast<int>(blockIdx.x);
+  const int g = (b % groups) * 2 + static_cast<int>(threadIdx.x >> 7);
+  b /= groups;
+  const int rank = b % p.ranks;
+  const int t = b / p.ranks;                           // tile, from tile0 on
+  const int n = static_cast<int>(threadIdx.x & 127);
+  const long long t0 = static_cast<long long>(t) * p.kblocks;
+  const int first = static_cast<int>(div64((t0 + 1) * p.sharers - 1, p.total));
+  const int last = static_cast<int>(div64((t0 + p.kblocks) * p.sharers - 1, p.total));
+  const int tile = p.tile0 + t;
+  const int per_group = p.group_m * p.num_n;
+  const int first_m = tile / per_group * p.group_m;
+  const int gm = min(p.num_m - first_m, p.group_m);
+  const int r = tile % per_group;
+  const int64_t col = (static_cast<int64_t>(r / gm) * p.ranks + rank) * 128 + n;
+  const int64_t row = static_cast<int64_t>(first_m + r % gm) * p.rows + 4 * g;
+  const int rows = static_cast<int>(min(p.M - row, static_cast<int64_t>(min(p.rows - 4 * g, 4))));
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (first == last || rows <= 0 || col >= p.N) return;   // whole tiles are finished already
+  float v[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int c0 = first; c0 <= last; c0 += IN_FLIGHT) {
+    float4 q[IN_FLIGHT];
+#pragma unroll
+    for (int j = 0; j < IN_FLIGHT; ++j) {
+      const int c = min(c0 + j, last);
+      const int64_t slot = (static_cast<int64_t>(c) * p.ranks + rank) * 2 + (div64(c * p.total, p.sharers) >= t0 ? 0 : 1);
+      q[j] = __ldcg(reinterpret_cast<const float4*>(p.part + slot * p.slot_floats) + g * 128 + n);
+    }
+#pragma unroll
+    for (int j = 0; j < IN_FLIGHT; ++j) {
+      if (c0 + j <= last) {
+        v[0] += q[j].x;
+        v[1] += q[j].y;
+        v[2] += q[j].z;
+        v[3] += q[j].w;
+      }
+    }
+  }
+  epi_finish<4>(p.epi, row, rows, col, v);
+}
+
+}  // namespace fix
+
+cudaError_t launch_proj_fixup(const FixupArgs& a) {
+  const unsigned grid = static_cast<unsigned>(a.tiles) * a.ranks * ((a.rows + 7) / 8);
+  return launch_pdl(fix::proj_fixup_kernel, grid, fix::THREADS, 0, a.stream, a);
+}
+
+}  // namespace fn

@@ -15,9 +15,9 @@
 // rounds as fill every pair; the k ranges of the tiles that are left over
 // (fewer than pairs) are cut into equal shares over all pairs where that
 // saves more than the exchange costs.  Sharing CTAs write fp32 partials to
-// the workspace and count themselves; the one that counts last adds them in
-// ascending k order and finishes the tile (no CTA waits for another, no
-// floating-point atomics, bit-identical repeats).
+// the workspace, and a fix-up kernel adds them in ascending k order and
+// finishes the tile (no CTA waits for another, no floating-point atomics,
+// bit-identical repeats).
 //
 // Layout per CTA: 10 warps.
 //   warp 0      TMA producer (own weight columns, own rows)
@@ -58,7 +58,7 @@ struct Params {
   int sharers;                     // pairs that take a share of them (each at least one k block)
   int stages;
   Epilogue epi;
-  unsigned int* status;            // workspace header: status word and counters
+  unsigned int* status;            // workspace header: status word
   float* part;                     // [grid][2][MAX_NB x 128]
   unsigned long long budget_ns;
   int withhold;
@@ -72,7 +72,6 @@ struct alignas(8) Bars {
   uint32_t tmem_base;
   int abort_flag;
   int epi_ok[2];
-  int last;
 };
 constexpr size_t SMEM = 1024 + RING_BYTES + sizeof(Bars);
 static_assert(SMEM <= 232448, "shared memory budget");
@@ -329,11 +328,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         release();
         continue;
       }
-      // Shared tile: publish the partial (float4 groups [row / 4][column]) and
-      // count; the CTA that counts last adds all of them and finishes.
-      const long long total = static_cast<long long>(p.rest) * p.kblocks;
-      const int r = g.tile - p.full;
-      const long long t0 = static_cast<long long>(r) * p.kblocks;
+      // Shared tile: publish the partial (float4 groups [row / 4][column]); the
+      // fix-up kernel adds them and finishes.
+      const long long t0 = static_cast<long long>(g.tile - p.full) * p.kblocks;
       const int slot = static_cast<int>(blockIdx.x) * 2 + (share_begin(p, pair) >= t0 ? 0 : 1);
       float4* mine = reinterpret_cast<float4*>(p.part + static_cast<int64_t>(slot) * SLOT_FLOATS);
 #pragma unroll 1
@@ -342,42 +339,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         dec::tmem_ld_cols<32>(taddr + c * 32, v);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          __stcg(mine + (c * 8 + j) * 128 + n, make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
+          if (row0 + 32 * c + 4 * j < p.M)
+            __stcg(mine + (c * 8 + j) * 128 + n, make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
       }
       release();
-      const int c_first = static_cast<int>(((t0 + 1) * p.sharers - 1) / total);
-      const int c_last = static_cast<int>(((t0 + p.kblocks) * p.sharers - 1) / total);
-      __threadfence();
-      named_bar_sync(1, EPI_THREADS);
-      if (et == 0) {
-        bars.last = count_partial(p.status, c_first * 2 + static_cast<int>(rank), c_last - c_first + 1);
-        __threadfence();
-      }
-      named_bar_sync(1, EPI_THREADS);
-      if (!bars.last) continue;
-#pragma unroll 1
-      for (int c = half; c < chunks; c += 2) {
-        float v[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = 0.f;
-#pragma unroll 2
-        for (int o = c_first; o <= c_last; ++o) {
-          // a pair's first shared segment is slot 0; this tile is not its first when its share begins before it
-          const int sl = (o * 2 + static_cast<int>(rank)) * 2 + (share_begin(p, o) >= t0 ? 0 : 1);
-          const float4* src = reinterpret_cast<const float4*>(p.part + static_cast<int64_t>(sl) * SLOT_FLOATS);
-          float4 t[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) t[j] = __ldcg(src + (c * 8 + j) * 128 + n);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            v[4 * j] += t[j].x;
-            v[4 * j + 1] += t[j].y;
-            v[4 * j + 2] += t[j].z;
-            v[4 * j + 3] += t[j].w;
-          }
-        }
-        finish(c, v);
-      }
     }
   }
 
@@ -409,7 +374,7 @@ Plan make_plan(int64_t M, int64_t K, int64_t N, int num_sms) {
   q.num_n = static_cast<int>((N + BN - 1) / BN);
   q.kblocks = static_cast<int>((K + BK - 1) / BK);
   const int64_t tiles = static_cast<int64_t>(q.num_m) * q.num_n;
-  const int pairs = (num_sms < kMaxCounters ? num_sms : kMaxCounters) / 2;
+  const int pairs = num_sms / 2;
   const int64_t rest = tiles % pairs;
   // At most 8 pairs to a tile (the last one reads all partials), at least 4 k
   // blocks to a share.
@@ -473,7 +438,27 @@ cudaError_t launch_proj_tile(const ProjArgs& a) {
   p.withhold = a.withhold;
   const cudaError_t e = ensure_smem_limit<proj_tile_kernel>(static_cast<int>(SMEM));
   if (e != cudaSuccess) return e;
-  return launch_pdl(proj_tile_kernel, static_cast<unsigned>(2 * q.pairs), NUM_THREADS, SMEM, a.stream, tx, tw, p);
+  const cudaError_t l =
+      launch_pdl(proj_tile_kernel, static_cast<unsigned>(2 * q.pairs), NUM_THREADS, SMEM, a.stream, tx, tw, p);
+  if (l != cudaSuccess || q.rest == 0) return l;
+  FixupArgs f = {};
+  f.part = p.part;
+  f.slot_floats = SLOT_FLOATS;
+  f.total = static_cast<int64_t>(q.rest) * q.kblocks;
+  f.kblocks = q.kblocks;
+  f.sharers = q.sharers;
+  f.ranks = 2;
+  f.tile0 = q.full;
+  f.tiles = q.rest;
+  f.group_m = p.group_m;
+  f.num_m = q.num_m;
+  f.num_n = q.num_n;
+  f.rows = q.nb;
+  f.M = a.M;
+  f.N = a.N;
+  f.epi = a.epi;
+  f.stream = a.stream;
+  return launch_proj_fixup(f);
 }
 
 }  // namespace fn

@@ -23,9 +23,11 @@
 // masks.
 //
 // A tile whose k range falls to one CTA is finished by it.  The CTAs that
-// share a tile write fp32 partials to the workspace and count themselves; the
-// one that counts last adds all partials in ascending k order (a fixed order,
-// so repeats are bit-identical) and finishes.  No CTA waits for another.
+// share a tile write fp32 partials to the workspace.  With few rows, and for
+// the experts, they count themselves, and the one that counts last adds all
+// partials in ascending k order (a fixed order, so repeats are bit-identical)
+// and finishes; kProj above 16 rows leaves that to the fix-up kernel.  No CTA
+// waits for another.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -41,8 +43,10 @@ constexpr int BK = 64;
 constexpr int NUM_THREADS = 192;           // producer, MMA issuer, 4 epilogue warps
 constexpr int W_BOX_BYTES = 64 * BK * 2;   // 64 columns x 64 k rows
 constexpr int SMEM_BUDGET = 200 * 1024;
-constexpr int RC = 16;                     // rows of an epilogue chunk
+constexpr int RC = 8;                      // rows of an epilogue chunk
 constexpr int MAX_SHARE = 16;              // CTAs to a tile: the last one reads all their partials
+constexpr unsigned ALIGN_SLACK = 3;
+constexpr int FIXUP_ROWS = 16;             // kProj: more rows than these are finished by the fix-up kernel
 
 enum Mode : int { kProj = 0, kUp = 1, kDown = 2 };
 enum : unsigned { kSiteProdEmpty = 1, kSiteMmaAccEmpty, kSiteMmaFull, kSiteEpiAccFull };
@@ -59,6 +63,7 @@ struct Params {
   const uint8_t* w;              // weight base and row bytes (L2 prefetch addresses, kProj)
   int64_t w_row_bytes;
   int prefetch_iters;
+  int fixup;                     // kProj: shared tiles are finished by the fix-up kernel
   Epilogue epi;                  // kProj, kDown
   MoeRoute route;                // kUp, kDown
   __nv_bfloat16* act;            // kUp writes [slot][MPAD][I]
@@ -97,6 +102,19 @@ constexpr size_t smem_bytes() {
 }
 static_assert(smem_bytes<16, 1>() <= 232448 && smem_bytes<64, 2>() <= 232448, "shared memory budget");
 
+// CTAs that take a share of tiles x kblocks iterations: all of them, but no
+// more than MAX_SHARE to a tile; or a whole number per tile where that costs
+// at most ALIGN_SLACK iterations more, since a share that ends with its tile
+// has one exchange instead of two.
+__host__ __device__ __forceinline__ unsigned share_count(int tiles, int kblocks, unsigned ctas) {
+  const unsigned total = static_cast<unsigned>(tiles) * kblocks;
+  unsigned most = total < ctas ? total : ctas;
+  if (most > static_cast<unsigned>(tiles) * MAX_SHARE) most = static_cast<unsigned>(tiles) * MAX_SHARE;
+  const unsigned s = most / tiles;
+  if (s == 0) return most;
+  return (kblocks + s - 1) / s <= (total + most - 1) / most + ALIGN_SLACK ? s * tiles : most;
+}
+
 __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, unsigned long long budget) {
   const uint64_t t0 = globaltimer_ns();
   while (!mbar_try_wait(bar, parity)) {
@@ -117,7 +135,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   auto stage_x = [&](int s) { return smem + s * C::STAGE_BYTES + C::W_BYTES; };
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int cta = blockIdx.x;
+  const unsigned cta = blockIdx.x;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -145,24 +163,23 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
   // The iteration space: tiles x kblocks, cut into one contiguous share per CTA.
   int tiles = p.tiles, kblocks = p.kblocks;
-  long long total = static_cast<long long>(tiles) * kblocks;
-  auto shares = [&]() {
-    const long long most = min(total, static_cast<long long>(tiles) * MAX_SHARE);
-    return static_cast<int>(min(most, static_cast<long long>(gridDim.x)));
+  unsigned total, grid, it0, it1;
+  auto cut = [&]() {
+    total = static_cast<unsigned>(tiles) * kblocks;
+    grid = share_count(tiles, kblocks, gridDim.x);
+    it0 = cta < grid ? cta * total / grid : 0;
+    it1 = cta < grid ? (cta + 1) * total / grid : 0;
   };
-  int grid = shares();
   if (MODE == kProj) {
-    // This overlaps the previous kernel in the stream: an L2 prefetch cannot
-    // return stale data, whoever wrote the weight.  One 128-byte line per
-    // thread and step.
-    // (the first k blocks of the share)
-    const long long b0 = cta < grid ? cta * total / grid : 0;
-    const long long b1 = cta < grid ? (cta + 1LL) * total / grid : 0;
-    const int n_it = static_cast<int>(min(static_cast<long long>(p.prefetch_iters), b1 - b0));
+    cut();
+    // This overlaps the previous kernel in the stream: an L2 prefetch of the
+    // share's first k blocks cannot return stale data, whoever wrote the
+    // weight.  One 128-byte line per thread and step.
+    const int n_it = static_cast<int>(min(static_cast<unsigned>(p.prefetch_iters), it1 - it0));
     for (int i = threadIdx.x; i < n_it * BK * 2; i += NUM_THREADS) {
-      const long long it = b0 + i / (BK * 2);
-      const int tile = static_cast<int>(it / kblocks);
-      const int64_t k = (it - static_cast<long long>(tile) * kblocks) * BK + (i >> 1) % BK;
+      const unsigned it = it0 + i / (BK * 2);
+      const unsigned tile = it / kblocks;
+      const int64_t k = static_cast<int64_t>(it - tile * kblocks) * BK + (i >> 1) % BK;
       const int64_t col = static_cast<int64_t>(tile) * 128 + (i & 1) * 64;
       if (k < p.wrows && col < p.ncols)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(p.w + k * p.w_row_bytes + col * 2));
@@ -171,8 +188,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  grid_dependency_wait();
-  grid_launch_dependents();
+  // The router has completed before kUp allows kDown to launch (kUp waits for
+  // it first), so kDown may read the experts' list and the weights, which no
+  // kernel of this call writes, while kUp still runs; its other operand and
+  // the workspace only behind the wait.
+  if (MODE != kDown) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+  }
   if (MODE != kProj) {
     // the chosen experts in ascending order, from the router's ids
     for (int i = threadIdx.x; i < p.M * p.route.k; i += NUM_THREADS) {
@@ -192,13 +215,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const int n = bars.n_active;
     if (MODE == kUp) tiles *= n;
     else kblocks *= n;
-    total = static_cast<long long>(tiles) * kblocks;
-    grid = shares();
+    cut();
   }
-  const long long it0 = cta < grid ? cta * total / grid : 0;
-  const long long it1 = cta < grid ? (cta + 1LL) * total / grid : 0;
   // the CTA whose share holds iteration `it`
-  auto owner_of = [&](long long it) { return static_cast<int>(((it + 1) * grid - 1) / total); };
+  auto owner_of = [&](unsigned it) { return ((it + 1) * grid - 1) / total; };
+  // a share: its first tile and k block, then whole tiles
+  const int first_tile = static_cast<int>(it0 / kblocks);
+  const int first_kb = static_cast<int>(it0) - first_tile * kblocks;
+  const int share = static_cast<int>(it1 - it0);
 
   const uint32_t tmem_base = bars.tmem_base;
   const WaitCtl ctl{&bars.abort_flag, p.status, p.budget_ns};
@@ -209,37 +233,65 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const uint64_t w_policy = l2_policy_evict_first();   // the weight is streamed once
       int s = 0;
       uint32_t ph = 0, issued = 0, last_ph = 0;
-      bool ok = true;
-      for (long long it = it0; it < it1 && ok;) {
-        const int tile = static_cast<int>(it / kblocks);
-        const int kb0 = static_cast<int>(it - static_cast<long long>(tile) * kblocks);
-        const int kb1 = static_cast<int>(min(static_cast<long long>(kblocks), kb0 + (it1 - it)));
-        int wcol = tile * 128, wrow = 0;                    // kProj, kDown: this tile's columns
+      int tile = first_tile, kb = first_kb;
+      // what iteration (tile, kb) reads
+      int wcol, wrow, xrow, kk;
+      auto locate = [&]() {
+        wcol = tile * 128;                                  // kProj, kDown: this tile's columns
+        wrow = xrow = 0;
+        kk = kb;
         if (MODE == kUp) {
           wcol = tile % p.tiles * 256;                      // gate | up, 128 columns each
           wrow = bars.experts[tile / p.tiles] * p.wrows;
         }
-        int slot = MODE == kDown ? kb0 / p.kblocks : 0;
-        int kk = MODE == kDown ? kb0 - slot * p.kblocks : kb0;
-        if (MODE == kDown) wrow = bars.experts[slot] * p.wrows;
-        for (int kb = kb0; kb < kb1; ++kb) {
-          if (!mbar_wait(&bars.empty[s], ph ^ 1, ctl, kSiteProdEmpty)) { ok = false; break; }
-          mbar_arrive_expect_tx(&bars.full[s], C::X_BYTES + C::W_BYTES);
-          tma_load_2d(stage_x(s), &tmap_x, &bars.full[s], kk * BK, slot * MPAD);
-#pragma unroll
-          for (int bx = 0; bx < 2 * HALVES; ++bx)
-            tma_load_2d_hint(stage_w(s) + bx * W_BOX_BYTES, &tmap_w, &bars.full[s], wcol + bx * 64, wrow + kk * BK,
-                             w_policy);
-          issued |= 1u << s;
-          last_ph = (last_ph & ~(1u << s)) | (ph << s);
-          if (++s == STAGES) { s = 0; ph ^= 1; }
-          ++kk;
-          if (MODE == kDown && kk == p.kblocks && kb + 1 < kb1) {
-            kk = 0;
-            wrow = bars.experts[++slot] * p.wrows;
-          }
+        if (MODE == kDown) {
+          const int slot = kb / p.kblocks;
+          kk = kb - slot * p.kblocks;
+          xrow = slot * MPAD;
+          wrow = bars.experts[slot] * p.wrows;
         }
-        it += kb1 - kb0;
+      };
+      auto step = [&](bool more) {
+        ++kk;
+        if (++kb == kblocks) {
+          kb = 0;
+          ++tile;
+          if (more) locate();
+        } else if (MODE == kDown && kk == p.kblocks) {
+          if (more) locate();
+        }
+      };
+      auto load_w = [&](int st) {
+#pragma unroll
+        for (int bx = 0; bx < 2 * HALVES; ++bx)
+          tma_load_2d_hint(stage_w(st) + bx * W_BOX_BYTES, &tmap_w, &bars.full[st], wcol + bx * 64, wrow + kk * BK,
+                           w_policy);
+      };
+      int early = 0;                       // kDown: stages whose weights are on their way
+      if (MODE == kDown) {
+        early = min(share, STAGES);
+        if (share) locate();
+        for (int i = 0; i < early; ++i) {
+          mbar_arrive_expect_tx(&bars.full[i], C::X_BYTES + C::W_BYTES);
+          load_w(i);
+          step(i + 1 < early);
+        }
+        tile = first_tile;
+        kb = first_kb;
+        grid_dependency_wait();
+      }
+      if (share) locate();
+      for (int i = 0; i < share; ++i) {
+        if (i >= early) {
+          if (!mbar_wait(&bars.empty[s], ph ^ 1, ctl, kSiteProdEmpty)) break;
+          mbar_arrive_expect_tx(&bars.full[s], C::X_BYTES + C::W_BYTES);
+        }
+        tma_load_2d(stage_x(s), &tmap_x, &bars.full[s], kk * BK, xrow);
+        if (i >= early) load_w(s);
+        issued |= 1u << s;
+        last_ph = (last_ph & ~(1u << s)) | (ph << s);
+        if (++s == STAGES) { s = 0; ph ^= 1; }
+        step(i + 1 < share);
       }
       for (int i = 0; i < STAGES; ++i)
         if (issued & (1u << i)) drain_wait(&bars.full[i], (last_ph >> i) & 1u, p.budget_ns);
@@ -252,11 +304,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       int s = 0;
       uint32_t ph = 0;
       bool ok = true;
-      int seg = 0;
-      for (long long it = it0; it < it1 && ok; ++seg) {
-        const int tile = static_cast<int>(it / kblocks);
-        const int kb0 = static_cast<int>(it - static_cast<long long>(tile) * kblocks);
-        const int kb1 = static_cast<int>(min(static_cast<long long>(kblocks), kb0 + (it1 - it)));
+      int kb0 = first_kb, left = share;
+      for (int seg = 0; left > 0 && ok; ++seg) {
+        const int kb1 = min(kblocks, kb0 + left);
         const int b = seg & 1;
         const uint32_t aph = (seg >> 1) & 1;
         if (!mbar_wait(&bars.acc_empty[b], aph ^ 1, ctl, kSiteMmaAccEmpty)) break;
@@ -282,7 +332,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
         if (!ok) break;
         if (!(p.withhold && seg == 0)) umma_commit(&bars.acc_full[b]);
-        it += kb1 - kb0;
+        left -= kb1 - kb0;
+        kb0 = 0;
       }
       umma_commit(&bars.drain);
       drain_wait(&bars.drain, 0, p.budget_ns);
@@ -293,12 +344,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const int q = warp & 3;                       // TMEM lane quarter this warp may access
     const int n = q * 32 + lane;                  // column within the tile
     const int et = threadIdx.x - 64;              // 0..127
-    int seg = 0;
-    for (long long it = it0; it < it1; ++seg) {
-      const int tile = static_cast<int>(it / kblocks);
-      const int kb0 = static_cast<int>(it - static_cast<long long>(tile) * kblocks);
-      const int kb1 = static_cast<int>(min(static_cast<long long>(kblocks), kb0 + (it1 - it)));
-      it += kb1 - kb0;
+    if (MODE == kDown) {                          // also before this kernel's stores: partials, y
+      grid_dependency_wait();
+      grid_launch_dependents();
+    }
+    int next_tile = first_tile, next_kb = first_kb, left = share;
+    for (int seg = 0; left > 0; ++seg) {
+      const int tile = next_tile, kb0 = next_kb;
+      const int kb1 = min(kblocks, kb0 + left);
+      left -= kb1 - kb0;
+      ++next_tile;
+      next_kb = 0;
       const int b = seg & 1;
       const uint32_t aph = (seg >> 1) & 1;
       // One thread waits and the whole group follows its decision, so the
@@ -309,22 +365,26 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       tc_fence_after();
       // Chunks of 16 rows: the code of one chunk serves them all.
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + b * HALVES * MPAD;
-      auto finish = [&](int m0, float(&acc)[HALVES][RC]) {
+      float w[RC], r[RC];                         // kUp: routing weight and 1 / rms of the chunk's rows
+      auto route = [&](int m0) {
         if constexpr (MODE == kUp) {
-          // act = w silu(r gate) (r up), one round to bf16; 0 for rows that did not choose the expert
-          const int slot = tile / p.tiles;
-          const float* wt = p.route.weight + bars.experts[slot] * kMoeMaxRows + m0;
-          __nv_bfloat16* dst = p.act + (static_cast<int64_t>(slot) * MPAD + m0) * p.ncols + tile % p.tiles * 128 + n;
-          float w[RC], r[RC];
+          const float* wt = p.route.weight + bars.experts[tile / p.tiles] * kMoeMaxRows + m0;
 #pragma unroll
           for (int j = 0; j < RC; ++j) {
             w[j] = m0 + j < p.M ? __ldcg(wt + j) : 0.f;
             r[j] = m0 + j < p.M ? __ldcg(p.route.rinv + m0 + j) : 0.f;
           }
+        }
+      };
+      auto finish = [&](int m0, float(&acc)[HALVES][RC]) {
+        if constexpr (MODE == kUp) {
+          // act = w silu(r gate) (r up), one round to bf16; 0 for rows that did not choose the expert
+          __nv_bfloat16* dst =
+              p.act + (static_cast<int64_t>(tile / p.tiles) * MPAD + m0) * p.ncols + tile % p.tiles * 128 + n;
 #pragma unroll
           for (int j = 0; j < RC; ++j) {
             const float v = w[j] * (silu_f32(acc[0][j] * r[j]) * (acc[HALVES - 1][j] * r[j]));
-            dst[static_cast<int64_t>(j) * p.ncols] = __float2bfloat16_rn(w[j] != 0.f ? v : 0.f);
+            if (m0 + j < p.M) dst[static_cast<int64_t>(j) * p.ncols] = __float2bfloat16_rn(w[j] != 0.f ? v : 0.f);
           }
         } else {
           const int64_t col = static_cast<int64_t>(tile) * 128 + n;
@@ -334,19 +394,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       auto load = [&](int m0, float(&acc)[HALVES][RC]) {
         uint32_t raw[HALVES][RC];
 #pragma unroll
-        for (int h = 0; h < HALVES; ++h) tmem_ld16(taddr + h * MPAD + m0, raw[h]);
+        for (int h = 0; h < HALVES; ++h) tmem_ld8(taddr + h * MPAD + m0, raw[h]);
         tmem_ld_wait();
 #pragma unroll
         for (int h = 0; h < HALVES; ++h)
 #pragma unroll
           for (int j = 0; j < RC; ++j) acc[h][j] = __uint_as_float(raw[h][j]);
       };
-      // kUp stores the padding rows too (zeros, the next kernel's operand)
-      const int m_end = MODE == kUp ? MPAD : p.M;
       if (kb0 == 0 && kb1 == kblocks) {
 #pragma unroll 1
-        for (int m0 = 0; m0 < m_end; m0 += RC) {
+        for (int m0 = 0; m0 < p.M; m0 += RC) {
           float acc[HALVES][RC];
+          route(m0);
           load(m0, acc);
           finish(m0, acc);
         }
@@ -357,7 +416,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       // Shared tile: publish the partial (float4 groups [half][row / 4][column],
       // rows below M only), count, and go on unless this was the last one.
       {
-        const int slot = cta * 2 + (seg == 0 ? 0 : 1);
+        const int slot = static_cast<int>(cta) * 2 + (seg == 0 ? 0 : 1);
         float4* mine = reinterpret_cast<float4*>(p.part + static_cast<int64_t>(slot) * C::SLOT_FLOATS);
 #pragma unroll 1
         for (int m0 = 0; m0 < p.M; m0 += RC) {
@@ -374,8 +433,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       tc_fence_before();
       mbar_arrive(&bars.acc_empty[b]);
-      const long long t0 = static_cast<long long>(tile) * kblocks;
-      const int c_first = owner_of(t0), c_last = owner_of(t0 + kblocks - 1);
+      if (MODE == kProj && p.fixup) continue;
+      const unsigned t0 = static_cast<unsigned>(tile) * kblocks;
+      const int c_first = static_cast<int>(owner_of(t0)), c_last = static_cast<int>(owner_of(t0 + kblocks - 1));
+      route(0);
       __threadfence();
       named_bar_sync(1, 128);
       if (et == 0) {
@@ -386,42 +447,41 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       if (!bars.last) continue;
       // every partial of the tile is visible: add them in ascending k order
 #pragma unroll 1
-      for (int m0 = 0; m0 < m_end; m0 += RC) {
+      for (int m0 = 0; m0 < p.M; m0 += RC) {
         float acc[HALVES][RC];
+        if (m0) route(m0);
 #pragma unroll
         for (int h = 0; h < HALVES; ++h)
 #pragma unroll
           for (int j = 0; j < RC; ++j) acc[h][j] = 0.f;
         constexpr int GROUPS = HALVES * RC / 4;
         constexpr int CB = 16 / GROUPS;                          // contributors in flight
-        if (m0 < p.M) {
 #pragma unroll 1
-          for (int c0 = c_first; c0 <= c_last; c0 += CB) {
-            float4 v[CB][GROUPS];
+        for (int c0 = c_first; c0 <= c_last; c0 += CB) {
+          float4 v[CB][GROUPS];
 #pragma unroll
-            for (int j = 0; j < CB; ++j) {
-              const int c = min(c0 + j, c_last);
-              // a CTA's first segment is slot 0; this tile is not its first when its share begins before it
-              const int sl = c * 2 + (c * total / grid >= t0 ? 0 : 1);
-              const float4* src =
-                  reinterpret_cast<const float4*>(p.part + static_cast<int64_t>(sl) * C::SLOT_FLOATS) + m0 / 4 * 128 + n;
+          for (int j = 0; j < CB; ++j) {
+            const unsigned c = min(c0 + j, c_last);
+            // a CTA's first segment is slot 0; this tile is not its first when its share begins before it
+            const int sl = static_cast<int>(c) * 2 + (c * total / grid >= t0 ? 0 : 1);
+            const float4* src =
+                reinterpret_cast<const float4*>(p.part + static_cast<int64_t>(sl) * C::SLOT_FLOATS) + m0 / 4 * 128 + n;
 #pragma unroll
-              for (int g = 0; g < GROUPS; ++g) {
-                v[j][g] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (c0 + j <= c_last && m0 + 4 * (g % (RC / 4)) < p.M)
-                  v[j][g] = __ldcg(src + (g / (RC / 4) * (MPAD / 4) + g % (RC / 4)) * 128);
-              }
+            for (int g = 0; g < GROUPS; ++g) {
+              v[j][g] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (c0 + j <= c_last && m0 + 4 * (g % (RC / 4)) < p.M)
+                v[j][g] = __ldcg(src + (g / (RC / 4) * (MPAD / 4) + g % (RC / 4)) * 128);
             }
+          }
 #pragma unroll
-            for (int j = 0; j < CB; ++j) {
+          for (int j = 0; j < CB; ++j) {
 #pragma unroll
-              for (int g = 0; g < GROUPS; ++g) {
-                float* a = &acc[g / (RC / 4)][g % (RC / 4) * 4];
-                a[0] += v[j][g].x;
-                a[1] += v[j][g].y;
-                a[2] += v[j][g].z;
-                a[3] += v[j][g].w;
-              }
+            for (int g = 0; g < GROUPS; ++g) {
+              float* a = &acc[g / (RC / 4)][g % (RC / 4) * 4];
+              a[0] += v[j][g].x;
+              a[1] += v[j][g].y;
+              a[2] += v[j][g].z;
+              a[3] += v[j][g].w;
             }
           }
         }
@@ -443,11 +503,9 @@ cudaError_t launch(Params& p, const CUtensorMap& tx, const CUtensorMap& tw, int 
   constexpr size_t SMEM = smem_bytes<MPAD, HALVES>();
   const cudaError_t e = ensure_smem_limit<stream_kernel<MPAD, HALVES, MODE>>(static_cast<int>(SMEM));
   if (e != cudaSuccess) return e;
-  // the experts' space is at least tiles x kblocks (one expert): known to the kernel only
-  const long long total = static_cast<long long>(p.tiles) * p.kblocks;
   if (num_sms > kMaxCounters) num_sms = kMaxCounters;
-  const long long most = total < static_cast<long long>(p.tiles) * MAX_SHARE ? total : static_cast<long long>(p.tiles) * MAX_SHARE;
-  const unsigned grid = static_cast<unsigned>(MODE == kProj && most < num_sms ? most : num_sms);
+  // the experts' space is known to the kernel only
+  const unsigned grid = MODE == kProj ? share_count(p.tiles, p.kblocks, num_sms) : static_cast<unsigned>(num_sms);
   return launch_pdl(stream_kernel<MPAD, HALVES, MODE>, grid, NUM_THREADS, SMEM, stream, tx, tw, p);
 }
 
@@ -483,9 +541,30 @@ cudaError_t launch_proj_stream(const ProjArgs& a) {
   p.w_row_bytes = a.ldw * 2;
   p.prefetch_iters = a.prefetch_iters;
   p.epi = a.epi;
-  if (mp == 16) return strm::launch<16, 1, kProj>(p, tx, tw, a.num_sms, a.stream);
-  if (mp == 32) return strm::launch<32, 1, kProj>(p, tx, tw, a.num_sms, a.stream);
-  return strm::launch<64, 1, kProj>(p, tx, tw, a.num_sms, a.stream);
+  p.fixup = a.M > FIXUP_ROWS;
+  const cudaError_t e = mp == 16   ? strm::launch<16, 1, kProj>(p, tx, tw, a.num_sms, a.stream)
+                        : mp == 32 ? strm::launch<32, 1, kProj>(p, tx, tw, a.num_sms, a.stream)
+                                   : strm::launch<64, 1, kProj>(p, tx, tw, a.num_sms, a.stream);
+  if (e != cudaSuccess || !p.fixup) return e;
+  const int ctas = a.num_sms < kMaxCounters ? a.num_sms : kMaxCounters;
+  FixupArgs f = {};
+  f.sharers = static_cast<int>(share_count(p.tiles, p.kblocks, ctas));
+  if (f.sharers <= p.tiles && p.tiles % f.sharers == 0) return e;       // whole tiles only
+  f.part = p.part;
+  f.slot_floats = static_cast<int64_t>(mp) * 128;
+  f.total = static_cast<int64_t>(p.tiles) * p.kblocks;
+  f.kblocks = p.kblocks;
+  f.ranks = 1;
+  f.tile0 = 0;
+  f.tiles = p.tiles;
+  f.group_m = f.num_m = 1;
+  f.num_n = p.tiles;
+  f.rows = static_cast<int>((a.M + 3) / 4 * 4);
+  f.M = a.M;
+  f.N = a.N;
+  f.epi = a.epi;
+  f.stream = a.stream;
+  return launch_proj_fixup(f);
 }
 
 // ---------------------------------------------------------------------------

@@ -182,52 +182,81 @@ def _need(ok: bool, what: str) -> None:
         raise ValueError(what)
 
 
+# The checks below run on every call of a decode step: each is one condition,
+# and the message is put together only when it fails.
 def _rows(t: torch.Tensor, name: str, dtypes, shape=None) -> int:
     """Check a matrix with contiguous rows; returns its row stride."""
-    _need(t.dim() == 2 and t.dtype in dtypes, f"{name}: a matrix of {[str(d) for d in dtypes]} is needed")
-    _need(shape is None or tuple(t.shape) == tuple(shape), f"{name}: shape {tuple(t.shape)}, expected {shape}")
-    _need(t.stride(1) == 1 or t.shape[1] == 1, f"{name}: rows must be contiguous")
+    if t.dim() != 2 or t.dtype not in dtypes:
+        raise ValueError(f"{name}: a matrix of {[str(d) for d in dtypes]} is needed")
+    rows, cols = t.shape
+    if shape is not None and (rows, cols) != shape:
+        raise ValueError(f"{name}: shape {(rows, cols)}, expected {shape}")
+    ld, inner = t.stride()
+    if inner != 1 and cols != 1:
+        raise ValueError(f"{name}: rows must be contiguous")
     # a single row has no stride of its own; overlapping rows are refused by the library
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    return ld if rows > 1 else max(ld, cols)
 
 
 def _vec(t: Optional[torch.Tensor], name: str, dtype, n: int, dev) -> None:
-    if t is not None:
-        _need(t.dtype == dtype and t.shape == (n,) and t.is_contiguous() and t.device == dev,
-              f"{name}: a contiguous {dtype} vector of {n} on {dev} is needed")
+    if t is not None and (t.dtype != dtype or t.shape != (n,) or not t.is_contiguous() or t.device != dev):
+        raise ValueError(f"{name}: a contiguous {dtype} vector of {n} on {dev} is needed")
 
 
-class _on:
-    """Run on the device that holds the tensors, whatever the current one is,
-    and on `stream` (torch.cuda.Stream or a raw handle; the device's current
-    one by default): what is allocated or zeroed inside belongs to that
-    stream, as under torch.cuda.stream."""
+def _dense(t: Optional[torch.Tensor], name: str, dtype, shape, dev) -> None:
+    if t is not None and (t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != dev):
+        raise ValueError(f"{name}: contiguous {dtype} {shape} on {dev} is needed")
 
-    def __init__(self, dev: torch.device, stream):
-        _need(dev.type == "cuda", f"tensors on {dev}: a CUDA device is needed")
-        self.guard = torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else None
-        self.on = None
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
-        if stream is not None:
-            self.on = torch.cuda.stream(stream)
-        self.stream = torch.cuda.current_stream(dev) if stream is None else stream
+
+class _Here:
+    """The tensors' device is the current one and the stream its current one:
+    nothing to switch."""
 
     def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        if self.on is not None:
-            self.on.__enter__()
-        return self.stream
+        return None
 
     def __exit__(self, *exc):
-        if self.on is not None:
-            self.on.__exit__(*exc)
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+        return None
+
+
+_HERE = _Here()
+
+
+class _Elsewhere:
+    """Another device than the current one, or a stream of the caller's
+    (torch.cuda.Stream or a raw handle): what is allocated or zeroed inside
+    belongs to that stream, as under torch.cuda.stream."""
+
+    def __init__(self, dev: torch.device, stream):
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
+        self.parts = [torch.cuda.device(dev)] + ([torch.cuda.stream(stream)] if stream is not None else [])
+
+    def __enter__(self):
+        for part in self.parts:
+            part.__enter__()
+
+    def __exit__(self, *exc):
+        for part in reversed(self.parts):
+            part.__exit__(*exc)
+
+
+def _on(dev: torch.device, stream):
+    if dev.type != "cuda":
+        raise ValueError(f"tensors on {dev}: a CUDA device is needed")
+    if stream is None and dev.index == torch.cuda.current_device():
+        return _HERE
+    return _Elsewhere(dev, stream)
+
+
+def _handle(dev: torch.device) -> int:
+    """The device's current stream, without the Stream object around it."""
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 _ACT = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+_BF16 = (torch.bfloat16,)
+_BF16_FP32 = (torch.bfloat16, torch.float32)
 
 
 def proj(x: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None, act: str = "none",
@@ -236,32 +265,39 @@ def proj(x: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None, 
     """act(x @ W + bias) + residual (see fn_proj): x bf16 [M, K], W bf16 [K, N],
     bias fp32 [N]; the output is bf16 or fp32, the type of `out`, else
     `out_dtype`, else the residual's, else bf16.  `out` may be the residual."""
-    ldx = _rows(x, "x", (torch.bfloat16,))
+    ldx = _rows(x, "x", _BF16)
+    ldw = _rows(W, "W", _BF16)
     M, K = x.shape
-    _need(W.dim() == 2 and W.shape[0] == K, f"W: {K} rows are needed")
-    ldw = _rows(W, "W", (torch.bfloat16,))
-    N = W.shape[1]
+    KW, N = W.shape
     dev = x.device
-    _need(act in _ACT, f"act: one of {list(_ACT)}")
+    if KW != K:
+        raise ValueError(f"W: {K} rows are needed")
+    if act not in _ACT:
+        raise ValueError(f"act: one of {list(_ACT)}")
     _vec(bias, "bias", torch.float32, N, dev)
-    if out is None:
-        dt = out_dtype or (residual.dtype if residual is not None else torch.bfloat16)
-        with _on(dev, stream):
+    with _on(dev, stream):
+        if out is None:
+            dt = out_dtype or (residual.dtype if residual is not None else torch.bfloat16)
             out = torch.empty((M, N), dtype=dt, device=dev)
-    ldy = _rows(out, "out", (torch.bfloat16, torch.float32), (M, N))
-    ldr = 0 if residual is None else _rows(residual, "residual", (out.dtype,), (M, N))
-    _need(W.device == dev and out.device == dev and (residual is None or residual.device == dev),
-          f"every tensor must be on {dev}")
-    # a single row's stride is free: the library wants multiples of 8
-    ldx, ldw = (ldx + 7) // 8 * 8 if M <= 1 else ldx, (ldw + 7) // 8 * 8 if K == 1 else ldw
-    if out is residual:
-        ldr = ldy
-    with _on(dev, stream) as s:
+        ldy = _rows(out, "out", _BF16_FP32, (M, N))
+        if residual is None:
+            ldr = 0
+        elif residual is out:
+            ldr = ldy
+        else:
+            ldr = _rows(residual, "residual", (out.dtype,), (M, N))
+        if W.device != dev or out.device != dev or (residual is not None and residual.device != dev):
+            raise ValueError(f"every tensor must be on {dev}")
+        # a single row's stride is free: the library wants multiples of 8
+        if M <= 1:
+            ldx = (ldx + 7) // 8 * 8
+        if K == 1:
+            ldw = (ldw + 7) // 8 * 8
         if ws is None:
             ws = Workspace(dev)
         buf = ws.reserve(fn_workspace_size_proj(M, K, N))
         check(fn_proj(x, ldx, M, K, W, ldw, N, bias, _ACT[act], residual, ldr, _DTYPE[out.dtype], out, ldy, buf,
-                      buf.numel(), s), "fn_proj")
+                      buf.numel(), _handle(dev)), "fn_proj")
     return out
 
 
@@ -271,16 +307,17 @@ _SCORE = {"softmax": 0, "sigmoid": 1}
 def fold_experts(W_gate: torch.Tensor, g: torch.Tensor, W_up: torch.Tensor, stream=None) -> torch.Tensor:
     """Fold the norm gain into every expert's gate and up weights [E, d, I]:
     bf16 [E, d, 2I], per expert the interleaved layout of `fold`."""
+    _need(W_gate.dim() == 3, "W_gate [E, d, I] is needed")
     E, d, N = W_gate.shape
     dev = W_gate.device
-    for t, n in ((W_gate, "W_gate"), (W_up, "W_up")):
-        _need(t.dtype == torch.bfloat16 and tuple(t.shape) == (E, d, N) and t.is_contiguous() and t.device == dev,
-              f"{n}: contiguous bf16 {(E, d, N)} on {dev} is needed")
+    _dense(W_gate, "W_gate", torch.bfloat16, (E, d, N), dev)
+    _dense(W_up, "W_up", torch.bfloat16, (E, d, N), dev)
     _vec(g, "g", torch.float32, d, dev)
-    with _on(dev, stream) as s:
+    with _on(dev, stream):
         out = torch.empty((E, d, 2 * N), dtype=torch.bfloat16, device=dev)
         for e in range(E):
-            check(fn_fold_weights(W_gate[e], W_up[e], g, d, N, FN_W_BF16, out[e], None, s), "fn_fold_weights")
+            check(fn_fold_weights(W_gate[e], W_up[e], g, d, N, FN_W_BF16, out[e], None, _handle(dev)),
+                  "fn_fold_weights")
     return out
 
 
@@ -293,28 +330,33 @@ def moe_swiglu(x: torch.Tensor, g: Optional[torch.Tensor], router: torch.Tensor,
     (y bf16 [M, d], expert ids int32 [M, top_k], routing weights fp32 [M, top_k]).
     Wgu [E, d, 2I] from `fold_experts`; `out` may be x or the residual."""
     dev = x.device
-    _need(x.dim() == 2 and Wgu.dim() == 3 and Wd.dim() == 3, "x [M, d], Wgu [E, d, 2I], Wd [E, I, d] are needed")
+    if x.dim() != 2 or Wd.dim() != 3:
+        raise ValueError("x [M, d], Wgu [E, d, 2I], Wd [E, I, d] are needed")
     M, d = x.shape
-    E, I = Wd.shape[0], Wd.shape[1]
-    _need(score in _SCORE, f"score: one of {list(_SCORE)}")
-    _need(isinstance(top_k, int) and 0 < top_k <= E, f"top_k: 1..{E}")
-    if out is None:
-        with _on(dev, stream):
-            out = torch.empty((M, d), dtype=torch.bfloat16, device=dev)
-    for t, n, shape in ((x, "x", (M, d)), (router, "router", (E, d)), (Wgu, "Wgu", (E, d, 2 * I)),
-                        (Wd, "Wd", (E, I, d)), (residual, "residual", (M, d)), (out, "out", (M, d))):
-        _need(t is None or (t.dtype == torch.bfloat16 and tuple(t.shape) == shape and t.is_contiguous()
-                            and t.device == dev), f"{n}: contiguous bf16 {shape} on {dev} is needed")
+    E, I, _ = Wd.shape
+    if score not in _SCORE:
+        raise ValueError(f"score: one of {list(_SCORE)}")
+    if not 0 < top_k <= E:
+        raise ValueError(f"top_k: 1..{E}")
+    bf = torch.bfloat16
+    _dense(x, "x", bf, (M, d), dev)
+    _dense(router, "router", bf, (E, d), dev)
+    _dense(Wgu, "Wgu", bf, (E, d, 2 * I), dev)
+    _dense(Wd, "Wd", bf, (E, I, d), dev)
+    _dense(residual, "residual", bf, (M, d), dev)
+    _dense(out, "out", bf, (M, d), dev)
     _vec(g, "g", torch.float32, d, dev)
     _vec(select_bias, "select_bias", torch.float32, E, dev)
-    with _on(dev, stream) as s:
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((M, d), dtype=bf, device=dev)
         ids = torch.empty((M, top_k), dtype=torch.int32, device=dev)
         w = torch.empty((M, top_k), dtype=torch.float32, device=dev)
         if ws is None:
             ws = Workspace(dev)
         buf = ws.reserve(fn_workspace_size_moe(M, d, I, E, top_k))
         check(fn_moe_swiglu(x, M, d, g, router, E, Wgu, Wd, I, top_k, _SCORE[score], select_bias, renorm, route_scale,
-                            eps, residual, out, ids, w, buf, buf.numel(), s), "fn_moe_swiglu")
+                            eps, residual, out, ids, w, buf, buf.numel(), _handle(dev)), "fn_moe_swiglu")
     return out, ids, w
 
 
@@ -335,22 +377,21 @@ def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None,
     M, V = logits.shape
     dev = logits.device
     _vec(targets, "targets", torch.int32, M, dev)
-    if out is None:
-        with _on(dev, stream):
-            f = torch.empty((3, M), dtype=torch.float32, device=dev)
-            out = TokenLogprobs(f[0] if targets is not None else None, f[1], f[2],
+    with _on(dev, stream):
+        if out is None:
+            lp, ent, lse = torch.empty((3, M), dtype=torch.float32, device=dev).unbind()
+            out = TokenLogprobs(lp if targets is not None else None, ent, lse,
                                 torch.empty((M, top_k), dtype=torch.int32, device=dev),
                                 torch.empty((M, top_k), dtype=torch.float32, device=dev))
-    else:
-        for t, n in ((out.logprob, "logprob"), (out.entropy, "entropy"), (out.lse, "lse")):
-            _vec(t, n, torch.float32, M, dev)
-        for t, d in ((out.top_ids, torch.int32), (out.top_logprobs, torch.float32)):
-            _need(t.dtype == d and t.shape == (M, top_k) and t.is_contiguous() and t.device == dev,
-                  f"top alternatives: contiguous [{M}, {top_k}] outputs on {dev} are needed")
-    with _on(dev, stream) as s:
+        else:
+            _vec(out.logprob, "logprob", torch.float32, M, dev)
+            _vec(out.entropy, "entropy", torch.float32, M, dev)
+            _vec(out.lse, "lse", torch.float32, M, dev)
+            _dense(out.top_ids, "top_ids", torch.int32, (M, top_k), dev)
+            _dense(out.top_logprobs, "top_logprobs", torch.float32, (M, top_k), dev)
         check(fn_token_logprobs(logits, _DTYPE[logits.dtype], M, V, ld, targets, scale, top_k, out.logprob,
                                 out.entropy, out.lse, out.top_ids if top_k else None,
-                                out.top_logprobs if top_k else None, s), "fn_token_logprobs")
+                                out.top_logprobs if top_k else None, _handle(dev)), "fn_token_logprobs")
     return out
 
 
@@ -364,14 +405,16 @@ def token_logprobs_backward(logits: torch.Tensor, targets: Optional[torch.Tensor
     M, V = logits.shape
     dev = logits.device
     _vec(targets, "targets", torch.int32, M, dev)
-    for t, n in ((lse, "lse"), (entropy, "entropy"), (grad_logprob, "grad_logprob"), (grad_entropy, "grad_entropy")):
-        _vec(t, n, torch.float32, M, dev)
-    if out is None:
-        with _on(dev, stream):
+    _vec(lse, "lse", torch.float32, M, dev)
+    _vec(entropy, "entropy", torch.float32, M, dev)
+    _vec(grad_logprob, "grad_logprob", torch.float32, M, dev)
+    _vec(grad_entropy, "grad_entropy", torch.float32, M, dev)
+    with _on(dev, stream):
+        if out is None:
             out = torch.empty((M, V), dtype=logits.dtype, device=dev)
-    ldd = _rows(out, "out", (logits.dtype,), (M, V))
-    _need(out.device == dev, f"out on {out.device}, logits on {dev}")
-    with _on(dev, stream) as s:
+        ldd = _rows(out, "out", (logits.dtype,), (M, V))
+        if out.device != dev:
+            raise ValueError(f"out on {out.device}, logits on {dev}")
         check(fn_token_logprobs_backward(logits, _DTYPE[logits.dtype], M, V, ld, targets, lse, entropy, grad_logprob,
-                                         grad_entropy, scale, out, ldd, s), "fn_token_logprobs_backward")
+                                         grad_entropy, scale, out, ldd, _handle(dev)), "fn_token_logprobs_backward")
     return out
