@@ -598,7 +598,7 @@ fn_status fn_moe_swiglu(const void* x, int64_t M, int64_t d, const float* g, con
   if (M > kMoeMaxRows || E > kMoeMaxExperts || top_k > kMoeMaxTopK || d % 64 != 0 || I % 128 != 0)
     return FN_ERR_UNSUPPORTED_SHAPE;
   if (d > kMaxProjDim || I > kMaxProjDim / 2 || E * d > kMaxDim || E * I > kMaxDim) return FN_ERR_UNSUPPORTED_SHAPE;
-  if (E * (I / 128) * (d / 64) > kMaxDim / 128) return FN_ERR_UNSUPPORTED_SHAPE;   // iterations, as in fn_proj
+  if (E * (I / 64) * (d / 64) > kMaxDim / 128) return FN_ERR_UNSUPPORTED_SHAPE;   // iterations, as in fn_proj
   if (M == 0) return FN_OK;
   if (!x || !router || !Wgu || !Wd || !y) return FN_ERR_INVALID_ARG;
   if (!workspace) return FN_ERR_WORKSPACE;

@@ -18,12 +18,16 @@ constexpr int kCounterOffset = 16;
 constexpr int kMaxCounters = static_cast<int>(kWsHeaderBytes) - kCounterOffset;
 
 // Count this CTA's partial; true for the last of `n` (which resets the byte).
-// Thread-level: the caller orders the partial's stores before and the others'
-// loads after (__threadfence on both sides).
+// One thread calls it behind a barrier that follows all of the CTA's stores,
+// and a barrier follows before the others' partials are read: the acquire and
+// release of the atomic carry what the barriers have ordered.
 __device__ __forceinline__ bool count_partial(unsigned int* header, int index, int n) {
   unsigned int* word = header + (kCounterOffset + index) / 4;
   const int shift = (index & 3) * 8;
-  const bool last = ((atomicAdd(word, 1u << shift) >> shift) & 0xFFu) == static_cast<unsigned int>(n - 1);
+  unsigned int old;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;"
+               : "=r"(old) : "l"(word), "r"(1u << shift) : "memory");
+  const bool last = ((old >> shift) & 0xFFu) == static_cast<unsigned int>(n - 1);
   if (last) atomicSub(word, static_cast<unsigned int>(n) << shift);
   return last;
 }
