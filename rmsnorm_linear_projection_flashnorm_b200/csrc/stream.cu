@@ -72,7 +72,7 @@ template <int MPAD, int HALVES, int MODE>
 struct Cfg {
   // The expert kernels up to 32 rows leave room for a second CTA on the SM: the
   // next kernel's, which starts on its weights while this one drains.
-  static constexpr int SMEM_BUDGET = MODE != kProj && MPAD <= 32 ? 104 * 1024 : 200 * 1024;
+  static constexpr int SMEM_BUDGET = (MODE == kProj || MPAD > 32 ? 200 : MODE == kUp ? 104 : 112) * 1024;
   static constexpr int W_BYTES = HALVES * 2 * W_BOX_BYTES;
   static constexpr int X_BYTES = MPAD * BK * 2;
   static constexpr int STAGE_BYTES = W_BYTES + X_BYTES;
@@ -83,14 +83,14 @@ struct Cfg {
   static constexpr int SLOT_FLOATS = HALVES * MPAD * 128;
 };
 
-template <int STAGES>
+template <int STAGES, bool SWAP>
 struct alignas(16) Bars {
   uint64_t full[STAGES], empty[STAGES];
   uint64_t acc_full[2], acc_empty[2];
   uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
-  float swap[2][2][RC / 2 * 64];   // kUp: rows passed between the gate and the up threads
+  float swap[SWAP ? 2 : 1][2][SWAP ? RC / 2 * 64 : 1];   // kUp: rows passed between the gate and the up threads
   int epi_ok[2];
   int last;                        // the count of the tile's contributors is complete
   int n_active;
@@ -101,10 +101,13 @@ struct alignas(16) Bars {
 template <int MPAD, int HALVES, int MODE>
 constexpr size_t smem_bytes() {
   using C = Cfg<MPAD, HALVES, MODE>;
-  return 1024 + C::STAGES * C::STAGE_BYTES + sizeof(Bars<C::STAGES>);
+  return 1024 + C::STAGES * C::STAGE_BYTES + sizeof(Bars<C::STAGES, MODE == kUp && HALVES == 1>);
 }
 static_assert(smem_bytes<16, 1, kProj>() <= 232448 && smem_bytes<64, 2, kUp>() <= 232448, "shared memory budget");
-static_assert(2 * (smem_bytes<32, 2, kUp>() + 1024) <= 233472, "two CTAs to an SM");
+static_assert(smem_bytes<32, 2, kUp>() + smem_bytes<32, 1, kDown>() + 2048 <= 233472 &&
+                  smem_bytes<16, 2, kUp>() + smem_bytes<16, 1, kDown>() + 2048 <= 233472 &&
+                  smem_bytes<16, 1, kUp>() + smem_bytes<16, 1, kDown>() + 2048 <= 233472,
+              "two CTAs to an SM");
 
 // CTAs that take a share of tiles x kblocks iterations: all of them, but no
 // more than MAX_SHARE to a tile; or a whole number per tile where that costs
@@ -135,7 +138,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   constexpr int STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  Bars<STAGES>& bars = *reinterpret_cast<Bars<STAGES>*>(smem + STAGES * C::STAGE_BYTES);
+  using Shared = Bars<STAGES, MODE == kUp && HALVES == 1>;
+  Shared& bars = *reinterpret_cast<Shared*>(smem + STAGES * C::STAGE_BYTES);
   auto stage_w = [&](int s) { return smem + s * C::STAGE_BYTES; };
   auto stage_x = [&](int s) { return smem + s * C::STAGE_BYTES + C::W_BYTES; };
   const int warp = threadIdx.x >> 5;
