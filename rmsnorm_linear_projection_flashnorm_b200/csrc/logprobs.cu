@@ -6,23 +6,31 @@
 //   lse = m + ln s,  logprob = d_target - ln s,  entropy = ln s - t / s
 // all from ONE pass over the logits with running (m, s, t): when the maximum
 // grows by D the sums become s' = s e^{-D}, t' = e^{-D} (t - s D).  The
-// products run in the base-2 exponent domain (d log2 e), 32-bit floats.
+// products run in the base-2 exponent domain, c = scale log2 e, 32-bit floats:
+// d = fma(x, c, -mu) with mu = m c rounded, one instruction for a pair, and the
+// rounding of mu (known exactly, fma(m, c, -mu)) taken out at the end.
 //
 // The pass is bound by HBM (2 or 4 bytes per logit, read once).  The SM side
-// stays below it: about 6 issue slots and one ex2 per 16-bit logit, packed
-// fp32 pairs where the arithmetic allows.
+// stays below it: per pair of 16-bit logits two ex2 and about 8 issue slots.
+// Every thread copies the vectors that it will read itself to shared memory
+// two tiles ahead (cp.async), so loads are in flight while it computes and the
+// main loop has no barrier.
 //
 // Top alternatives in the same pass: a logit becomes a 64-bit key, its ordered
 // bit pattern above the complement of its index, so keys are unique, ties go
-// to the lower index and the order of arrival does not matter.  A threshold
-// key, never above the true k-th largest, filters the stream: one comparison
-// per 16-byte vector.  The first tile sets it from the threads' own maxima
-// (the k-th largest of 256 disjoint groups' maxima is a lower bound of the
-// k-th largest element, and at most k groups hold anything above it, which
-// bounds the survivors by k * 32); survivors go to a small buffer that is
-// reduced to its top k by warp bitonic sorts when it fills.  Rows that grow
-// steadily overflow the buffer in a tile; that tile is filtered again under a
-// threshold from its own maxima, so the buffer bound always holds.
+// to the lower index and the order of arrival does not matter.  Each warp
+// keeps its 32 largest keys, sorted, one per lane.  A threshold key, never
+// above the true k-th largest, filters the stream: one comparison per 32
+// logits of a thread.  It is the largest of
+//   the warps' own k-th keys;
+//   the smallest of the warps' (k / 8, rounded up)-th values: 8 warps hold that
+//     many each, so k logits are not below it;
+//   where many lanes hold survivors at once (a row's first tile, rows that grow
+//     steadily), the k-th largest of the lanes' maxima.
+// What a warp does per survivor decides the speed (at 8 alternatives of 131072
+// logits, 130 instructions each doubled the kernel's time), so vectors with a
+// survivor are only queued; 32 of them at a time give up their keys, which are
+// sorted and merged into the list.
 //
 // Work split: one thread-block cluster per row; C = 1, 2, 4 or 8 CTAs, more
 // when there are few rows, so one decoded token still uses 8 SMs.  The CTAs'
@@ -42,8 +50,10 @@ constexpr int THREADS = 256;
 constexpr int WARPS = THREADS / 32;
 constexpr int VECS = 4;                       // 16-byte vectors per thread and tile
 constexpr int MAX_K = kMaxTopAlternatives;    // 32: one key per lane
-constexpr int SOFT = 256;                     // survivors kept before they are reduced
-constexpr int CAP = 1024 + SOFT;              // k * 32 elements of one tile + what was kept
+constexpr int STAGES = 2;                     // tiles in flight
+constexpr int TILE = THREADS * VECS;          // 16-byte vectors
+constexpr int CROWD = 12;                     // lanes with survivors from which the threshold is raised first
+constexpr float FAR = -200.f;                 // 2^FAR is 0 in fp32: nothing below it counts
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 static_assert(MAX_K == 32, "one list entry per lane");
@@ -81,6 +91,17 @@ struct Elem<__nv_bfloat16> {
       f[2 * i + 1] = bf16hi_to_f32(w[i]);
     }
   }
+  // Largest pair of values not above f, and both halves of a word kept from below it.
+  static __device__ __forceinline__ bool floor_word(float f, uint32_t& w) {
+    const __nv_bfloat16 h = __float2bfloat16_rd(f);
+    const uint32_t u = __bfloat16_as_ushort(h);
+    w = u | u << 16;
+    return isfinite(__bfloat162float(h));
+  }
+  static __device__ __forceinline__ uint32_t clamp(uint32_t v, uint32_t w) {
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(v) : "r"(v), "r"(w));
+    return v;
+  }
   static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
     return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
                       pack_bf16x2(f[6], f[7]));
@@ -108,6 +129,16 @@ struct Elem<__half> {
       f[2 * i + 1] = p.y;
     }
   }
+  static __device__ __forceinline__ bool floor_word(float f, uint32_t& w) {
+    const __half h = __float2half_rd(f);
+    const uint32_t u = __half_as_ushort(h);
+    w = u | u << 16;
+    return isfinite(__half2float(h));
+  }
+  static __device__ __forceinline__ uint32_t clamp(uint32_t v, uint32_t w) {
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(v) : "r"(v), "r"(w));
+    return v;
+  }
   static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
     uint32_t w[4];
 #pragma unroll
@@ -133,6 +164,13 @@ struct Elem<float> {
     f[2] = __uint_as_float(v.z);
     f[3] = __uint_as_float(v.w);
   }
+  static __device__ __forceinline__ bool floor_word(float f, uint32_t& w) {
+    w = __float_as_uint(f);
+    return isfinite(f);
+  }
+  static __device__ __forceinline__ uint32_t clamp(uint32_t v, uint32_t w) {
+    return __float_as_uint(max_nan(__uint_as_float(v), __uint_as_float(w)));
+  }
   static __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
     return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
   }
@@ -145,12 +183,14 @@ struct Elem<float> {
 // ---------------------------------------------------------------------------
 using Key = unsigned long long;
 
-__device__ __forceinline__ Key make_key(float v, uint32_t idx) {
+__device__ __forceinline__ uint32_t ordered(float v) {
   v += 0.0f;                                        // -0 ties with +0
   const uint32_t u = __float_as_uint(v);
-  uint32_t o = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-  if (v != v) o = 0xFFFFFFFFu;                      // NaN ranks first
-  return (static_cast<Key>(o) << 32) | (0xFFFFFFFFu - idx);
+  if (v != v) return 0xFFFFFFFFu;                   // NaN ranks first
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ Key make_key(float v, uint32_t idx) {
+  return (static_cast<Key>(ordered(v)) << 32) | (0xFFFFFFFFu - idx);
 }
 __device__ __forceinline__ float key_value(Key k) {
   const uint32_t o = static_cast<uint32_t>(k >> 32);
@@ -163,12 +203,14 @@ __device__ __forceinline__ int key_index(Key k) {
 
 // One step of a bitonic network over the lanes: keep the larger key where
 // `keep_max`, else the smaller.
-__device__ __forceinline__ Key cmp_xchg(Key k, int mask, bool keep_max) {
-  const Key o = __shfl_xor_sync(0xffffffffu, k, mask);
+template <typename K>
+__device__ __forceinline__ K cmp_xchg(K k, int mask, bool keep_max) {
+  const K o = __shfl_xor_sync(0xffffffffu, k, mask);
   return (k > o) == keep_max ? k : o;
 }
 // Sort 32 keys over the lanes, largest in lane 0.
-__device__ __forceinline__ Key warp_sort(Key k, int lane) {
+template <typename K>
+__device__ __forceinline__ K warp_sort(K k, int lane) {
 #pragma unroll
   for (int size = 2; size <= 32; size <<= 1) {
 #pragma unroll
@@ -190,13 +232,21 @@ __device__ __forceinline__ Key warp_merge(Key a, Key b, int lane) {
 }
 
 struct Stat {
-  float m, s, t;   // maximum (raw logits), sum of 2^d, sum of d 2^d, d = (x - m) c
+  float m, s, t;   // maximum (raw logits), sum of 2^d, sum of d 2^d
 };
+// The reference of d for maximum m: d = fma(x, c, -mu) where mu = m c is of
+// ordinary size, else d = (x - m) c (a maximum near the type's lowest value,
+// or infinite).
+constexpr float ORDINARY = 1e30f;
+__device__ __forceinline__ float distance(float a, float b, float c) {   // of a's reference below b's, >= FAR
+  if (a == b) return 0.f;
+  const float mu = __fmul_rn(b, c);
+  return max_nan(fabsf(mu) < ORDINARY ? __fsub_rn(__fmul_rn(a, c), mu) : (a - b) * c, FAR);
+}
 __device__ __forceinline__ Stat merge_stat(const Stat& a, const Stat& b, float c) {
   Stat r;
   r.m = max_nan(a.m, b.m);
-  const float da = a.m == r.m ? 0.f : max_nan((a.m - r.m) * c, -200.f);
-  const float db = b.m == r.m ? 0.f : max_nan((b.m - r.m) * c, -200.f);
+  const float da = distance(a.m, r.m, c), db = distance(b.m, r.m, c);
   const float fa = ex2(da), fb = ex2(db);
   r.s = fa * a.s + fb * b.s;
   r.t = fa * fmaf(a.s, da, a.t) + fb * fmaf(b.s, db, b.t);
@@ -204,34 +254,32 @@ __device__ __forceinline__ Stat merge_stat(const Stat& a, const Stat& b, float c
 }
 
 struct Smem {
-  Key buf[CAP];
-  Key lists[WARPS][32];
-  Key top[32];          // this CTA's result, read by rank 0 of the cluster
+  uint4 stage[STAGES][TILE];
+  uint4 queue[WARPS][64];        // vectors with survivors
+  Key buf[WARPS][64];            // survivors; at the end the warps' lists
+  int queue_at[WARPS][64];       // their first logit
+  Key top[32];                   // this CTA's result, read by rank 0 of the cluster
+  Key thr;                       // largest of the warps' k-th keys
+  uint32_t share[WARPS];         // the warps' (k / WARPS, rounded up)-th ordered values
   Stat wstat[WARPS];
   Stat stat;            // this CTA's (m, s, t), read by rank 0
-  int count;
 };
 
-// Reduce n keys (shared memory, or one per thread when buf is null) to the 32
-// largest, sorted, in sm.top.  All threads call; ends with a barrier.
-__device__ __forceinline__ void block_top32(Smem& sm, const Key* buf, int n, Key own, int warp, int lane) {
-  Key best;
-  if (buf) {
-    best = 0;
-    for (int i = warp * 32; i < n; i += THREADS) {
-      const Key k = warp_sort(i + lane < n ? buf[i + lane] : 0, lane);
-      best = i < THREADS ? k : warp_merge(best, k, lane);
-    }
-  } else {
-    best = warp_sort(own, lane);
-  }
-  sm.lists[warp][lane] = best;
+__device__ __forceinline__ void copy_async(uint4* dst, const uint4* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
+// Merge the warps' sorted lists (the first `n` of them) into sm.top.  All
+// threads call; ends with a barrier.
+__device__ __forceinline__ void merge_lists(Smem& sm, Key best, int n, int warp, int lane) {
+  __syncwarp();
+  sm.buf[warp][lane] = best;
 #pragma unroll
   for (int w = WARPS / 2; w > 0; w >>= 1) {
     __syncthreads();
-    if (warp < w) {
-      best = warp_merge(best, sm.lists[warp + w][lane], lane);
-      sm.lists[warp][lane] = best;
+    if (warp < w && warp + w < n) {
+      best = warp_merge(best, sm.buf[warp + w][lane], lane);
+      sm.buf[warp][lane] = best;
     }
   }
   if (warp == 0) sm.top[lane] = best;
@@ -254,10 +302,12 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const Params p) {
   constexpr int N = E::N;
   __shared__ Smem sm;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = blockIdx.x % p.C;
+  const int rank = static_cast<int>(blockIdx.x % p.C);
   const int64_t row = blockIdx.x / p.C;
   const T* x = static_cast<const T*>(p.logits) + row * p.ld;
   const float c = p.scale * LOG2E;
+  if (TOPK && threadIdx.x < WARPS) sm.share[threadIdx.x] = 0;
+  if (TOPK && threadIdx.x == 0) sm.thr = 0;
   grid_dependency_wait();
   grid_launch_dependents();
 
@@ -272,137 +322,209 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const Params p) {
   const int v1 = static_cast<int>(static_cast<int64_t>(nv) * (rank + 1) / p.C);
   const uint4* xv = reinterpret_cast<const uint4*>(x + head);
 
-  Stat st{-INFINITY, 0.f, 0.f};
-  float thr_v = -INFINITY;
-  Key thr = 0;
-
-  const int nscal = rank == 0 ? head + p.V - tail0 : 0;
-  if (rank == 0) {
-    if (static_cast<int>(threadIdx.x) < nscal) {
-      const int i = static_cast<int>(threadIdx.x);
-      const int idx = i < head ? i : tail0 + i - head;
-      const float v = E::load(x + idx);
-      st.m = v;
-      st.s = v == -INFINITY ? 0.f : (isinf(v) ? NAN : v - v + 1.f);   // NaN for NaN and +inf
-      if (TOPK) sm.buf[i] = make_key(v, idx);
-    }
-  }
-  if (TOPK && threadIdx.x == 0) sm.count = nscal;
-
-  bool first = true;
-  int kept = nscal;                            // keys in the buffer, the same in every thread
-  for (int base = v0; base < v1; base += THREADS * VECS) {
-    uint4 q[VECS];
-    bool have[VECS];
+  auto fetch = [&](int base, int s) {         // this thread's vectors of a tile
 #pragma unroll
     for (int j = 0; j < VECS; ++j) {
       const int i = base + j * THREADS + static_cast<int>(threadIdx.x);
-      have[j] = i < v1;
-      if (have[j]) q[j] = __ldcs(xv + i);
+      if (i < v1) copy_async(&sm.stage[s][j * THREADS + threadIdx.x], xv + i);
     }
-    float vm[VECS];
-    float bm = -INFINITY;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int s = 0; s < STAGES; ++s) fetch(v0 + s * TILE, s);
+  if (TOPK) __syncthreads();                  // sm.thr is set
+
+  Stat st{-INFINITY, 0.f, 0.f};
+  // top alternatives of this warp
+  Key best = 0, thr = 0;
+  float thr_v = -INFINITY;                    // keys above thr: values above thr_v, or equal
+  uint32_t thr_i = 0xFFFFFFFFu;               // to it with an index up to thr_i
+  int pending = 0, queued = 0;
+  const int part = (p.k + WARPS - 1) / WARPS;
+  auto raise = [&](Key t) {
+    if (t > thr) {
+      thr = t;
+      thr_v = key_value(t + 1);
+      thr_i = 0xFFFFFFFFu - static_cast<uint32_t>(t + 1);
+    }
+  };
+  auto flush = [&]() {                        // the first 32 survivors into the list
+    __syncwarp();
+    best = warp_merge(best, warp_sort(lane < pending ? sm.buf[warp][lane] : 0, lane), lane);
+    const Key rest = sm.buf[warp][32 + lane];
+    __syncwarp();
+    pending = max(pending - 32, 0);
+    if (lane < pending) sm.buf[warp][lane] = rest;
+    const Key kth = __shfl_sync(0xffffffffu, best, p.k - 1);
+    const uint32_t val = static_cast<uint32_t>(__shfl_sync(0xffffffffu, best, part - 1) >> 32);
+    if (lane == 0) {
+      if (kth > thr) atomicMax(&sm.thr, kth);
+      if (val > sm.share[warp]) sm.share[warp] = val;
+    }
+    raise(kth);
+  };
+  auto append = [&](bool on, Key k) {
+    const uint32_t b = __ballot_sync(0xffffffffu, on);
+    if (on) sm.buf[warp][pending + __popc(b & ((1u << lane) - 1u))] = k;
+    pending += __popc(b);
+    if (pending >= 32) flush();
+  };
+  auto process = [&]() {                      // the first 32 vectors of the queue
+    __syncwarp();
+    uint32_t mask = 0;
+    float f[N];
+    int at = 0;
+    if (lane < queued) {
+      E::unpack(sm.queue[warp][lane], f);
+      at = sm.queue_at[warp][lane];
+#pragma unroll
+      for (int e = 0; e < N; ++e) mask |= !(f[e] < thr_v) ? 1u << e : 0u;
+    }
+    while (__any_sync(0xffffffffu, mask != 0)) {
+      const int e = __ffs(static_cast<int>(mask)) - 1;      // the lane's next candidate
+      float fe = f[0];
+#pragma unroll
+      for (int i = 1; i < N; ++i) fe = e == i ? f[i] : fe;
+      const Key k = make_key(fe, static_cast<uint32_t>(at + e));
+      append(mask != 0 && k > thr, k);
+      mask &= mask - 1;
+    }
+    if (pending > 0) flush();
+    if (lane + 32 < queued) {
+      const uint4 v = sm.queue[warp][32 + lane];
+      sm.queue[warp][lane] = v;
+      sm.queue_at[warp][lane] = sm.queue_at[warp][32 + lane];
+    }
+    queued = max(queued - 32, 0);
+    __syncwarp();
+  };
+
+  if (rank == 0 && warp == 0) {
+    const int nscal = head + p.V - tail0;
+    const int idx = lane < head ? lane : tail0 + lane - head;
+    const bool on = lane < nscal;
+    float v = 0.f;
+    if (on) {
+      v = E::load(x + idx);
+      st.m = v;
+      st.s = v == -INFINITY ? 0.f : (isinf(v) ? NAN : v - v + 1.f);   // NaN for NaN and +inf
+      const float mu = __fmul_rn(v, c);
+      if (fabsf(mu) < ORDINARY) {                                    // d = fma(v, c, -mu): mu's rounding
+        const float d = fmaf(v, c, -mu);
+        st.s = ex2(d);
+        st.t = d * st.s;
+      }
+    }
+    if (TOPK) append(on, make_key(v, idx));
+  }
+
+  for (int base = v0, s = 0; base < v1; base += TILE, s ^= 1) {
+    uint4 q[VECS];
+    int have = 0;                             // of this thread's vectors, the first so many
+    asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
 #pragma unroll
     for (int j = 0; j < VECS; ++j) {
-      vm[j] = have[j] ? E::vmax(q[j]) : -INFINITY;
+      if (base + j * THREADS + static_cast<int>(threadIdx.x) < v1) {
+        q[j] = sm.stage[s][j * THREADS + threadIdx.x];
+        have = j + 1;
+      }
+    }
+    float bm = -INFINITY;
+    float vm[VECS];
+#pragma unroll
+    for (int j = 0; j < VECS; ++j) {
+      vm[j] = j < have ? E::vmax(q[j]) : -INFINITY;
       bm = max_nan(bm, vm[j]);
     }
+    fetch(base + STAGES * TILE, s);           // the slot's vectors are in registers
     // running softmax statistics
-    if (!(bm <= st.m)) {                       // grows, or NaN
+    if (!(bm <= st.m)) {                      // grows, or NaN
       if (st.s > 0.f) {
-        const float D = max_nan((st.m - bm) * c, -200.f);
+        const float D = distance(st.m, bm, c);
         const float f = ex2(D);
         st.t = f * fmaf(st.s, D, st.t);
         st.s *= f;
       }
-      st.m = bm;
+      st.m = max_nan(st.m, bm);               // NaN stays
     }
-    const float mu = st.m == -INFINITY ? 0.f : st.m;
-    const uint64_t nm2 = f2_pack(-mu, -mu), c2 = f2_pack(c, c);
-    uint64_t s2 = f2_pack(st.s, 0.f), t2 = f2_pack(st.t, 0.f);
+    const float mu = __fmul_rn(st.m, c);
+    uint32_t low;                             // nothing below it counts: masked logits are finite from here on
+    if (E::floor_word(st.m + FAR / c, low) && fabsf(mu) < ORDINARY) {
+      const uint64_t nm2 = f2_pack(-mu, -mu), c2 = f2_pack(c, c);
+      uint64_t s2 = f2_pack(st.s, 0.f), t2 = f2_pack(st.t, 0.f);
 #pragma unroll
-    for (int j = 0; j < VECS; ++j) {
-      if (have[j]) {
+      for (int j = 0; j < VECS; ++j) {
+        if (j < have) {
+          float f[N];
+          E::unpack(make_uint4(E::clamp(q[j].x, low), E::clamp(q[j].y, low), E::clamp(q[j].z, low),
+                               E::clamp(q[j].w, low)), f);
+#pragma unroll
+          for (int e = 0; e < N; e += 2) {
+            const uint64_t d2 = f2_fma(f2_pack(f[e], f[e + 1]), c2, nm2);
+            const uint64_t e2 = f2_pack(ex2(f2_lo(d2)), ex2(f2_hi(d2)));
+            s2 = f2_add(s2, e2);
+            t2 = f2_fma(d2, e2, t2);
+          }
+        }
+      }
+      st.s = f2_lo(s2) + f2_hi(s2);
+      st.t = f2_lo(t2) + f2_hi(t2);
+    } else if (st.m != -INFINITY) {
+      // a maximum near the type's lowest value (or infinite, or NaN): exact differences
+#pragma unroll 1
+      for (int j = 0; j < have; ++j) {
+        const uint4 v = j == 0 ? q[0] : j == 1 ? q[1] : j == 2 ? q[2] : q[3];
         float f[N];
-        E::unpack(q[j], f);
+        E::unpack(v, f);
 #pragma unroll
-        for (int e = 0; e < N; e += 2) {
-          const uint64_t d2 = f2_mul(f2_add(f2_pack(f[e], f[e + 1]), nm2), c2);
-          // masked logits (d = -inf) contribute 0 to both sums, not 0 * inf
-          const float d0 = max_nan(f2_lo(d2), -200.f), d1 = max_nan(f2_hi(d2), -200.f);
-          const uint64_t e2 = f2_pack(ex2(d0), ex2(d1));
-          s2 = f2_add(s2, e2);
-          t2 = f2_fma(f2_pack(d0, d1), e2, t2);
+        for (int e = 0; e < N; ++e) {
+          const float d = fabsf(mu) < ORDINARY ? max_nan(fmaf(f[e], c, -mu), FAR) : max_nan((f[e] - st.m) * c, FAR);
+          const float w = ex2(d);
+          st.s += w;
+          st.t = fmaf(d, w, st.t);
         }
       }
     }
-    st.s = f2_lo(s2) + f2_hi(s2);
-    st.t = f2_lo(t2) + f2_hi(t2);
 
     if constexpr (TOPK) {
-      auto survivors = [&]() {
+      // the other warps' bounds; any earlier value of them is a bound too
+      raise(*static_cast<volatile Key*>(&sm.thr));
+      const uint32_t least = __reduce_min_sync(
+          0xffffffffu, lane < WARPS ? *static_cast<volatile uint32_t*>(&sm.share[lane]) : 0xFFFFFFFFu);
+      if (least) raise((static_cast<Key>(least) << 32) - 1);
+      const uint32_t hit = __ballot_sync(0xffffffffu, have && !(bm < thr_v));
+      if (hit) {
+        const int i0 = head + (base + static_cast<int>(threadIdx.x)) * N;
+        if (__popc(hit) > CROWD) {
+          const uint32_t o = warp_sort(have ? ordered(bm) : 0u, lane);
+          const uint32_t kth = __shfl_sync(0xffffffffu, o, p.k - 1), val = __shfl_sync(0xffffffffu, o, part - 1);
+          if (kth) raise((static_cast<Key>(kth) << 32) - 1);
+          if (lane == 0 && val > sm.share[warp]) sm.share[warp] = val;
+        }
+        uint32_t mine = 0;                    // this thread's vectors with survivors
 #pragma unroll
         for (int j = 0; j < VECS; ++j) {
-          if (have[j] && !(vm[j] < thr_v)) {
-            float f[N];
-            E::unpack(q[j], f);
-            const uint32_t i0 = static_cast<uint32_t>(head) + static_cast<uint32_t>(base + j * THREADS + threadIdx.x) * N;
-#pragma unroll
-            for (int e = 0; e < N; ++e) {
-              const Key k = make_key(f[e], i0 + e);
-              if (k > thr) {
-                const int pos = atomicAdd(&sm.count, 1);
-                if (pos < CAP) sm.buf[pos] = k;
-              }
-            }
-          }
+          const bool low = vm[j] < thr_v || (vm[j] == thr_v && static_cast<uint32_t>(i0 + j * THREADS * N) > thr_i);
+          mine |= j < have && !low ? 1u << j : 0u;
         }
-      };
-      __syncthreads();                                  // every thread has read the last count
-      bool again = first;
-      if (!first) {
-        survivors();
-        __syncthreads();
-        again = sm.count > CAP;
-      }
-      if (again) {
-        // threshold from this tile's own maxima: the k-th largest of the
-        // threads' largest keys
-        Key own = 0;
-#pragma unroll
-        for (int j = 0; j < VECS; ++j) {
-          if (have[j]) {
-            float f[N];
-            E::unpack(q[j], f);
-            const uint32_t i0 = static_cast<uint32_t>(head) + static_cast<uint32_t>(base + j * THREADS + threadIdx.x) * N;
-#pragma unroll
-            for (int e = 0; e < N; ++e) {
-              const Key k = make_key(f[e], i0 + e);
-              own = k > own ? k : own;
-            }
+        while (true) {
+          const uint32_t b = __ballot_sync(0xffffffffu, mine != 0);
+          if (b == 0) break;
+          if (mine) {
+            const int j = __ffs(static_cast<int>(mine)) - 1;
+            const int at = queued + __popc(b & ((1u << lane) - 1u));
+            sm.queue[warp][at] = j == 0 ? q[0] : j == 1 ? q[1] : j == 2 ? q[2] : q[3];
+            sm.queue_at[warp][at] = i0 + j * THREADS * N;
+            mine &= mine - 1;
           }
+          queued += __popc(b);
+          if (queued >= 32) process();
         }
-        block_top32(sm, nullptr, 0, own, warp, lane);
-        const Key kth = sm.top[p.k - 1];
-        if (kth != 0 && kth - 1 > thr) thr = kth - 1;   // keys >= kth survive
-        thr_v = thr ? key_value(thr + 1) : -INFINITY;
-        if (threadIdx.x == 0) sm.count = kept;
-        __syncthreads();
-        survivors();
-        __syncthreads();
-      }
-      first = false;
-      kept = sm.count;                                  // <= CAP: k * 32 + SOFT
-      if (kept > SOFT) {
-        block_top32(sm, sm.buf, kept, 0, warp, lane);
-        thr = sm.top[p.k - 1];                          // kept > SOFT >= k: a real key, already there
-        thr_v = key_value(thr);
-        if (warp == 0) sm.buf[lane] = sm.top[lane];
-        kept = p.k;
-        if (threadIdx.x == 0) sm.count = kept;
       }
     }
   }
+  if (TOPK && queued > 0) process();
+  if (TOPK && pending > 0) flush();
 
   // this CTA's statistics, fixed order
 #pragma unroll
@@ -414,29 +536,34 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const Params p) {
     st = merge_stat(st, b, c);
   }
   if (lane == 0) sm.wstat[warp] = st;
-  __syncthreads();
-  if (TOPK) block_top32(sm, sm.buf, kept, 0, warp, lane);
+  if (TOPK) merge_lists(sm, best, WARPS, warp, lane);
+  else __syncthreads();
   if (threadIdx.x == 0) {
     Stat a = sm.wstat[0];
     for (int w = 1; w < WARPS; ++w) a = merge_stat(a, sm.wstat[w], c);
     sm.stat = a;
   }
-  Key best = TOPK && warp == 0 ? sm.top[lane] : 0;
   if (p.C > 1) {
     cluster_sync_all();
-    if (rank == 0 && warp == 0) {
-      Stat a = sm.stat;
-      for (int r = 1; r < p.C; ++r) {
-        const uint32_t sa = dsmem_addr(&sm.stat, r);
-        Stat b;
-        b.m = dsmem_ld_f32(sa);
-        b.s = dsmem_ld_f32(sa + 4);
-        b.t = dsmem_ld_f32(sa + 8);
-        a = merge_stat(a, b, c);
-        if (TOPK) best = warp_merge(best, dsmem_ld_u64(dsmem_addr(&sm.top[lane], r)), lane);
+    if (rank == 0) {
+      // warp w fetches rank w's results
+      if (warp > 0 && warp < p.C && lane == 0) {
+        const uint32_t sa = dsmem_addr(&sm.stat, warp);
+        sm.wstat[warp].m = dsmem_ld_f32(sa);
+        sm.wstat[warp].s = dsmem_ld_f32(sa + 4);
+        sm.wstat[warp].t = dsmem_ld_f32(sa + 8);
       }
-      if (lane == 0) sm.stat = a;
-      __syncwarp();
+      if (TOPK) {
+        best = warp < p.C ? dsmem_ld_u64(dsmem_addr(&sm.top[lane], warp)) : 0;
+        merge_lists(sm, best, p.C, warp, lane);
+      } else {
+        __syncthreads();
+      }
+      if (threadIdx.x == 0) {
+        Stat a = sm.stat;
+        for (int r = 1; r < p.C; ++r) a = merge_stat(a, sm.wstat[r], c);
+        sm.stat = a;
+      }
     }
     cluster_sync_all();          // peers stay until rank 0 has read them
   } else {
@@ -447,15 +574,18 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const Params p) {
   const Stat a = sm.stat;
   const float zmax = a.m * p.scale;
   const bool empty = zmax == -INFINITY;      // the mask leaves nothing
-  const float ls = logf(a.s);
+  const float mu = __fmul_rn(a.m, c);
+  const float delta = fabsf(mu) < ORDINARY ? fmaf(a.m, c, -mu) : 0.f;   // d's reference against the maximum itself
+  const float ls = logf(a.s) - delta * LN2;
   if (TOPK && lane < p.k) {
-    p.top_ids[row * p.k + lane] = key_index(best);
-    p.top_logprobs[row * p.k + lane] = empty ? -INFINITY : (key_value(best) - a.m) * p.scale - ls;
+    const Key k = sm.top[lane];
+    p.top_ids[row * p.k + lane] = key_index(k);
+    p.top_logprobs[row * p.k + lane] = empty ? -INFINITY : (key_value(k) - a.m) * p.scale - ls;
   }
   if (lane == 0) {
     if (p.lse) p.lse[row] = empty ? -INFINITY : zmax + ls;
     if (p.entropy) {
-      const float h = ls - a.t / a.s * LN2;
+      const float h = ls - (a.t / a.s - delta) * LN2;
       p.entropy[row] = empty || h < 0.f ? 0.f : h;
     }
     if (p.logprob) {
@@ -484,9 +614,9 @@ cudaError_t launch_fwd(const LogprobArgs& a) {
   p.top_logprobs = a.top_logprobs;
   // CTAs per row: as many as keep every CTA at least one full tile and the
   // grid within two waves of the 4 CTAs an SM holds
-  constexpr int64_t TILE = static_cast<int64_t>(THREADS) * VECS * Elem<T>::N;
+  constexpr int64_t LOGITS = static_cast<int64_t>(TILE) * Elem<T>::N;
   int C = 1;
-  while (C < 8 && a.M * C * 2 <= 8LL * a.num_sms && a.V >= TILE * C * 2) C *= 2;
+  while (C < 8 && a.M * C * 2 <= 8LL * a.num_sms && a.V >= LOGITS * C * 2) C *= 2;
   p.C = C;
   const unsigned grid = static_cast<unsigned>(a.M * C);
   if (a.top_k > 0) {
@@ -596,8 +726,8 @@ cudaError_t launch_bwd(const LogprobBwdArgs& a) {
   p.ld = a.ld;
   p.ldd = a.ldd;
   p.V = static_cast<int>(a.V);
-  constexpr int64_t TILE = static_cast<int64_t>(THREADS) * BWD_VECS * Elem<T>::N;
-  p.chunks = static_cast<int>((a.V + TILE - 1) / TILE);
+  constexpr int64_t CHUNK = static_cast<int64_t>(THREADS) * BWD_VECS * Elem<T>::N;
+  p.chunks = static_cast<int>((a.V + CHUNK - 1) / CHUNK);
   p.targets = a.targets;
   p.lse = a.lse;
   p.entropy = a.entropy;

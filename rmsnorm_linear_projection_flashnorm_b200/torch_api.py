@@ -278,7 +278,7 @@ def proj(x: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None, 
     with _on(dev, stream):
         if out is None:
             dt = out_dtype or (residual.dtype if residual is not None else torch.bfloat16)
-            out = torch.empty((M, N), dtype=dt, device=dev)
+            out = torch.empty(M, N, dtype=dt, device=dev)
         ldy = _rows(out, "out", _BF16_FP32, (M, N))
         if residual is None:
             ldr = 0
@@ -349,9 +349,9 @@ def moe_swiglu(x: torch.Tensor, g: Optional[torch.Tensor], router: torch.Tensor,
     _vec(select_bias, "select_bias", torch.float32, E, dev)
     with _on(dev, stream):
         if out is None:
-            out = torch.empty((M, d), dtype=bf, device=dev)
-        ids = torch.empty((M, top_k), dtype=torch.int32, device=dev)
-        w = torch.empty((M, top_k), dtype=torch.float32, device=dev)
+            out = torch.empty(M, d, dtype=bf, device=dev)
+        ids = torch.empty(M, top_k, dtype=torch.int32, device=dev)
+        w = torch.empty(M, top_k, dtype=torch.float32, device=dev)
         if ws is None:
             ws = Workspace(dev)
         buf = ws.reserve(fn_workspace_size_moe(M, d, I, E, top_k))
@@ -379,10 +379,10 @@ def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None,
     _vec(targets, "targets", torch.int32, M, dev)
     with _on(dev, stream):
         if out is None:
-            lp, ent, lse = torch.empty((3, M), dtype=torch.float32, device=dev).unbind()
+            lp, ent, lse = torch.empty(3, M, dtype=torch.float32, device=dev).unbind()
             out = TokenLogprobs(lp if targets is not None else None, ent, lse,
-                                torch.empty((M, top_k), dtype=torch.int32, device=dev),
-                                torch.empty((M, top_k), dtype=torch.float32, device=dev))
+                                torch.empty(M, top_k, dtype=torch.int32, device=dev),
+                                torch.empty(M, top_k, dtype=torch.float32, device=dev))
         else:
             _vec(out.logprob, "logprob", torch.float32, M, dev)
             _vec(out.entropy, "entropy", torch.float32, M, dev)
