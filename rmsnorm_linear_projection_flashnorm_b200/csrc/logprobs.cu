@@ -22,15 +22,19 @@
 // keeps its 32 largest keys, sorted, one per lane.  A threshold key, never
 // above the true k-th largest, filters the stream: one comparison per 32
 // logits of a thread.  It is the largest of
+//   the k-th largest of all threads' maxima, taken after 1, 4, 16, ... tiles
+//     (about k logits of a tile lie above it, however many there were before);
 //   the warps' own k-th keys;
-//   the smallest of the warps' (k / 8, rounded up)-th values: 8 warps hold that
-//     many each, so k logits are not below it;
-//   where many lanes hold survivors at once (a row's first tile, rows that grow
-//     steadily), the k-th largest of the lanes' maxima.
+//   where many lanes of a warp hold survivors (rows that grow steadily), the
+//     k-th largest of their maxima.
 // What a warp does per survivor decides the speed (at 8 alternatives of 131072
-// logits, 130 instructions each doubled the kernel's time), so vectors with a
-// survivor are only queued; 32 of them at a time give up their keys, which are
-// sorted and merged into the list.
+// logits, 130 instructions for each survivor of the warps' own thresholds
+// doubled the kernel's time), so vectors with a survivor are only queued; 32 of
+// them at a time give up their keys.  A warp whose buffer fills sorts it into a
+// list of its 32 largest; most rows end before that.  At the end a key's place
+// is the number of keys above it, which a thread counts for each.  Logits of
+// -inf never survive; where fewer than k others are left, the row's first ones
+// fill the places.
 //
 // Work split: one thread-block cluster per row; C = 1, 2, 4 or 8 CTAs, more
 // when there are few rows, so one decoded token still uses 8 SMs.  The CTAs'
@@ -39,6 +43,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <cfloat>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -76,13 +81,6 @@ struct Elem;
 template <>
 struct Elem<__nv_bfloat16> {
   static constexpr int N = 8;
-  static __device__ __forceinline__ float vmax(const uint4& v) {
-    uint32_t a, b;
-    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(v.x), "r"(v.y));
-    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(v.z), "r"(v.w));
-    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(b));
-    return max_nan(bf16lo_to_f32(a), bf16hi_to_f32(a));
-  }
   static __device__ __forceinline__ void unpack(const uint4& v, float (&f)[8]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -91,6 +89,11 @@ struct Elem<__nv_bfloat16> {
       f[2 * i + 1] = bf16hi_to_f32(w[i]);
     }
   }
+  static __device__ __forceinline__ uint32_t wmax(uint32_t a, uint32_t b) {   // NaN if either is
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(b));
+    return a;
+  }
+  static __device__ __forceinline__ float wvalue(uint32_t a) { return max_nan(bf16lo_to_f32(a), bf16hi_to_f32(a)); }
   // Largest pair of values not above f, and both halves of a word kept from below it.
   static __device__ __forceinline__ bool floor_word(float f, uint32_t& w) {
     const __nv_bfloat16 h = __float2bfloat16_rd(f);
@@ -112,14 +115,6 @@ struct Elem<__nv_bfloat16> {
 template <>
 struct Elem<__half> {
   static constexpr int N = 8;
-  static __device__ __forceinline__ float vmax(const uint4& v) {
-    uint32_t a, b;
-    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(a) : "r"(v.x), "r"(v.y));
-    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(b) : "r"(v.z), "r"(v.w));
-    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(b));
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&a));
-    return max_nan(f.x, f.y);
-  }
   static __device__ __forceinline__ void unpack(const uint4& v, float (&f)[8]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -128,6 +123,14 @@ struct Elem<__half> {
       f[2 * i] = p.x;
       f[2 * i + 1] = p.y;
     }
+  }
+  static __device__ __forceinline__ uint32_t wmax(uint32_t a, uint32_t b) {
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(b));
+    return a;
+  }
+  static __device__ __forceinline__ float wvalue(uint32_t a) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&a));
+    return max_nan(f.x, f.y);
   }
   static __device__ __forceinline__ bool floor_word(float f, uint32_t& w) {
     const __half h = __float2half_rd(f);
@@ -154,16 +157,16 @@ struct Elem<__half> {
 template <>
 struct Elem<float> {
   static constexpr int N = 4;
-  static __device__ __forceinline__ float vmax(const uint4& v) {
-    return max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)),
-                   max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
-  }
   static __device__ __forceinline__ void unpack(const uint4& v, float (&f)[4]) {
     f[0] = __uint_as_float(v.x);
     f[1] = __uint_as_float(v.y);
     f[2] = __uint_as_float(v.z);
     f[3] = __uint_as_float(v.w);
   }
+  static __device__ __forceinline__ uint32_t wmax(uint32_t a, uint32_t b) {
+    return __float_as_uint(max_nan(__uint_as_float(a), __uint_as_float(b)));
+  }
+  static __device__ __forceinline__ float wvalue(uint32_t a) { return __uint_as_float(a); }
   static __device__ __forceinline__ bool floor_word(float f, uint32_t& w) {
     w = __float_as_uint(f);
     return isfinite(f);
@@ -177,6 +180,13 @@ struct Elem<float> {
   static __device__ __forceinline__ float load(const float* p) { return *p; }
   static __device__ __forceinline__ float from(float f) { return f; }
 };
+
+// Maximum of a vector as a packed word; NaN if any value is.
+template <typename T>
+__device__ __forceinline__ uint32_t vmax(const uint4& v) {
+  using E = Elem<T>;
+  return E::wmax(E::wmax(v.x, v.y), E::wmax(v.z, v.w));
+}
 
 // ---------------------------------------------------------------------------
 // keys: (ordered value, complement of the index); 0 is below every real key
@@ -201,6 +211,9 @@ __device__ __forceinline__ int key_index(Key k) {
   return static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(k));
 }
 
+// The largest key of -inf; those above it have values.
+constexpr Key NOTHING = 0x007FFFFFFFFFFFFFull;
+
 // One step of a bitonic network over the lanes: keep the larger key where
 // `keep_max`, else the smaller.
 template <typename K>
@@ -223,9 +236,10 @@ __device__ __forceinline__ K warp_sort(K k, int lane) {
 }
 // The 32 largest of two sorted runs, sorted: the larger of a[i] and b[31 - i]
 // is a bitonic run that holds them.
-__device__ __forceinline__ Key warp_merge(Key a, Key b, int lane) {
-  const Key r = __shfl_sync(0xffffffffu, b, 31 - lane);
-  Key k = a > r ? a : r;
+template <typename K>
+__device__ __forceinline__ K warp_merge(K a, K b, int lane) {
+  const K r = __shfl_sync(0xffffffffu, b, 31 - lane);
+  K k = a > r ? a : r;
 #pragma unroll
   for (int j = 16; j > 0; j >>= 1) k = cmp_xchg(k, j, (lane & j) == 0);
   return k;
@@ -254,13 +268,17 @@ __device__ __forceinline__ Stat merge_stat(const Stat& a, const Stat& b, float c
 }
 
 struct Smem {
-  uint4 stage[STAGES][TILE];
+  union {
+    uint4 stage[STAGES][TILE];
+    Key pool[WARPS * 64];        // at the end: what the warps kept, then what the ranks kept
+  };
   uint4 queue[WARPS][64];        // vectors with survivors
-  Key buf[WARPS][64];            // survivors; at the end the warps' lists
+  Key buf[WARPS][64];            // survivors
   int queue_at[WARPS][64];       // their first logit
   Key top[32];                   // this CTA's result, read by rank 0 of the cluster
   Key thr;                       // largest of the warps' k-th keys
-  uint32_t share[WARPS];         // the warps' (k / WARPS, rounded up)-th ordered values
+  int pooled;                    // keys in the pool
+  uint32_t vals[WARPS][32];      // sorted maxima of the lanes, merged in vals[0]
   Stat wstat[WARPS];
   Stat stat;            // this CTA's (m, s, t), read by rank 0
 };
@@ -269,20 +287,16 @@ __device__ __forceinline__ void copy_async(uint4* dst, const uint4* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
-// Merge the warps' sorted lists (the first `n` of them) into sm.top.  All
-// threads call; ends with a barrier.
-__device__ __forceinline__ void merge_lists(Smem& sm, Key best, int n, int warp, int lane) {
-  __syncwarp();
-  sm.buf[warp][lane] = best;
-#pragma unroll
-  for (int w = WARPS / 2; w > 0; w >>= 1) {
-    __syncthreads();
-    if (warp < w && warp + w < n) {
-      best = warp_merge(best, sm.buf[warp + w][lane], lane);
-      sm.buf[warp][lane] = best;
-    }
+// The k largest of the n unique keys in sm.pool, largest first, to sm.top.  All
+// threads call, behind a barrier; ends with one.
+__device__ __forceinline__ void select_top(Smem& sm, int n, int k) {
+  for (int i = static_cast<int>(threadIdx.x); i < n; i += THREADS) {
+    const Key key = sm.pool[i];
+    int above = 0;
+#pragma unroll 8
+    for (int o = 0; o < n; ++o) above += sm.pool[o] > key ? 1 : 0;
+    if (above < k) sm.top[above] = key;
   }
-  if (warp == 0) sm.top[lane] = best;
   __syncthreads();
 }
 
@@ -306,8 +320,10 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const Params p) {
   const int64_t row = blockIdx.x / p.C;
   const T* x = static_cast<const T*>(p.logits) + row * p.ld;
   const float c = p.scale * LOG2E;
-  if (TOPK && threadIdx.x < WARPS) sm.share[threadIdx.x] = 0;
-  if (TOPK && threadIdx.x == 0) sm.thr = 0;
+  if (TOPK && threadIdx.x == 0) {
+    sm.thr = 0;
+    sm.pooled = 0;
+  }
   grid_dependency_wait();
   grid_launch_dependents();
 
@@ -323,10 +339,15 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const Params p) {
   const uint4* xv = reinterpret_cast<const uint4*>(x + head);
 
   auto fetch = [&](int base, int s) {         // this thread's vectors of a tile
+    const uint4* src = xv + base + threadIdx.x;
+    uint4* dst = &sm.stage[s][threadIdx.x];
+    if (base + TILE <= v1) {
 #pragma unroll
-    for (int j = 0; j < VECS; ++j) {
-      const int i = base + j * THREADS + static_cast<int>(threadIdx.x);
-      if (i < v1) copy_async(&sm.stage[s][j * THREADS + threadIdx.x], xv + i);
+      for (int j = 0; j < VECS; ++j) copy_async(dst + j * THREADS, src + j * THREADS);
+    } else {
+#pragma unroll
+      for (int j = 0; j < VECS; ++j)
+        if (base + j * THREADS + static_cast<int>(threadIdx.x) < v1) copy_async(dst + j * THREADS, src + j * THREADS);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -336,11 +357,11 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const Params p) {
 
   Stat st{-INFINITY, 0.f, 0.f};
   // top alternatives of this warp
-  Key best = 0, thr = 0;
-  float thr_v = -INFINITY;                    // keys above thr: values above thr_v, or equal
-  uint32_t thr_i = 0xFFFFFFFFu;               // to it with an index up to thr_i
-  int pending = 0, queued = 0;
-  const int part = (p.k + WARPS - 1) / WARPS;
+  Key best = 0, bound = 0;                    // bound: from all threads' maxima
+  Key thr = NOTHING;                          // keys above it survive: values above thr_v,
+  float thr_v = -FLT_MAX;                     // or equal to it with an index up to thr_i
+  uint32_t thr_i = 0xFFFFFFFFu;
+  int pending = 0, queued = 0, tile = 0, refresh = 1;
   auto raise = [&](Key t) {
     if (t > thr) {
       thr = t;
@@ -356,11 +377,7 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const Params p) {
     pending = max(pending - 32, 0);
     if (lane < pending) sm.buf[warp][lane] = rest;
     const Key kth = __shfl_sync(0xffffffffu, best, p.k - 1);
-    const uint32_t val = static_cast<uint32_t>(__shfl_sync(0xffffffffu, best, part - 1) >> 32);
-    if (lane == 0) {
-      if (kth > thr) atomicMax(&sm.thr, kth);
-      if (val > sm.share[warp]) sm.share[warp] = val;
-    }
+    if (lane == 0 && kth > thr) atomicMax(&sm.thr, kth);
     raise(kth);
   };
   auto append = [&](bool on, Key k) {
@@ -372,14 +389,22 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const Params p) {
   auto process = [&]() {                      // the first 32 vectors of the queue
     __syncwarp();
     uint32_t mask = 0;
-    float f[N];
+    float f[N] = {};
     int at = 0;
     if (lane < queued) {
       E::unpack(sm.queue[warp][lane], f);
       at = sm.queue_at[warp][lane];
-#pragma unroll
-      for (int e = 0; e < N; ++e) mask |= !(f[e] < thr_v) ? 1u << e : 0u;
+      mask = (1u << N) - 1u;
     }
+    // candidates, again whenever a flush has raised the threshold (long ties)
+    Key seen = thr;
+    auto filter = [&]() {
+      seen = thr;
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (f[e] < thr_v || (f[e] == thr_v && static_cast<uint32_t>(at + e) > thr_i)) mask &= ~(1u << e);
+    };
+    filter();
     while (__any_sync(0xffffffffu, mask != 0)) {
       const int e = __ffs(static_cast<int>(mask)) - 1;      // the lane's next candidate
       float fe = f[0];
@@ -388,8 +413,8 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const Params p) {
       const Key k = make_key(fe, static_cast<uint32_t>(at + e));
       append(mask != 0 && k > thr, k);
       mask &= mask - 1;
+      if (thr != seen) filter();
     }
-    if (pending > 0) flush();
     if (lane + 32 < queued) {
       const uint4 v = sm.queue[warp][32 + lane];
       sm.queue[warp][lane] = v;
@@ -415,26 +440,32 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const Params p) {
         st.t = d * st.s;
       }
     }
-    if (TOPK) append(on, make_key(v, idx));
+    if (TOPK) append(on && v != -INFINITY, make_key(v, idx));
   }
 
   for (int base = v0, s = 0; base < v1; base += TILE, s ^= 1) {
     uint4 q[VECS];
-    int have = 0;                             // of this thread's vectors, the first so many
-    asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
-#pragma unroll
-    for (int j = 0; j < VECS; ++j) {
-      if (base + j * THREADS + static_cast<int>(threadIdx.x) < v1) {
-        q[j] = sm.stage[s][j * THREADS + threadIdx.x];
-        have = j + 1;
-      }
-    }
+    int have = VECS;                          // of this thread's vectors, the first so many
     float bm = -INFINITY;
-    float vm[VECS];
+    asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+    const uint4* own = &sm.stage[s][threadIdx.x];
+    if (base + TILE <= v1) {
 #pragma unroll
-    for (int j = 0; j < VECS; ++j) {
-      vm[j] = j < have ? E::vmax(q[j]) : -INFINITY;
-      bm = max_nan(bm, vm[j]);
+      for (int j = 0; j < VECS; ++j) q[j] = own[j * THREADS];
+      uint32_t w = vmax<T>(q[0]);
+#pragma unroll
+      for (int j = 1; j < VECS; ++j) w = E::wmax(w, vmax<T>(q[j]));
+      bm = E::wvalue(w);
+    } else {
+      have = 0;
+#pragma unroll
+      for (int j = 0; j < VECS; ++j) {
+        if (base + j * THREADS + static_cast<int>(threadIdx.x) < v1) {
+          q[j] = own[j * THREADS];
+          bm = max_nan(bm, E::wvalue(vmax<T>(q[j])));
+          have = j + 1;
+        }
+      }
     }
     fetch(base + STAGES * TILE, s);           // the slot's vectors are in registers
     // running softmax statistics
@@ -452,20 +483,23 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const Params p) {
     if (E::floor_word(st.m + FAR / c, low) && fabsf(mu) < ORDINARY) {
       const uint64_t nm2 = f2_pack(-mu, -mu), c2 = f2_pack(c, c);
       uint64_t s2 = f2_pack(st.s, 0.f), t2 = f2_pack(st.t, 0.f);
+      auto add = [&](const uint4& v) {
+        float f[N];
+        E::unpack(make_uint4(E::clamp(v.x, low), E::clamp(v.y, low), E::clamp(v.z, low), E::clamp(v.w, low)), f);
 #pragma unroll
-      for (int j = 0; j < VECS; ++j) {
-        if (j < have) {
-          float f[N];
-          E::unpack(make_uint4(E::clamp(q[j].x, low), E::clamp(q[j].y, low), E::clamp(q[j].z, low),
-                               E::clamp(q[j].w, low)), f);
-#pragma unroll
-          for (int e = 0; e < N; e += 2) {
-            const uint64_t d2 = f2_fma(f2_pack(f[e], f[e + 1]), c2, nm2);
-            const uint64_t e2 = f2_pack(ex2(f2_lo(d2)), ex2(f2_hi(d2)));
-            s2 = f2_add(s2, e2);
-            t2 = f2_fma(d2, e2, t2);
-          }
+        for (int e = 0; e < N; e += 2) {
+          const uint64_t d2 = f2_fma(f2_pack(f[e], f[e + 1]), c2, nm2);
+          const uint64_t e2 = f2_pack(ex2(f2_lo(d2)), ex2(f2_hi(d2)));
+          s2 = f2_add(s2, e2);
+          t2 = f2_fma(d2, e2, t2);
         }
+      };
+      if (have == VECS) {
+#pragma unroll
+        for (int j = 0; j < VECS; ++j) add(q[j]);
+      } else {
+#pragma unroll 1
+        for (int j = 0; j < have; ++j) add(j == 0 ? q[0] : j == 1 ? q[1] : q[2]);
       }
       st.s = f2_lo(s2) + f2_hi(s2);
       st.t = f2_lo(t2) + f2_hi(t2);
@@ -487,26 +521,45 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const Params p) {
     }
 
     if constexpr (TOPK) {
-      // the other warps' bounds; any earlier value of them is a bound too
-      raise(*static_cast<volatile Key*>(&sm.thr));
-      const uint32_t least = __reduce_min_sync(
-          0xffffffffu, lane < WARPS ? *static_cast<volatile uint32_t*>(&sm.share[lane]) : 0xFFFFFFFFu);
-      if (least) raise((static_cast<Key>(least) << 32) - 1);
+      if (++tile == refresh) {
+        refresh *= 4;
+        uint32_t o = warp_sort(ordered(st.m), lane);
+        sm.vals[warp][lane] = o;
+#pragma unroll
+        for (int w = WARPS / 2; w > 0; w >>= 1) {
+          __syncthreads();
+          if (warp < w) {
+            o = warp_merge(o, sm.vals[warp + w][lane], lane);
+            sm.vals[warp][lane] = o;
+          }
+        }
+        __syncthreads();
+        bound = (static_cast<Key>(sm.vals[0][p.k - 1]) << 32) - 1;
+        raise(bound);
+        __syncthreads();
+      }
       const uint32_t hit = __ballot_sync(0xffffffffu, have && !(bm < thr_v));
       if (hit) {
         const int i0 = head + (base + static_cast<int>(threadIdx.x)) * N;
         if (__popc(hit) > CROWD) {
+          raise(*static_cast<volatile Key*>(&sm.thr));    // any earlier value is a bound too
           const uint32_t o = warp_sort(have ? ordered(bm) : 0u, lane);
-          const uint32_t kth = __shfl_sync(0xffffffffu, o, p.k - 1), val = __shfl_sync(0xffffffffu, o, part - 1);
+          const uint32_t kth = __shfl_sync(0xffffffffu, o, p.k - 1);
           if (kth) raise((static_cast<Key>(kth) << 32) - 1);
-          if (lane == 0 && val > sm.share[warp]) sm.share[warp] = val;
         }
-        uint32_t mine = 0;                    // this thread's vectors with survivors
+        uint32_t mine = (1u << have) - 1u;    // this thread's vectors with survivors
+        Key seen;
+        auto filter = [&]() {
+          seen = thr;
 #pragma unroll
-        for (int j = 0; j < VECS; ++j) {
-          const bool low = vm[j] < thr_v || (vm[j] == thr_v && static_cast<uint32_t>(i0 + j * THREADS * N) > thr_i);
-          mine |= j < have && !low ? 1u << j : 0u;
-        }
+          for (int j = 0; j < VECS; ++j) {
+            if (j < have) {
+              const float vm = E::wvalue(vmax<T>(q[j]));
+              if (vm < thr_v || (vm == thr_v && static_cast<uint32_t>(i0 + j * THREADS * N) > thr_i)) mine &= ~(1u << j);
+            }
+          }
+        };
+        filter();
         while (true) {
           const uint32_t b = __ballot_sync(0xffffffffu, mine != 0);
           if (b == 0) break;
@@ -519,12 +572,12 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const Params p) {
           }
           queued += __popc(b);
           if (queued >= 32) process();
+          if (thr != seen) filter();
         }
       }
     }
   }
   if (TOPK && queued > 0) process();
-  if (TOPK && pending > 0) flush();
 
   // this CTA's statistics, fixed order
 #pragma unroll
@@ -536,8 +589,23 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const Params p) {
     st = merge_stat(st, b, c);
   }
   if (lane == 0) sm.wstat[warp] = st;
-  if (TOPK) merge_lists(sm, best, WARPS, warp, lane);
-  else __syncthreads();
+  __syncthreads();                            // every thread is done with its vectors
+  if constexpr (TOPK) {
+    // the pool: this warp's buffer and list, as far as all warps' bounds leave them
+    const Key cut = max(sm.thr, bound + 1);
+    const Key kept = lane < pending ? sm.buf[warp][lane] : 0;
+    const uint32_t buf = __ballot_sync(0xffffffffu, kept >= cut && kept != 0);
+    const uint32_t list = __ballot_sync(0xffffffffu, best >= cut && best != 0);
+    int at = 0;
+    if (lane == 0) at = atomicAdd(&sm.pooled, __popc(buf) + __popc(list));
+    at = __shfl_sync(0xffffffffu, at, 0);
+    const uint32_t before = (1u << lane) - 1u;
+    if (buf >> lane & 1u) sm.pool[at + __popc(buf & before)] = kept;
+    if (list >> lane & 1u) sm.pool[at + __popc(buf) + __popc(list & before)] = best;
+    if (threadIdx.x < 32) sm.top[threadIdx.x] = 0;
+    __syncthreads();
+    select_top(sm, sm.pooled, p.k);
+  }
   if (threadIdx.x == 0) {
     Stat a = sm.wstat[0];
     for (int w = 1; w < WARPS; ++w) a = merge_stat(a, sm.wstat[w], c);
@@ -553,12 +621,10 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const Params p) {
         sm.wstat[warp].s = dsmem_ld_f32(sa + 4);
         sm.wstat[warp].t = dsmem_ld_f32(sa + 8);
       }
-      if (TOPK) {
-        best = warp < p.C ? dsmem_ld_u64(dsmem_addr(&sm.top[lane], warp)) : 0;
-        merge_lists(sm, best, p.C, warp, lane);
-      } else {
-        __syncthreads();
-      }
+      if (TOPK && warp < p.C && lane < p.k)
+        sm.pool[warp * p.k + lane] = dsmem_ld_u64(dsmem_addr(&sm.top[lane], warp));
+      __syncthreads();
+      if constexpr (TOPK) select_top(sm, p.C * p.k, p.k);
       if (threadIdx.x == 0) {
         Stat a = sm.stat;
         for (int r = 1; r < p.C; ++r) a = merge_stat(a, sm.wstat[r], c);
@@ -571,6 +637,18 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const Params p) {
   }
   if (rank != 0 || warp != 0) return;
 
+  if constexpr (TOPK) {
+    int found = __popc(__ballot_sync(0xffffffffu, lane < p.k && sm.top[lane] != 0));
+    for (int i0 = 0; found < p.k && i0 < p.V; i0 += 32) {
+      const int i = i0 + lane;
+      const bool on = i < p.V && E::load(x + i) == -INFINITY;
+      const uint32_t b = __ballot_sync(0xffffffffu, on);
+      const int at = found + __popc(b & ((1u << lane) - 1u));
+      if (on && at < p.k) sm.top[at] = make_key(-INFINITY, static_cast<uint32_t>(i));
+      found += __popc(b);
+    }
+    __syncwarp();
+  }
   const Stat a = sm.stat;
   const float zmax = a.m * p.scale;
   const bool empty = zmax == -INFINITY;      // the mask leaves nothing
