@@ -63,22 +63,29 @@ __device__ __forceinline__ void epi_act(int act, float (&z)[N]) {
   }
 }
 
+// Rows past the end repeat the last one: without a condition on each, all loads
+// are in flight before the first value is used (with one, the conversion sat
+// behind every load, and a residual doubled the time of 4096 x 2048 x 4096).
 template <int N, typename T>
-__device__ __forceinline__ void epi_load(const T* src, int64_t ld, int rows, float (&r)[N]) {
+__device__ __forceinline__ void epi_load(const T* src, int64_t ld, int rows, T (&r)[N]) {
 #pragma unroll
-  for (int j = 0; j < N; ++j) r[j] = j < rows ? static_cast<float>(src[j * ld]) : 0.f;
+  for (int j = 0; j < N; ++j) r[j] = src[min(j, rows - 1) * ld];
 }
 
-// Rows row0 .. row0 + rows - 1 (at most N) of column col.
+// Rows row0 .. row0 + rows - 1 (1 to N of them) of column col.
 template <int N>
 __device__ __forceinline__ void epi_finish(const Epilogue& e, int64_t row0, int rows, int64_t col, float (&v)[N]) {
   float res[N];
+  if (!e.residual) {
 #pragma unroll
-  for (int j = 0; j < N; ++j) res[j] = 0.f;
-  if (e.residual) {
-    const int64_t at = row0 * e.ldr + col;
-    if (e.out_fp32) epi_load<N>(static_cast<const float*>(e.residual) + at, e.ldr, rows, res);
-    else epi_load<N>(static_cast<const __nv_bfloat16*>(e.residual) + at, e.ldr, rows, res);
+    for (int j = 0; j < N; ++j) res[j] = 0.f;
+  } else if (e.out_fp32) {
+    epi_load<N>(static_cast<const float*>(e.residual) + row0 * e.ldr + col, e.ldr, rows, res);
+  } else {
+    __nv_bfloat16 h[N];
+    epi_load<N>(static_cast<const __nv_bfloat16*>(e.residual) + row0 * e.ldr + col, e.ldr, rows, h);
+#pragma unroll
+    for (int j = 0; j < N; ++j) res[j] = __bfloat162float(h[j]);
   }
   const float bias = e.bias ? __ldg(e.bias + col) : 0.f;
 #pragma unroll
@@ -95,6 +102,113 @@ __device__ __forceinline__ void epi_finish(const Epilogue& e, int64_t row0, int 
 #pragma unroll
     for (int j = 0; j < N; ++j)
       if (j < rows) dst[j * e.ldy] = __float2bfloat16_rn(v[j] + res[j]);
+  }
+}
+
+// The same for a warp that holds 16 rows of 32 columns, one column per lane:
+// the values pass through shared memory (16 rows of SCRATCH_LD floats of this
+// warp's own), so that a lane has 4 columns of 4 rows and reads the residual and
+// writes the output 8 or 16 bytes at a time.  One column per lane takes 2-byte
+// stores, and four times as many of them.
+constexpr int SCRATCH_LD = 36;
+constexpr int SCRATCH_FLOATS = 16 * SCRATCH_LD;
+
+// Whether every row's groups of 4 columns lie on whole vectors.
+inline __host__ bool epi_vector_ok(const Epilogue& e, int64_t N) {
+  const uintptr_t bytes = e.out_fp32 ? 16 : 8;
+  return N % 4 == 0 && e.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(e.y) % bytes == 0 &&
+         (!e.residual || (e.ldr % 4 == 0 && reinterpret_cast<uintptr_t>(e.residual) % bytes == 0));
+}
+
+template <bool F32>
+struct Quad;             // 4 values of the output's type
+template <>
+struct Quad<true> {
+  using Raw = float4;
+  static __device__ __forceinline__ void get(const Raw& r, float* f) { f[0] = r.x, f[1] = r.y, f[2] = r.z, f[3] = r.w; }
+  static __device__ __forceinline__ Raw put(const float* f) { return make_float4(f[0], f[1], f[2], f[3]); }
+};
+template <>
+struct Quad<false> {
+  using Raw = uint2;
+  static __device__ __forceinline__ void get(const Raw& r, float* f) {
+    f[0] = bf16lo_to_f32(r.x), f[1] = bf16hi_to_f32(r.x), f[2] = bf16lo_to_f32(r.y), f[3] = bf16hi_to_f32(r.y);
+  }
+  static __device__ __forceinline__ Raw put(const float* f) {
+    return make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+  }
+};
+
+// The residual of 16 rows of 32 columns ahead of its use, in the vector form:
+// a dependent load in the epilogue waits 1 us while the operand stream fills L2.
+template <bool F32>
+__device__ __forceinline__ void epi_fetch(const Epilogue& e, int lane, int64_t row0, int rows, int64_t col0, int64_t N,
+                                          typename Quad<F32>::Raw (&r)[4]) {
+  using T = typename Quad<F32>::Raw;
+  const int64_t col = col0 + lane % 8 * 4;
+  if (rows <= 0 || col >= N) return;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const int64_t at = (row0 + min(g * 4 + lane / 8, rows - 1)) * e.ldr + col;
+    r[g] = F32 ? *reinterpret_cast<const T*>(static_cast<const float*>(e.residual) + at)
+               : *reinterpret_cast<const T*>(static_cast<const __nv_bfloat16*>(e.residual) + at);
+  }
+}
+
+template <bool F32>
+__device__ __forceinline__ void epi_finish_16x32(const Epilogue& e, bool vec, const typename Quad<F32>::Raw (&raw)[4],
+                                                 float* scratch, int lane, int64_t row0, int rows, int64_t col0,
+                                                 int64_t N, const float4& bias, const float (&v)[16]) {
+  using Q = Quad<F32>;
+  using T = typename Q::Raw;
+  const int64_t col = col0 + lane % 8 * 4;
+  const int cols = static_cast<int>(col < N ? (N - col < 4 ? N - col : 4) : 0);
+#pragma unroll
+  for (int j = 0; j < 16; ++j) scratch[j * SCRATCH_LD + lane] = v[j];
+  __syncwarp();
+  float z[16];
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const float4 f = *reinterpret_cast<const float4*>(scratch + (g * 4 + lane / 8) * SCRATCH_LD + lane % 8 * 4);
+    z[4 * g] = f.x + bias.x, z[4 * g + 1] = f.y + bias.y, z[4 * g + 2] = f.z + bias.z, z[4 * g + 3] = f.w + bias.w;
+  }
+  __syncwarp();
+  epi_act<16>(e.act, z);
+  if (cols == 0) return;
+  if (vec) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      if (e.residual) {
+        float f[4];
+        Q::get(raw[g], f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) z[4 * g + j] += f[j];
+      }
+      const int r = g * 4 + lane / 8;
+      const int64_t at = (row0 + r) * e.ldy + col;
+      if (r < rows) {
+        if (F32) *reinterpret_cast<T*>(static_cast<float*>(e.y) + at) = Q::put(z + 4 * g);
+        else *reinterpret_cast<T*>(static_cast<__nv_bfloat16*>(e.y) + at) = Q::put(z + 4 * g);
+      }
+    }
+    return;
+  }
+  float res[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const int64_t at = (row0 + min(j / 4 * 4 + lane / 8, rows - 1)) * e.ldr + col + min(j % 4, cols - 1);
+    res[j] = !e.residual ? 0.f
+             : F32       ? static_cast<const float*>(e.residual)[at]
+                         : __bfloat162float(static_cast<const __nv_bfloat16*>(e.residual)[at]);
+  }
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const int r = j / 4 * 4 + lane / 8;
+    const int64_t at = (row0 + r) * e.ldy + col + j % 4;
+    if (r < rows && j % 4 < cols) {
+      if (F32) static_cast<float*>(e.y)[at] = z[j] + res[j];
+      else static_cast<__nv_bfloat16*>(e.y)[at] = __float2bfloat16_rn(z[j] + res[j]);
+    }
   }
 }
 

@@ -44,7 +44,8 @@ constexpr int W_BYTES = 2 * W_BOX_BYTES;       // a CTA's 128 columns
 constexpr int NUM_THREADS = 320;
 constexpr int EPI_THREADS = 256;
 constexpr int MAX_STAGES = 11;
-constexpr int RING_BYTES = 7 * 32 * 1024;      // 7 stages at 256 rows
+constexpr int RING_BYTES = 6 * 32 * 1024;      // 6 stages at 256 rows
+constexpr int SCRATCH_BYTES = 8 * SCRATCH_FLOATS * 4;   // of the epilogue warps
 constexpr int TMEM_COLS = 512;
 
 enum : unsigned { kSiteProdEmpty = 1, kSiteMmaAccEmpty, kSiteMmaFull, kSiteEpiAccFull };
@@ -58,10 +59,15 @@ struct Params {
   int sharers;                     // pairs that take a share of them (each at least one k block)
   int stages;
   Epilogue epi;
+  int vec;                         // the epilogue's vector form applies
   unsigned int* status;            // workspace header: status word
   float* part;                     // [grid][2][MAX_NB x 128]
   unsigned long long budget_ns;
   int withhold;
+  const uint8_t* w;                // weight base and row bytes (L2 prefetch addresses)
+  int64_t w_row_bytes;
+  int wrows;
+  int prefetch_iters;
 };
 
 struct alignas(8) Bars {
@@ -73,7 +79,7 @@ struct alignas(8) Bars {
   int abort_flag;
   int epi_ok[2];
 };
-constexpr size_t SMEM = 1024 + RING_BYTES + sizeof(Bars);
+constexpr size_t SMEM = 1024 + RING_BYTES + SCRATCH_BYTES + sizeof(Bars);
 static_assert(SMEM <= 232448, "shared memory budget");
 constexpr int SLOT_FLOATS = MAX_NB * 128;
 
@@ -146,12 +152,13 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, unsig
   }
 }
 
+template <bool F32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     proj_tile_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
                      const Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  Bars& bars = *reinterpret_cast<Bars*>(smem + RING_BYTES);
+  Bars& bars = *reinterpret_cast<Bars*>(smem + RING_BYTES + SCRATCH_BYTES);
   const int x_bytes = p.nb * (BK * 2 / 2);           // this CTA's nb / 2 rows
   const int stage_bytes = W_BYTES + x_bytes;
   const int stages = p.stages;
@@ -183,6 +190,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   if (warp == 1) {
     tmem_alloc_pair(&bars.tmem_base, TMEM_COLS);
     tmem_relinquish_pair();
+  }
+  {
+    // This overlaps the previous kernel in the stream: an L2 prefetch of the
+    // first k blocks cannot return stale data, whoever wrote the weight.  One
+    // 128-byte line per thread and step.
+    SegIter segs(p, pair, npairs);
+    Seg g;
+    if (segs.next(g)) {
+      int mb, nb;
+      tile_coords(g.tile, p, mb, nb);
+      const int n_it = min(p.prefetch_iters, g.kb1 - g.kb0);
+      for (int i = threadIdx.x; i < n_it * BK * 2; i += NUM_THREADS) {
+        const int64_t k = static_cast<int64_t>(g.kb0 + i / (BK * 2)) * BK + (i >> 1) % BK;
+        const int64_t col = static_cast<int64_t>(nb) * BN + rank * 128 + (i & 1) * 64;
+        if (k < p.wrows && col < p.N) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.w + k * p.w_row_bytes + col * 2));
+      }
+    }
   }
   tc_fence_before();
   cluster_sync_all();                                 // both CTAs' barriers are initialised
@@ -292,17 +316,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       tile_coords(g.tile, p, mb, nb);
       const int b = i & 1;
       const uint32_t aph = (i >> 1) & 1;
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + b * MAX_NB;
+      const int n = q * 32 + lane;                 // column within this CTA's 128
+      const int64_t col0 = static_cast<int64_t>(nb) * BN + rank * 128 + q * 32;   // of this warp's 32 columns
+      float4 bias = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (p.epi.bias) {
+        const int64_t last = p.N - 1, c = col0 + lane % 8 * 4;
+        bias = make_float4(__ldg(p.epi.bias + min(c, last)), __ldg(p.epi.bias + min(c + 1, last)),
+                           __ldg(p.epi.bias + min(c + 2, last)), __ldg(p.epi.bias + min(c + 3, last)));
+      }
+      const int row0 = mb * p.nb;
+      // this warp's chunks of 16 rows: half, half + 2, ...; their residual DEPTH ahead
+      constexpr int DEPTH = F32 ? 2 : 4;
+      const bool ahead = !g.shared && p.vec && p.epi.residual;
+      typename Quad<F32>::Raw raw[DEPTH][4];
+      if (ahead)
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d)
+          epi_fetch<F32>(p.epi, lane, row0 + 16 * (half + 2 * d), min(p.M - row0 - 16 * (half + 2 * d), 16), col0, p.N, raw[d]);
       // One thread waits and the whole epilogue follows its decision, so the
       // group never splits at the named barriers or the .sync.aligned loads.
       if (et == 0) bars.epi_ok[b] = mbar_wait_spin(&bars.acc_full[b], aph, ctl, kSiteEpiAccFull) ? 1 : 0;
       named_bar_sync(1, EPI_THREADS);
       if (!bars.epi_ok[b]) break;
       tc_fence_after();
-      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + b * MAX_NB;
-      const int n = q * 32 + lane;                 // column within this CTA's 128
-      const int64_t col = static_cast<int64_t>(nb) * BN + rank * 128 + n;
-      const bool col_ok = col < p.N;
-      const int row0 = mb * p.nb;
       auto release = [&]() {
         // this CTA's epilogue has read TMEM buffer b
         tc_fence_before();
@@ -313,17 +350,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
           if (et == 0) mbar_arrive_remote(acc_empty0 + b * 8);
         }
       };
-      auto finish = [&](int c, float(&v)[32]) {
-        // rows row0 + 32 c + j of column col
-        const int r0 = row0 + 32 * c;
-        if (col_ok) epi_finish<32>(p.epi, r0, min(p.M - r0, 32), col, v);
-      };
       if (!g.shared) {
+        float* scratch = reinterpret_cast<float*>(smem + RING_BYTES) + (warp - 2) * SCRATCH_FLOATS;
 #pragma unroll 1
-        for (int c = half; c < chunks; c += 2) {
-          float v[32];
-          dec::tmem_ld_cols<32>(taddr + c * 32, v);
-          finish(c, v);
+        for (int c0 = half; c0 < 2 * chunks; c0 += 2 * DEPTH) {
+#pragma unroll
+          for (int d = 0; d < DEPTH; ++d) {
+            const int c = c0 + 2 * d, r0 = row0 + 16 * c;
+            if (c < 2 * chunks && r0 < p.M) {
+              float v[16];
+              dec::tmem_ld_cols<16>(taddr + c * 16, v);
+              epi_finish_16x32<F32>(p.epi, p.vec, raw[d], scratch, lane, r0, min(p.M - r0, 16), col0, p.N, bias, v);
+              const int rn = r0 + 32 * DEPTH;
+              if (ahead && c + 2 * DEPTH < 2 * chunks)
+                epi_fetch<F32>(p.epi, lane, rn, min(p.M - rn, 16), col0, p.N, raw[d]);
+            }
+          }
         }
         release();
         continue;
@@ -391,6 +433,14 @@ Plan make_plan(int64_t M, int64_t K, int64_t N, int num_sms) {
   return q;
 }
 
+template <bool F32>
+cudaError_t launch_kernel(const Params& p, const Plan& q, cudaStream_t stream, const CUtensorMap& tx,
+                          const CUtensorMap& tw) {
+  const cudaError_t e = ensure_smem_limit<proj_tile_kernel<F32>>(static_cast<int>(SMEM));
+  if (e != cudaSuccess) return e;
+  return launch_pdl(proj_tile_kernel<F32>, static_cast<unsigned>(2 * q.pairs), NUM_THREADS, SMEM, stream, tx, tw, p);
+}
+
 }  // namespace ptile
 
 size_t proj_tile_workspace_bytes(int64_t M, int64_t K, int64_t N, int num_sms) {
@@ -431,15 +481,18 @@ cudaError_t launch_proj_tile(const ProjArgs& a) {
   p.stages = RING_BYTES / stage_bytes;
   if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;
   p.epi = a.epi;
+  p.vec = epi_vector_ok(a.epi, a.N);
+  p.w = static_cast<const uint8_t*>(a.W);
+  p.w_row_bytes = a.ldw * 2;
+  p.wrows = static_cast<int>(a.K);
+  p.prefetch_iters = a.prefetch_iters;
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
   p.status = reinterpret_cast<unsigned int*>(ws);
   p.part = reinterpret_cast<float*>(ws + kWsHeaderBytes);
   p.budget_ns = a.budget_ns;
   p.withhold = a.withhold;
-  const cudaError_t e = ensure_smem_limit<proj_tile_kernel>(static_cast<int>(SMEM));
-  if (e != cudaSuccess) return e;
-  const cudaError_t l =
-      launch_pdl(proj_tile_kernel, static_cast<unsigned>(2 * q.pairs), NUM_THREADS, SMEM, a.stream, tx, tw, p);
+  const cudaError_t l = a.epi.out_fp32 ? launch_kernel<true>(p, q, a.stream, tx, tw)
+                                       : launch_kernel<false>(p, q, a.stream, tx, tw);
   if (l != cudaSuccess || q.rest == 0) return l;
   FixupArgs f = {};
   f.part = p.part;

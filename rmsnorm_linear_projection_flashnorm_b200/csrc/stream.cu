@@ -388,8 +388,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           const float* wt = p.route.weight + bars.experts[tile / p.tiles] * kMoeMaxRows + m0;
 #pragma unroll
           for (int j = 0; j < RC; ++j) {
-            w[j] = m0 + j < p.M ? __ldcg(wt + j) : 0.f;
-            r[j] = m0 + j < p.M ? __ldcg(p.route.rinv + m0 + j) : 0.f;
+            const int m = min(j, p.M - 1 - m0);          // rows past the end are not stored
+            w[j] = __ldcg(wt + m);
+            r[j] = __ldcg(p.route.rinv + m0 + m);
           }
         }
       };
