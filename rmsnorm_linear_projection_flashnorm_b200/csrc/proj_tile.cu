@@ -1,17 +1,21 @@
 // fn_proj above 64 rows: y = act(x W + b) + residual on pairs of SMs, sm_100a.
 //
-// Each 2-CTA cluster computes 256 weight columns x NB rows with
+// Each 2-CTA cluster computes 256 weight columns x H * NB rows with
 // tcgen05.mma.cta_group::2 (swap-AB: the weight columns on the MMA's M side,
 // 128 in each CTA, the rows of x on its N side).  N may be any multiple of 32
 // up to 256, so a batch is cut into equal row blocks padded by less than 32
 // rows each: 300 rows run as 2 x 160, not as 2 x 256.  Both operands are
 // staged by TMA with 128-byte swizzle: the CTA's 128 weight columns (16 KB per
 // 64-deep k step, N-major) and its half of the rows (NB / 2, K-major).
+// Above 256 rows a tile may take two MMAs per K step (H = 2, up to 512 rows in
+// one accumulator of 512 columns): a staged weight byte then feeds twice the
+// rows, but the epilogue does not overlap the next tile.  make_plan estimates
+// both.
 // Ragged K and N read zeros past the edge (TMA fill), the epilogue stores
 // what exists.
 //
-// Bound by the tensor cores at large M, by the weight stream from HBM at a
-// few hundred rows.  Tiles run whole, one after another per pair, in as many
+// Bound by the tensor cores (under the power cap) at large M and K, by the
+// operands' way from L2 into the SMs at a few hundred rows.  Tiles run whole, one after another per pair, in as many
 // rounds as fill every pair; the k ranges of the tiles that are left over
 // (fewer than pairs) are cut into equal shares over all pairs where that
 // saves more than the exchange costs.  Sharing CTAs write fp32 partials to
@@ -28,6 +32,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "decode_common.cuh"
 #include "epilogue.cuh"
 #include "internal.h"
@@ -38,7 +44,7 @@ namespace ptile {
 
 constexpr int BK = 64;
 constexpr int BN = 256;                        // weight columns per pair
-constexpr int MAX_NB = 256;                    // rows per tile
+constexpr int MAX_NB = 256;                    // rows per MMA
 constexpr int W_BOX_BYTES = 64 * BK * 2;       // 64 columns x 64 k rows
 constexpr int W_BYTES = 2 * W_BOX_BYTES;       // a CTA's 128 columns
 constexpr int NUM_THREADS = 320;
@@ -52,7 +58,9 @@ enum : unsigned { kSiteProdEmpty = 1, kSiteMmaAccEmpty, kSiteMmaFull, kSiteEpiAc
 
 struct Params {
   int M, N;
-  int nb, num_m, num_n, kblocks;
+  int nb;                          // rows per MMA
+  int rows;                        // rows per tile: H nb
+  int num_m, num_n, kblocks;
   int group_m;                     // tile raster: bands of group_m row blocks
   int full;                        // tiles that run whole
   int rest;                        // tiles whose k blocks are shared between pairs
@@ -61,7 +69,7 @@ struct Params {
   Epilogue epi;
   int vec;                         // the epilogue's vector form applies
   unsigned int* status;            // workspace header: status word
-  float* part;                     // [grid][2][MAX_NB x 128]
+  float* part;                     // [grid][2][rows x 128]
   unsigned long long budget_ns;
   int withhold;
   const uint8_t* w;                // weight base and row bytes (L2 prefetch addresses)
@@ -81,7 +89,6 @@ struct alignas(8) Bars {
 };
 constexpr size_t SMEM = 1024 + RING_BYTES + SCRATCH_BYTES + sizeof(Bars);
 static_assert(SMEM <= 232448, "shared memory budget");
-constexpr int SLOT_FLOATS = MAX_NB * 128;
 
 // First of the shared tiles' k blocks that pair c takes.
 __device__ __forceinline__ long long share_begin(const Params& p, int c) {
@@ -152,15 +159,16 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, unsig
   }
 }
 
-template <bool F32>
+template <bool F32, int H>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     proj_tile_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
                      const Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Bars& bars = *reinterpret_cast<Bars*>(smem + RING_BYTES + SCRATCH_BYTES);
-  const int x_bytes = p.nb * (BK * 2 / 2);           // this CTA's nb / 2 rows
-  const int stage_bytes = W_BYTES + x_bytes;
+  constexpr int NBUF = H == 1 ? 2 : 1;               // accumulators
+  const int x_bytes = p.nb * (BK * 2 / 2);           // this CTA's nb / 2 rows of an MMA
+  const int stage_bytes = W_BYTES + H * x_bytes;
   const int stages = p.stages;
 
   const int warp = threadIdx.x >> 5;
@@ -229,7 +237,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       while (ok && segs.next(g)) {
         int mb, nb;
         tile_coords(g.tile, p, mb, nb);
-        const int row0 = mb * p.nb + static_cast<int>(rank) * (p.nb / 2);
+        const int row0 = mb * p.rows + static_cast<int>(rank) * (p.nb / 2);
         const int col0 = nb * BN + static_cast<int>(rank) * 128;
         for (int kb = g.kb0; kb < g.kb1; ++kb) {
           if (!mbar_wait_spin(&bars.empty[s], ph ^ 1, ctl, kSiteProdEmpty)) { ok = false; break; }
@@ -238,7 +246,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
           uint8_t* st = smem + s * stage_bytes;
           tma_load_2d_pair(st, &tmap_w, fb, col0, kb * BK);
           tma_load_2d_pair(st + W_BOX_BYTES, &tmap_w, fb, col0 + 64, kb * BK);
-          tma_load_2d_pair(st + W_BYTES, &tmap_x, fb, kb * BK, row0);
+#pragma unroll
+          for (int h = 0; h < H; ++h)
+            tma_load_2d_pair(st + W_BYTES + h * x_bytes, &tmap_x, fb, kb * BK, row0 + h * p.nb);
           issued |= 1u << s;
           last_ph = (last_ph & ~(1u << s)) | (ph << s);
           if (++s == stages) { s = 0; ph ^= 1; }
@@ -272,8 +282,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         SegIter segs(p, pair, npairs);
         Seg g;
         for (; ok && segs.next(g); ++i) {
-          const int b = i & 1;
-          const uint32_t aph = (i >> 1) & 1;
+          const int b = NBUF == 2 ? i & 1 : 0;
+          const uint32_t aph = NBUF == 2 ? (i >> 1) & 1 : i & 1;
           if (!mbar_wait_spin(&bars.acc_empty[b], aph ^ 1, ctl, kSiteMmaAccEmpty)) break;
           tc_fence_after();
           const uint32_t d_tmem = tmem_base + b * MAX_NB;
@@ -285,8 +295,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
             for (int kk = 0; kk < BK / 16; ++kk) {
               // A: 128 weight columns of each CTA, N-major; B: nb / 2 rows of x of each CTA, K-major
               const uint64_t adesc = sdesc_sw128(w0 + kk * 2048, W_BOX_BYTES, 1024);
-              const uint64_t bdesc = sdesc_sw128(w0 + W_BYTES + kk * 32, 16, 1024);
-              umma_bf16_pair(d_tmem, adesc, bdesc, idesc, (kb != g.kb0 || kk != 0) ? 1u : 0u);
+#pragma unroll
+              for (int h = 0; h < H; ++h) {
+                const uint64_t bdesc = sdesc_sw128(w0 + W_BYTES + h * x_bytes + kk * 32, 16, 1024);
+                umma_bf16_pair(d_tmem + h * p.nb, adesc, bdesc, idesc, (kb != g.kb0 || kk != 0) ? 1u : 0u);
+              }
             }
             umma_commit_pair(&bars.empty[s], 0x3);
             if (++s == stages) { s = 0; ph ^= 1; }
@@ -307,15 +320,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     const int half = (warp - 2) >> 2;              // which of the quarter's two warps
     const int et = threadIdx.x - 64;               // 0..255
     const uint32_t acc_empty0 = dsmem_addr(&bars.acc_empty[0], 0);
-    const int chunks = p.nb / 32;
+    const int chunks = p.rows / 32;
     int i = 0;
     SegIter segs(p, pair, npairs);
     Seg g;
     for (; segs.next(g); ++i) {
       int mb, nb;
       tile_coords(g.tile, p, mb, nb);
-      const int b = i & 1;
-      const uint32_t aph = (i >> 1) & 1;
+      const int b = NBUF == 2 ? i & 1 : 0;
+      const uint32_t aph = NBUF == 2 ? (i >> 1) & 1 : i & 1;
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + b * MAX_NB;
       const int n = q * 32 + lane;                 // column within this CTA's 128
       const int64_t col0 = static_cast<int64_t>(nb) * BN + rank * 128 + q * 32;   // of this warp's 32 columns
@@ -325,7 +338,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         bias = make_float4(__ldg(p.epi.bias + min(c, last)), __ldg(p.epi.bias + min(c + 1, last)),
                            __ldg(p.epi.bias + min(c + 2, last)), __ldg(p.epi.bias + min(c + 3, last)));
       }
-      const int row0 = mb * p.nb;
+      const int row0 = mb * p.rows;
       // this warp's chunks of 16 rows: half, half + 2, ...; their residual DEPTH ahead
       constexpr int DEPTH = F32 ? 2 : 4;
       const bool ahead = !g.shared && p.vec && p.epi.residual;
@@ -336,9 +349,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
           epi_fetch<F32>(p.epi, lane, row0 + 16 * (half + 2 * d), min(p.M - row0 - 16 * (half + 2 * d), 16), col0, p.N, raw[d]);
       // One thread waits and the whole epilogue follows its decision, so the
       // group never splits at the named barriers or the .sync.aligned loads.
-      if (et == 0) bars.epi_ok[b] = mbar_wait_spin(&bars.acc_full[b], aph, ctl, kSiteEpiAccFull) ? 1 : 0;
+      if (et == 0) bars.epi_ok[i & 1] = mbar_wait_spin(&bars.acc_full[b], aph, ctl, kSiteEpiAccFull) ? 1 : 0;
       named_bar_sync(1, EPI_THREADS);
-      if (!bars.epi_ok[b]) break;
+      if (!bars.epi_ok[i & 1]) break;
       tc_fence_after();
       auto release = [&]() {
         // this CTA's epilogue has read TMEM buffer b
@@ -374,7 +387,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       // fix-up kernel adds them and finishes.
       const long long t0 = static_cast<long long>(g.tile - p.full) * p.kblocks;
       const int slot = static_cast<int>(blockIdx.x) * 2 + (share_begin(p, pair) >= t0 ? 0 : 1);
-      float4* mine = reinterpret_cast<float4*>(p.part + static_cast<int64_t>(slot) * SLOT_FLOATS);
+      float4* mine = reinterpret_cast<float4*>(p.part + static_cast<int64_t>(slot) * (p.rows * 128));
 #pragma unroll 1
       for (int c = half; c < chunks; c += 2) {
         float v[32];
@@ -405,48 +418,74 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
 
 // How a call is cut into tiles and shares.
 struct Plan {
-  int nb, num_m, num_n, kblocks, pairs, full, rest, sharers;
+  int h, nb, num_m, num_n, kblocks, pairs, full, rest, sharers;
+  double us;                       // estimate
+  int rows() const { return h * nb; }
 };
 
-Plan make_plan(int64_t M, int64_t K, int64_t N, int num_sms) {
+// One way to cut: tiles of h MMAs; the tiles of the last, partial round whole
+// (per_tile 0), shared evenly by per_tile pairs each, or by all pairs (-1).
+//
+// The estimate, from measurements of this kernel: a k step is bound by the
+// operand bytes that L2 delivers (75 GB/s to an SM while all read: 0.44 us at
+// 256 rows, 0.36 at 160) or by the tensor cores (0.30 us per 256 rows); the
+// last epilogue, and every one of the wide form, takes 4 us per 256 rows;
+// sharing costs a second kernel (6 us) and the partials' way through L2
+// (3.5 GB per ms).  1024 rows: 64 tiles of 256 x 256 with K 14336 took 129 us shared by
+// all pairs, and 109 us as 32 wide tiles.
+Plan make_plan(int h, int per_tile, int64_t M, int64_t K, int64_t N, int num_sms) {
   Plan q;
-  const int64_t blocks = (M + MAX_NB - 1) / MAX_NB;
+  q.h = h;
+  const int64_t blocks = (M + h * MAX_NB - 1) / (h * MAX_NB);
   q.num_m = static_cast<int>(blocks);
-  q.nb = static_cast<int>(((M + blocks - 1) / blocks + 31) / 32 * 32);
+  q.nb = static_cast<int>(((M + h * blocks - 1) / (h * blocks) + 31) / 32 * 32);
   q.num_n = static_cast<int>((N + BN - 1) / BN);
   q.kblocks = static_cast<int>((K + BK - 1) / BK);
   const int64_t tiles = static_cast<int64_t>(q.num_m) * q.num_n;
-  const int pairs = num_sms / 2;
-  const int64_t rest = tiles % pairs;
-  // At most 8 pairs to a tile (the last one reads all partials), at least 4 k
-  // blocks to a share.
-  const int64_t total = rest * q.kblocks;
-  int64_t sharers = pairs < rest * 8 ? pairs : rest * 8;
-  if (sharers > total / 4) sharers = total / 4;
-  // Sharing saves (1 - rest / sharers) of a tile's time, about 0.37 us per k
-  // block at 256 rows, and costs about 5 us.
-  const bool share = sharers > rest && q.kblocks * (sharers - rest) * q.nb > 14 * sharers * MAX_NB;
-  q.full = static_cast<int>(share ? tiles - rest : tiles);
-  q.rest = static_cast<int>(share ? rest : 0);
-  q.sharers = static_cast<int>(share ? sharers : 0);
-  q.pairs = tiles >= pairs ? pairs : share ? q.sharers : static_cast<int>(tiles);
+  const int64_t pairs = num_sms / 2;
+  const int64_t rest = per_tile ? tiles % pairs : 0;
+  // at most 8 pairs to a tile, at least 4 k blocks to a share
+  int64_t sharers = per_tile > 0 ? rest * per_tile : pairs < rest * 8 ? pairs : rest * 8;
+  if (sharers > rest * q.kblocks / 4) sharers = rest * q.kblocks / 4;
+  if (sharers > pairs || sharers <= rest) sharers = 0;
+  q.full = static_cast<int>(sharers ? tiles - rest : tiles);
+  q.rest = static_cast<int>(sharers ? rest : 0);
+  q.sharers = static_cast<int>(sharers);
+  q.pairs = static_cast<int>(tiles >= pairs ? pairs : sharers ? sharers : tiles);
+  const double step = std::max((W_BYTES + q.rows() * BK) / 75e3, q.rows() * 0.30 / 256);
+  const double epilogue = q.rows() * 4.0 / 256;
+  const double rounds = static_cast<double>((q.full + pairs - 1) / pairs);
+  q.us = rounds * q.kblocks * step + (h == 2 ? rounds : rounds > 0 ? 1 : 0) * epilogue;
+  if (sharers)
+    q.us += static_cast<double>(rest) * q.kblocks / sharers * step + epilogue + 6 +
+            static_cast<double>(sharers % rest ? sharers + rest : sharers) * q.rows() * BN * 4 / 3.5e6;
   return q;
 }
 
-template <bool F32>
+Plan best_plan(int64_t M, int64_t K, int64_t N, int num_sms) {
+  Plan best = make_plan(1, 0, M, K, N, num_sms);
+  for (int h = 1; h <= (M > MAX_NB ? 2 : 1); ++h)
+    for (int per_tile = -1; per_tile <= 8; ++per_tile) {
+      const Plan q = make_plan(h, per_tile, M, K, N, num_sms);
+      if (q.us < best.us) best = q;
+    }
+  return best;
+}
+
+template <bool F32, int H>
 cudaError_t launch_kernel(const Params& p, const Plan& q, cudaStream_t stream, const CUtensorMap& tx,
                           const CUtensorMap& tw) {
-  const cudaError_t e = ensure_smem_limit<proj_tile_kernel<F32>>(static_cast<int>(SMEM));
+  const cudaError_t e = ensure_smem_limit<proj_tile_kernel<F32, H>>(static_cast<int>(SMEM));
   if (e != cudaSuccess) return e;
-  return launch_pdl(proj_tile_kernel<F32>, static_cast<unsigned>(2 * q.pairs), NUM_THREADS, SMEM, stream, tx, tw, p);
+  return launch_pdl(proj_tile_kernel<F32, H>, static_cast<unsigned>(2 * q.pairs), NUM_THREADS, SMEM, stream, tx, tw, p);
 }
 
 }  // namespace ptile
 
 size_t proj_tile_workspace_bytes(int64_t M, int64_t K, int64_t N, int num_sms) {
-  const ptile::Plan q = ptile::make_plan(M, K, N, num_sms);
+  const ptile::Plan q = ptile::best_plan(M, K, N, num_sms);
   if (q.rest == 0) return kWsHeaderBytes;
-  return kWsHeaderBytes + static_cast<size_t>(q.pairs) * 2 * 2 * ptile::SLOT_FLOATS * 4;
+  return kWsHeaderBytes + static_cast<size_t>(q.pairs) * 2 * 2 * q.rows() * 128 * 4;
 }
 
 int64_t proj_tile_count(int64_t M, int64_t N) {
@@ -455,7 +494,7 @@ int64_t proj_tile_count(int64_t M, int64_t N) {
 
 cudaError_t launch_proj_tile(const ProjArgs& a) {
   using namespace ptile;
-  const Plan q = make_plan(a.M, a.K, a.N, a.num_sms);
+  const Plan q = best_plan(a.M, a.K, a.N, a.num_sms);
   CUtensorMap tx, tw;
   if (!make_tmap_2d_ld(&tx, a.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.M, a.K, a.ldx, q.nb / 2, BK))
     return cudaErrorInvalidValue;
@@ -465,19 +504,19 @@ cudaError_t launch_proj_tile(const ProjArgs& a) {
   p.M = static_cast<int>(a.M);
   p.N = static_cast<int>(a.N);
   p.nb = q.nb;
+  p.rows = q.rows();
   p.num_m = q.num_m;
   p.num_n = q.num_n;
   p.kblocks = q.kblocks;
   // Raster band: as many row blocks as keep the band's x within about 40 MB
   // of L2 (at most 16), so the weight is fetched once per band.
   const int64_t band_rows = (40ll << 20) / (a.K * 2);
-  p.group_m = static_cast<int>(band_rows / q.nb);
-  if (p.group_m < 1) p.group_m = 1;
-  if (p.group_m > 16) p.group_m = 16;
+  const int64_t most = 16 * MAX_NB / p.rows;
+  p.group_m = static_cast<int>(std::max<int64_t>(1, std::min(band_rows / p.rows, most)));
   p.full = q.full;
   p.rest = q.rest;
   p.sharers = q.sharers;
-  const int stage_bytes = W_BYTES + q.nb * BK;
+  const int stage_bytes = W_BYTES + p.rows * BK;
   p.stages = RING_BYTES / stage_bytes;
   if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;
   p.epi = a.epi;
@@ -491,12 +530,14 @@ cudaError_t launch_proj_tile(const ProjArgs& a) {
   p.part = reinterpret_cast<float*>(ws + kWsHeaderBytes);
   p.budget_ns = a.budget_ns;
   p.withhold = a.withhold;
-  const cudaError_t l = a.epi.out_fp32 ? launch_kernel<true>(p, q, a.stream, tx, tw)
-                                       : launch_kernel<false>(p, q, a.stream, tx, tw);
+  const cudaError_t l = q.h == 2 ? (a.epi.out_fp32 ? launch_kernel<true, 2>(p, q, a.stream, tx, tw)
+                                                   : launch_kernel<false, 2>(p, q, a.stream, tx, tw))
+                                 : (a.epi.out_fp32 ? launch_kernel<true, 1>(p, q, a.stream, tx, tw)
+                                                   : launch_kernel<false, 1>(p, q, a.stream, tx, tw));
   if (l != cudaSuccess || q.rest == 0) return l;
   FixupArgs f = {};
   f.part = p.part;
-  f.slot_floats = SLOT_FLOATS;
+  f.slot_floats = p.rows * 128;
   f.total = static_cast<int64_t>(q.rest) * q.kblocks;
   f.kblocks = q.kblocks;
   f.sharers = q.sharers;
@@ -506,7 +547,7 @@ cudaError_t launch_proj_tile(const ProjArgs& a) {
   f.group_m = p.group_m;
   f.num_m = q.num_m;
   f.num_n = q.num_n;
-  f.rows = q.nb;
+  f.rows = p.rows;
   f.M = a.M;
   f.N = a.N;
   f.epi = a.epi;

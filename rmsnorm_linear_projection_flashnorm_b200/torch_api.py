@@ -10,7 +10,7 @@ import torch
 from . import (FN_T_BF16, FN_T_FP16, FN_T_FP32, FN_W_BF16, FN_W_FP8_E4M3_B128, FN_W_MXFP8_E4M3, check, fn_adaln_shift_bias, fn_norm_proj_adaln,
                fn_norm_proj_swiglu_nvfp4_swizzled, fn_workspace_size_adaln, fn_fold_weights, fn_norm_proj, fn_norm_proj_swiglu,
                fn_norm_proj_partial, fn_norm_proj_swiglu_nvfp4, fn_post_scale, fn_query_device_status,
-               fn_moe_swiglu, fn_proj, fn_workspace_size_moe, fn_workspace_size_proj, fn_token_logprobs, fn_token_logprobs_backward, fn_workspace_size)
+               fn_workspace_size, fn_workspace_size_moe, fn_workspace_size_proj, lib)
 
 
 def weight_type(Wp: torch.Tensor, scales: Optional[torch.Tensor]) -> int:
@@ -249,9 +249,23 @@ def _on(dev: torch.device, stream):
     return _Elsewhere(dev, stream)
 
 
+def _at(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
 def _handle(dev: torch.device) -> int:
     """The device's current stream, without the Stream object around it."""
     return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _workspace(ws: Optional[Workspace], dev: torch.device, need: int) -> torch.Tensor:
+    """The caller's workspace, grown to `need` bytes, or one for this call."""
+    if ws is None:
+        return torch.zeros(need, dtype=torch.uint8, device=dev)
+    buf = ws.reserve(need)
+    if buf.device != dev:
+        raise ValueError(f"workspace on {buf.device}, tensors on {dev}")
+    return buf
 
 
 _ACT = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
@@ -293,11 +307,10 @@ def proj(x: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None, 
             ldx = (ldx + 7) // 8 * 8
         if K == 1:
             ldw = (ldw + 7) // 8 * 8
-        if ws is None:
-            ws = Workspace(dev)
-        buf = ws.reserve(fn_workspace_size_proj(M, K, N))
-        check(fn_proj(x, ldx, M, K, W, ldw, N, bias, _ACT[act], residual, ldr, _DTYPE[out.dtype], out, ldy, buf,
-                      buf.numel(), _handle(dev)), "fn_proj")
+        buf = _workspace(ws, dev, fn_workspace_size_proj(M, K, N))
+        check(lib().fn_proj(x.data_ptr(), ldx, M, K, W.data_ptr(), ldw, N, _at(bias), _ACT[act], _at(residual), ldr,
+                            _DTYPE[out.dtype], out.data_ptr(), ldy, buf.data_ptr(), buf.numel(), _handle(dev)),
+              "fn_proj")
     return out
 
 
@@ -352,11 +365,11 @@ def moe_swiglu(x: torch.Tensor, g: Optional[torch.Tensor], router: torch.Tensor,
             out = torch.empty(M, d, dtype=bf, device=dev)
         ids = torch.empty(M, top_k, dtype=torch.int32, device=dev)
         w = torch.empty(M, top_k, dtype=torch.float32, device=dev)
-        if ws is None:
-            ws = Workspace(dev)
-        buf = ws.reserve(fn_workspace_size_moe(M, d, I, E, top_k))
-        check(fn_moe_swiglu(x, M, d, g, router, E, Wgu, Wd, I, top_k, _SCORE[score], select_bias, renorm, route_scale,
-                            eps, residual, out, ids, w, buf, buf.numel(), _handle(dev)), "fn_moe_swiglu")
+        buf = _workspace(ws, dev, fn_workspace_size_moe(M, d, I, E, top_k))
+        check(lib().fn_moe_swiglu(x.data_ptr(), M, d, _at(g), router.data_ptr(), E, Wgu.data_ptr(), Wd.data_ptr(), I,
+                                  top_k, _SCORE[score], _at(select_bias), 1 if renorm else 0, route_scale, eps,
+                                  _at(residual), out.data_ptr(), ids.data_ptr(), w.data_ptr(), buf.data_ptr(),
+                                  buf.numel(), _handle(dev)), "fn_moe_swiglu")
     return out, ids, w
 
 
@@ -389,9 +402,10 @@ def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None,
             _vec(out.lse, "lse", torch.float32, M, dev)
             _dense(out.top_ids, "top_ids", torch.int32, (M, top_k), dev)
             _dense(out.top_logprobs, "top_logprobs", torch.float32, (M, top_k), dev)
-        check(fn_token_logprobs(logits, _DTYPE[logits.dtype], M, V, ld, targets, scale, top_k, out.logprob,
-                                out.entropy, out.lse, out.top_ids if top_k else None,
-                                out.top_logprobs if top_k else None, _handle(dev)), "fn_token_logprobs")
+        lp, ent, lse, ids, top = out
+        check(lib().fn_token_logprobs(logits.data_ptr(), _DTYPE[logits.dtype], M, V, ld, _at(targets), scale, top_k,
+                                      _at(lp), _at(ent), _at(lse), ids.data_ptr() if top_k else None,
+                                      top.data_ptr() if top_k else None, _handle(dev)), "fn_token_logprobs")
     return out
 
 
@@ -415,6 +429,7 @@ def token_logprobs_backward(logits: torch.Tensor, targets: Optional[torch.Tensor
         ldd = _rows(out, "out", (logits.dtype,), (M, V))
         if out.device != dev:
             raise ValueError(f"out on {out.device}, logits on {dev}")
-        check(fn_token_logprobs_backward(logits, _DTYPE[logits.dtype], M, V, ld, targets, lse, entropy, grad_logprob,
-                                         grad_entropy, scale, out, ldd, _handle(dev)), "fn_token_logprobs_backward")
+        check(lib().fn_token_logprobs_backward(logits.data_ptr(), _DTYPE[logits.dtype], M, V, ld, _at(targets),
+                                               lse.data_ptr(), _at(entropy), _at(grad_logprob), _at(grad_entropy),
+                                               scale, out.data_ptr(), ldd, _handle(dev)), "fn_token_logprobs_backward")
     return out
