@@ -155,18 +155,12 @@ __device__ __forceinline__ void epi_fetch(const Epilogue& e, int lane, int64_t r
   }
 }
 
-template <bool F32>
-__device__ __forceinline__ void epi_finish_16x32(const Epilogue& e, bool vec, const typename Quad<F32>::Raw (&raw)[4],
-                                                 float* scratch, int lane, int64_t row0, int rows, int64_t col0,
-                                                 int64_t N, const float4& bias, const float (&v)[16]) {
-  using Q = Quad<F32>;
-  using T = typename Q::Raw;
-  const int64_t col = col0 + lane % 8 * 4;
-  const int cols = static_cast<int>(col < N ? (N - col < 4 ? N - col : 4) : 0);
+// Transpose to 4 rows of 4 columns, add the bias, apply the activation.
+__device__ __forceinline__ void epi_transpose_act(const Epilogue& e, float* scratch, int lane, const float4& bias,
+                                                  const uint32_t (&v)[16], float (&z)[16]) {
 #pragma unroll
-  for (int j = 0; j < 16; ++j) scratch[j * SCRATCH_LD + lane] = v[j];
+  for (int j = 0; j < 16; ++j) scratch[j * SCRATCH_LD + lane] = __uint_as_float(v[j]);
   __syncwarp();
-  float z[16];
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
     const float4 f = *reinterpret_cast<const float4*>(scratch + (g * 4 + lane / 8) * SCRATCH_LD + lane % 8 * 4);
@@ -174,25 +168,37 @@ __device__ __forceinline__ void epi_finish_16x32(const Epilogue& e, bool vec, co
   }
   __syncwarp();
   epi_act<16>(e.act, z);
-  if (cols == 0) return;
-  if (vec) {
+}
+
+template <bool F32>
+__device__ __forceinline__ void epi_store_vec(const Epilogue& e, const typename Quad<F32>::Raw (&raw)[4], int lane,
+                                              int64_t row0, int rows, int64_t col0, int64_t N, float (&z)[16]) {
+  using Q = Quad<F32>;
+  using T = typename Q::Raw;
+  const int64_t col = col0 + lane % 8 * 4;
+  if (e.residual) {
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-      if (e.residual) {
-        float f[4];
-        Q::get(raw[g], f);
+      float f[4];
+      Q::get(raw[g], f);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) z[4 * g + j] += f[j];
-      }
-      const int r = g * 4 + lane / 8;
-      const int64_t at = (row0 + r) * e.ldy + col;
-      if (r < rows) {
-        if (F32) *reinterpret_cast<T*>(static_cast<float*>(e.y) + at) = Q::put(z + 4 * g);
-        else *reinterpret_cast<T*>(static_cast<__nv_bfloat16*>(e.y) + at) = Q::put(z + 4 * g);
-      }
+      for (int j = 0; j < 4; ++j) z[4 * g + j] += f[j];
     }
-    return;
   }
+  const int64_t at = (row0 + lane / 8) * e.ldy + col;
+  T* dst = F32 ? reinterpret_cast<T*>(static_cast<float*>(e.y) + at)
+               : reinterpret_cast<T*>(static_cast<__nv_bfloat16*>(e.y) + at);
+#pragma unroll
+  for (int g = 0; g < 4; ++g)
+    if (g * 4 + lane / 8 < rows && col < N) dst[g * e.ldy] = Q::put(z + 4 * g);   // 4 rows are ldy groups of 4
+}
+
+template <bool F32>
+__device__ __forceinline__ void epi_store_scalar(const Epilogue& e, int lane, int64_t row0, int rows, int64_t col0,
+                                                 int64_t N, float (&z)[16]) {
+  const int64_t col = col0 + lane % 8 * 4;
+  const int cols = static_cast<int>(col < N ? (N - col < 4 ? N - col : 4) : 0);
+  if (cols == 0) return;
   float res[16];
 #pragma unroll
   for (int j = 0; j < 16; ++j) {

@@ -65,6 +65,7 @@ struct Params {
   int full;                        // tiles that run whole
   int rest;                        // tiles whose k blocks are shared between pairs
   int sharers;                     // pairs that take a share of them (each at least one k block)
+  int share_q, share_r;            // rest * kblocks by sharers: quotient, remainder
   int stages;
   Epilogue epi;
   int vec;                         // the epilogue's vector form applies
@@ -91,8 +92,10 @@ constexpr size_t SMEM = 1024 + RING_BYTES + SCRATCH_BYTES + sizeof(Bars);
 static_assert(SMEM <= 232448, "shared memory budget");
 
 // First of the shared tiles' k blocks that pair c takes.
-__device__ __forceinline__ long long share_begin(const Params& p, int c) {
-  return c * (static_cast<long long>(p.rest) * p.kblocks) / p.sharers;
+// (c rest kblocks / sharers, with rest kblocks = share_q sharers + share_r: 32
+// bits, as 64-bit divisions would stand before the first load.)
+__device__ __forceinline__ int share_begin(const Params& p, int c) {
+  return c * p.share_q + static_cast<int>(static_cast<unsigned>(c * p.share_r) / static_cast<unsigned>(p.sharers));
 }
 
 // Segment i of a pair: a whole tile, or its part of the shared tiles.
@@ -102,7 +105,7 @@ struct Seg {
 };
 struct SegIter {
   int npairs, full, kblocks, next_tile;
-  long long it, end;
+  int it, end;
   __device__ SegIter(const Params& p, int pair, int npairs_)
       : npairs(npairs_), full(p.full), kblocks(p.kblocks), next_tile(pair), it(0), end(0) {
     if (pair < p.sharers) {
@@ -120,10 +123,10 @@ struct SegIter {
       return true;
     }
     if (it >= end) return false;
-    const int r = static_cast<int>(it / kblocks);
+    const int r = it / kblocks;
     s.tile = full + r;
-    s.kb0 = static_cast<int>(it - static_cast<long long>(r) * kblocks);
-    s.kb1 = static_cast<int>(min(static_cast<long long>(kblocks), s.kb0 + (end - it)));
+    s.kb0 = it - r * kblocks;
+    s.kb1 = min(kblocks, s.kb0 + (end - it));
     s.shared = s.kb0 != 0 || s.kb1 != kblocks;
     it += s.kb1 - s.kb0;
     return true;
@@ -340,7 +343,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       }
       const int row0 = mb * p.rows;
       // this warp's chunks of 16 rows: half, half + 2, ...; their residual DEPTH ahead
-      constexpr int DEPTH = F32 ? 2 : 4;
+      constexpr int DEPTH = F32 ? 2 : 3;
       const bool ahead = !g.shared && p.vec && p.epi.residual;
       typename Quad<F32>::Raw raw[DEPTH][4];
       if (ahead)
@@ -365,19 +368,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       };
       if (!g.shared) {
         float* scratch = reinterpret_cast<float*>(smem + RING_BYTES) + (warp - 2) * SCRATCH_FLOATS;
+        // One copy of the code for every chunk: unrolled by four it took 6 us per
+        // tile of 256 rows to fetch and run.
+        if (p.vec) {
 #pragma unroll 1
-        for (int c0 = half; c0 < 2 * chunks; c0 += 2 * DEPTH) {
+          for (int c = half; c < 2 * chunks; c += 2) {
+            const int r0 = row0 + 16 * c, rn = r0 + 32 * DEPTH;
+            if (r0 >= p.M) break;
+            uint32_t v[16];
+            float z[16];
+            tmem_ld16(taddr + c * 16, v);
+            tmem_ld_wait();
+            epi_transpose_act(p.epi, scratch, lane, bias, v, z);
+            epi_store_vec<F32>(p.epi, raw[0], lane, r0, min(p.M - r0, 16), col0, p.N, z);
 #pragma unroll
-          for (int d = 0; d < DEPTH; ++d) {
-            const int c = c0 + 2 * d, r0 = row0 + 16 * c;
-            if (c < 2 * chunks && r0 < p.M) {
-              float v[16];
-              dec::tmem_ld_cols<16>(taddr + c * 16, v);
-              epi_finish_16x32<F32>(p.epi, p.vec, raw[d], scratch, lane, r0, min(p.M - r0, 16), col0, p.N, bias, v);
-              const int rn = r0 + 32 * DEPTH;
-              if (ahead && c + 2 * DEPTH < 2 * chunks)
-                epi_fetch<F32>(p.epi, lane, rn, min(p.M - rn, 16), col0, p.N, raw[d]);
-            }
+            for (int d = 0; d + 1 < DEPTH; ++d)
+#pragma unroll
+              for (int g = 0; g < 4; ++g) raw[d][g] = raw[d + 1][g];
+            if (ahead && c + 2 * DEPTH < 2 * chunks)
+              epi_fetch<F32>(p.epi, lane, rn, min(p.M - rn, 16), col0, p.N, raw[DEPTH - 1]);
+          }
+        } else {
+#pragma unroll 1
+          for (int c = half; c < 2 * chunks; c += 2) {
+            const int r0 = row0 + 16 * c;
+            if (r0 >= p.M) break;
+            uint32_t v[16];
+            float z[16];
+            tmem_ld16(taddr + c * 16, v);
+            tmem_ld_wait();
+            epi_transpose_act(p.epi, scratch, lane, bias, v, z);
+            epi_store_scalar<F32>(p.epi, lane, r0, min(p.M - r0, 16), col0, p.N, z);
           }
         }
         release();
@@ -385,7 +406,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       }
       // Shared tile: publish the partial (float4 groups [row / 4][column]); the
       // fix-up kernel adds them and finishes.
-      const long long t0 = static_cast<long long>(g.tile - p.full) * p.kblocks;
+      const int t0 = (g.tile - p.full) * p.kblocks;
       const int slot = static_cast<int>(blockIdx.x) * 2 + (share_begin(p, pair) >= t0 ? 0 : 1);
       float4* mine = reinterpret_cast<float4*>(p.part + static_cast<int64_t>(slot) * (p.rows * 128));
 #pragma unroll 1
@@ -516,6 +537,10 @@ cudaError_t launch_proj_tile(const ProjArgs& a) {
   p.full = q.full;
   p.rest = q.rest;
   p.sharers = q.sharers;
+  if (q.sharers) {
+    p.share_q = q.rest * q.kblocks / q.sharers;
+    p.share_r = q.rest * q.kblocks % q.sharers;
+  }
   const int stage_bytes = W_BYTES + p.rows * BK;
   p.stages = RING_BYTES / stage_bytes;
   if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;
