@@ -29,12 +29,12 @@
 //     k-th largest of their maxima.
 // What a warp does per survivor decides the speed (at 8 alternatives of 131072
 // logits, 130 instructions for each survivor of the warps' own thresholds
-// doubled the kernel's time), so vectors with a survivor are only queued; 32 of
-// them at a time give up their keys.  A warp whose buffer fills sorts it into a
-// list of its 32 largest; most rows end before that.  At the end a key's place
-// is the number of keys above it, which a thread counts for each.  Logits of
-// -inf never survive; where fewer than k others are left, the row's first ones
-// fill the places.
+// doubled the kernel's time), so a thread that holds one only queues the place
+// of its vectors; 32 of them at a time are read again and give up their keys.
+// A warp whose buffer fills sorts it into a list of its 32 largest; most rows
+// end before that.  At the end a key's place is the number of keys above it,
+// which a thread counts for each.  Logits of -inf never survive; where fewer
+// than k others are left, the row's first ones fill the places.
 //
 // Work split: one thread-block cluster per row; C = 1, 2, 4 or 8 CTAs, more
 // when there are few rows, so one decoded token still uses 8 SMs.  The CTAs'
@@ -51,12 +51,10 @@
 namespace fn {
 namespace lp {
 
-constexpr int THREADS = 256;
-constexpr int WARPS = THREADS / 32;
+constexpr int MAX_THREADS = 256;
 constexpr int VECS = 4;                       // 16-byte vectors per thread and tile
 constexpr int MAX_K = kMaxTopAlternatives;    // 32: one key per lane
 constexpr int STAGES = 2;                     // tiles in flight
-constexpr int TILE = THREADS * VECS;          // 16-byte vectors
 constexpr int CROWD = 12;                     // lanes with survivors from which the threshold is raised first
 constexpr float FAR = -200.f;                 // 2^FAR is 0 in fp32: nothing below it counts
 constexpr float LOG2E = 1.4426950408889634f;
@@ -267,14 +265,15 @@ __device__ __forceinline__ Stat merge_stat(const Stat& a, const Stat& b, float c
   return r;
 }
 
+template <int THREADS>
 struct Smem {
+  static constexpr int WARPS = THREADS / 32, TILE = THREADS * VECS;   // of 16-byte vectors
   union {
     uint4 stage[STAGES][TILE];
     Key pool[WARPS * 64];        // at the end: what the warps kept, then what the ranks kept
   };
-  uint4 queue[WARPS][64];        // vectors with survivors
   Key buf[WARPS][64];            // survivors
-  int queue_at[WARPS][64];       // their first logit
+  int queue[WARPS][64];          // first vectors of threads with survivors
   Key top[32];                   // this CTA's result, read by rank 0 of the cluster
   Key thr;                       // largest of the warps' k-th keys
   int pooled;                    // keys in the pool
@@ -289,7 +288,8 @@ __device__ __forceinline__ void copy_async(uint4* dst, const uint4* src) {
 
 // The k largest of the n unique keys in sm.pool, largest first, to sm.top.  All
 // threads call, behind a barrier; ends with one.
-__device__ __forceinline__ void select_top(Smem& sm, int n, int k) {
+template <int THREADS>
+__device__ __forceinline__ void select_top(Smem<THREADS>& sm, int n, int k) {
   for (int i = static_cast<int>(threadIdx.x); i < n; i += THREADS) {
     const Key key = sm.pool[i];
     int above = 0;
@@ -310,11 +310,12 @@ struct Params {
   int* top_ids;
 };
 
-template <typename T, bool TOPK>
-__global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const Params p) {
+template <typename T, bool TOPK, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const Params p) {
   using E = Elem<T>;
   constexpr int N = E::N;
-  __shared__ Smem sm;
+  constexpr int WARPS = THREADS / 32, TILE = THREADS * VECS;
+  __shared__ Smem<THREADS> sm;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(blockIdx.x % p.C);
   const int64_t row = blockIdx.x / p.C;
@@ -386,40 +387,46 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const Params p) {
     pending += __popc(b);
     if (pending >= 32) flush();
   };
-  auto process = [&]() {                      // the first 32 vectors of the queue
+  auto process = [&]() {                      // the first 32 of the queue
     __syncwarp();
-    uint32_t mask = 0;
-    float f[N] = {};
-    int at = 0;
-    if (lane < queued) {
-      E::unpack(sm.queue[warp][lane], f);
-      at = sm.queue_at[warp][lane];
-      mask = (1u << N) - 1u;
-    }
-    // candidates, again whenever a flush has raised the threshold (long ties)
-    Key seen = thr;
-    auto filter = [&]() {
+    uint32_t mask = 0;                        // candidates of this lane's VECS vectors
+    int v = 0;
+    Key seen;
+    auto filter = [&](uint32_t among) {
       seen = thr;
+      mask = 0;
 #pragma unroll
-      for (int e = 0; e < N; ++e)
-        if (f[e] < thr_v || (f[e] == thr_v && static_cast<uint32_t>(at + e) > thr_i)) mask &= ~(1u << e);
+      for (int j = 0; j < VECS; ++j) {
+        if ((among >> (j * N) & ((1u << N) - 1u)) && v + j * THREADS < v1) {
+          float f[N];
+          E::unpack(__ldg(xv + v + j * THREADS), f);
+          const uint32_t i0 = static_cast<uint32_t>(head + (v + j * THREADS) * N);
+#pragma unroll
+          for (int e = 0; e < N; ++e)
+            if (!(f[e] < thr_v) && !(f[e] == thr_v && i0 + e > thr_i)) mask |= 1u << (j * N + e);
+        }
+      }
+      mask &= among;
     };
-    filter();
+    if (lane < queued) {
+      v = sm.queue[warp][lane];
+      filter(0xFFFFFFFFu);
+    }
     while (__any_sync(0xffffffffu, mask != 0)) {
-      const int e = __ffs(static_cast<int>(mask)) - 1;      // the lane's next candidate
-      float fe = f[0];
-#pragma unroll
-      for (int i = 1; i < N; ++i) fe = e == i ? f[i] : fe;
-      const Key k = make_key(fe, static_cast<uint32_t>(at + e));
-      append(mask != 0 && k > thr, k);
-      mask &= mask - 1;
-      if (thr != seen) filter();
+      Key k = 0;                              // the lane's next candidate
+      if (mask) {
+        const int b = __ffs(static_cast<int>(mask)) - 1;
+        const int i = head + (v + b / N * THREADS) * N + b % N;
+        k = make_key(E::load(x + i), static_cast<uint32_t>(i));
+        mask &= mask - 1;
+      }
+      seen = thr;
+      append(k > thr, k);
+      if (thr != seen && mask) filter(mask);  // a flush has raised the threshold (long ties)
     }
-    if (lane + 32 < queued) {
-      const uint4 v = sm.queue[warp][32 + lane];
-      sm.queue[warp][lane] = v;
-      sm.queue_at[warp][lane] = sm.queue_at[warp][32 + lane];
-    }
+    const int rest = sm.queue[warp][32 + lane];
+    __syncwarp();
+    sm.queue[warp][lane] = rest;
     queued = max(queued - 32, 0);
     __syncwarp();
   };
@@ -538,42 +545,21 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const Params p) {
         raise(bound);
         __syncthreads();
       }
-      const uint32_t hit = __ballot_sync(0xffffffffu, have && !(bm < thr_v));
+      const int v = base + static_cast<int>(threadIdx.x);
+      auto holds = [&]() {
+        return have && !(bm < thr_v) && !(bm == thr_v && static_cast<uint32_t>(head + v * N) > thr_i);
+      };
+      uint32_t hit = __ballot_sync(0xffffffffu, holds());
+      if (__popc(hit) > CROWD) {
+        raise(*static_cast<volatile Key*>(&sm.thr));      // any earlier value is a bound too
+        const uint32_t kth = __shfl_sync(0xffffffffu, warp_sort(have ? ordered(bm) : 0u, lane), p.k - 1);
+        if (kth) raise((static_cast<Key>(kth) << 32) - 1);
+        hit = __ballot_sync(0xffffffffu, holds());
+      }
       if (hit) {
-        const int i0 = head + (base + static_cast<int>(threadIdx.x)) * N;
-        if (__popc(hit) > CROWD) {
-          raise(*static_cast<volatile Key*>(&sm.thr));    // any earlier value is a bound too
-          const uint32_t o = warp_sort(have ? ordered(bm) : 0u, lane);
-          const uint32_t kth = __shfl_sync(0xffffffffu, o, p.k - 1);
-          if (kth) raise((static_cast<Key>(kth) << 32) - 1);
-        }
-        uint32_t mine = (1u << have) - 1u;    // this thread's vectors with survivors
-        Key seen;
-        auto filter = [&]() {
-          seen = thr;
-#pragma unroll
-          for (int j = 0; j < VECS; ++j) {
-            if (j < have) {
-              const float vm = E::wvalue(vmax<T>(q[j]));
-              if (vm < thr_v || (vm == thr_v && static_cast<uint32_t>(i0 + j * THREADS * N) > thr_i)) mine &= ~(1u << j);
-            }
-          }
-        };
-        filter();
-        while (true) {
-          const uint32_t b = __ballot_sync(0xffffffffu, mine != 0);
-          if (b == 0) break;
-          if (mine) {
-            const int j = __ffs(static_cast<int>(mine)) - 1;
-            const int at = queued + __popc(b & ((1u << lane) - 1u));
-            sm.queue[warp][at] = j == 0 ? q[0] : j == 1 ? q[1] : j == 2 ? q[2] : q[3];
-            sm.queue_at[warp][at] = i0 + j * THREADS * N;
-            mine &= mine - 1;
-          }
-          queued += __popc(b);
-          if (queued >= 32) process();
-          if (thr != seen) filter();
-        }
+        if (hit >> lane & 1u) sm.queue[warp][queued + __popc(hit & ((1u << lane) - 1u))] = v;
+        queued += __popc(hit);
+        if (queued >= 32) process();
       }
     }
   }
@@ -611,7 +597,7 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const Params p) {
     for (int w = 1; w < WARPS; ++w) a = merge_stat(a, sm.wstat[w], c);
     sm.stat = a;
   }
-  if (p.C > 1) {
+  if (THREADS == MAX_THREADS && p.C > 1) {    // warp w serves rank w
     cluster_sync_all();
     if (rank == 0) {
       // warp w fetches rank w's results
@@ -692,17 +678,22 @@ cudaError_t launch_fwd(const LogprobArgs& a) {
   p.top_logprobs = a.top_logprobs;
   // CTAs per row: as many as keep every CTA at least one full tile and the
   // grid within two waves of the 4 CTAs an SM holds
-  constexpr int64_t LOGITS = static_cast<int64_t>(TILE) * Elem<T>::N;
+  constexpr int64_t LOGITS = static_cast<int64_t>(MAX_THREADS) * VECS * Elem<T>::N;
   int C = 1;
   while (C < 8 && a.M * C * 2 <= 8LL * a.num_sms && a.V >= LOGITS * C * 2) C *= 2;
   p.C = C;
   const unsigned grid = static_cast<unsigned>(a.M * C);
+  // CTAs of 4 warps where the rows alone fill the SMs: what a warp does per row
+  // apart from its logits (thresholds, survivors, sums) is then done half as often
+  if (C == 1 && a.M * 2 > 8LL * a.num_sms)
+    return a.top_k > 0 ? launch_pdl(logprobs_kernel<T, true, 128>, grid, 128, 0, a.stream, p)
+                       : launch_pdl(logprobs_kernel<T, false, 128>, grid, 128, 0, a.stream, p);
   if (a.top_k > 0) {
-    return C > 1 ? launch_pdl_cluster(logprobs_kernel<T, true>, grid, C, THREADS, 0, a.stream, p)
-                 : launch_pdl(logprobs_kernel<T, true>, grid, THREADS, 0, a.stream, p);
+    return C > 1 ? launch_pdl_cluster(logprobs_kernel<T, true, MAX_THREADS>, grid, C, MAX_THREADS, 0, a.stream, p)
+                 : launch_pdl(logprobs_kernel<T, true, MAX_THREADS>, grid, MAX_THREADS, 0, a.stream, p);
   }
-  return C > 1 ? launch_pdl_cluster(logprobs_kernel<T, false>, grid, C, THREADS, 0, a.stream, p)
-               : launch_pdl(logprobs_kernel<T, false>, grid, THREADS, 0, a.stream, p);
+  return C > 1 ? launch_pdl_cluster(logprobs_kernel<T, false, MAX_THREADS>, grid, C, MAX_THREADS, 0, a.stream, p)
+               : launch_pdl(logprobs_kernel<T, false, MAX_THREADS>, grid, MAX_THREADS, 0, a.stream, p);
 }
 
 // ---------------------------------------------------------------------------
@@ -712,6 +703,7 @@ cudaError_t launch_fwd(const LogprobArgs& a) {
 // p_v = e^{z_v - lse}: one read and one write of the row, bound by HBM.  A
 // thread reads and writes the same elements, so the gradient may overwrite
 // the logits.
+constexpr int THREADS = 256;     // of the gradient kernel
 constexpr int BWD_VECS = 4;
 
 struct BwdParams {
