@@ -395,3 +395,22 @@ def test_decode_step_of_a_block_through_one_workspace():
     close(lp.logprob, elp, 1e-5)
     close(lp.entropy, eH, 1e-5)
     assert np.array_equal(lp.top_ids.cpu().numpy(), eids)
+
+
+@pytest.mark.gpu
+def test_weights_past_32_bits():
+    """Experts whose weights lie past 2^31 elements."""
+    d, I, E = 4096, 4096, 72                                # 72 x 4096 x 8192 elements of gate/up
+    layer = Layer.__new__(Layer)
+    layer.d, layer.I, layer.E, layer.g = d, I, E, None
+    g = torch.Generator(device="cuda").manual_seed(3)
+    layer.router = (torch.randn(E, d, generator=g, device="cuda") * d ** -0.5).bfloat16()
+    layer.Wgu = torch.empty(E, d, 2 * I, dtype=torch.bfloat16, device="cuda")
+    layer.down = torch.empty(E, I, d, dtype=torch.bfloat16, device="cuda")
+    for e in range(E):
+        layer.Wgu[e] = torch.randn(d, 2 * I, generator=g, device="cuda", dtype=torch.bfloat16) * d ** -0.5
+        layer.down[e] = torch.randn(I, d, generator=g, device="cuda", dtype=torch.bfloat16) * 2 * I ** -0.5
+    sb = torch.zeros(E, device="cuda")
+    sb[torch.tensor([0, 68, 70, 71])] = 10.0                # the first and the last experts
+    for M in (1, 20):
+        check(layer, M, 4, select_bias=sb)

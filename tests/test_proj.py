@@ -259,3 +259,66 @@ def test_timeout_is_reported(M):
     y = T.proj(x, w, ws=ws)
     torch.cuda.synchronize()
     assert ws.status()[0] == fnb.FN_OK and torch.isfinite(y).all()
+
+
+def aligned(M, K, N, fp32, residual, act, seed):
+    """Contiguous output and residual: the epilogue's vector form where N is a
+    multiple of 4.  What the tolerance counts is in the module's docstring."""
+    x, w = padded(M, K, up8(K), seed), padded(K, N, up8(N), seed + 1, K ** -0.5)
+    g = torch.Generator().manual_seed(seed + 2)
+    b = torch.randn(N, generator=g).cuda()
+    dt = torch.float32 if fp32 else torch.bfloat16
+    r = torch.randn(M, N, generator=g).to(dt).cuda() if residual else None
+    y = T.proj(x, w, bias=b, act=act, residual=r, out_dtype=dt)
+    torch.cuda.synchronize()
+    xd, wd = x.double(), w.double()
+    z = xd @ wd + b.double()
+    ref = z * torch.sigmoid(z) if act == "silu" else z
+    if residual:
+        ref = ref + r.double()
+    tol = 1.2 * ((8 + math.sqrt(K)) * 2 * U * (xd.abs() @ wd.abs()) + U * z.abs()) + 16 * U * z.abs()
+    tol = tol + U * ref.abs() + (U * r.double().abs() if residual else 0)
+    tol = tol + torch.finfo(dt).eps / 2 * ref.abs() * (1 + 2 ** -7) + 1e-30
+    over = (y.double() - ref).abs() - tol
+    assert not torch.isnan(y).any() and over.max() <= 0, over.max()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fp32", [False, True])
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("M,K,N", [(65, 200, 128), (100, 512, 260), (257, 333, 1000), (300, 14336, 1024), (512, 16384, 512),
+                                   (1000, 256, 4100), (4099, 128, 516), (700, 8192, 2052)])
+def test_aligned_output(M, K, N, fp32, residual):
+    aligned(M, K, N, fp32, residual, "silu" if M == 257 else "none", seed=M + N)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,K,N", [(5, 64, 1 << 16), (64, 128, 1 << 15)])
+def test_aligned_output_few_rows(M, K, N):
+    aligned(M, K, N, False, True, "none", seed=1)
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits():
+    """Output, residual (in place) and weight rows whose element offsets pass
+    2^31: the last rows and columns are right, and the first are not theirs."""
+    M, K, N = 66000, 64, 33000
+    x, w = padded(M, K, K, 1), padded(K, N, N, 2, K ** -0.5)
+    y = torch.ones(M, N, dtype=torch.bfloat16, device="cuda")
+    T.proj(x, w, residual=y, out=y)
+    torch.cuda.synchronize()
+    rows = torch.tensor([0, 1, 255, 256, M // 2, M - 257, M - 2, M - 1], device="cuda")
+    ref = x[rows].double() @ w.double() + 1
+    tol = 2 ** -8 * ref.abs() * (1 + 2 ** -7) + (8 + math.sqrt(K)) * 2 * U * (x[rows].double().abs() @ w.double().abs()) + 4 * U
+    assert ((y[rows].double() - ref).abs() <= tol).all()
+    del y
+    # a weight of more than 2^31 elements under few rows
+    K, N = 70000, 32768
+    x, w = padded(3, K, K, 3), torch.zeros(K, N, dtype=torch.bfloat16, device="cuda")
+    at = torch.tensor([0, 1, 65535, 65536, K - 2, K - 1], device="cuda")
+    w[at] = (torch.randn(len(at), N, device="cuda") * 0.5).bfloat16()
+    y = T.proj(x, w, out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    ref = x[:, at].double() @ w[at].double()
+    mag = x[:, at].double().abs() @ w[at].double().abs()
+    assert ((y.double() - ref).abs() <= (8 + math.sqrt(K)) * 2 * U * mag + U * ref.abs() + 1e-30).all()

@@ -408,3 +408,78 @@ def test_capture_streams_and_concurrent_calls():
     torch.cuda.synchronize()
     for a, b in outs:
         assert all(torch.equal(p, q) for p, q in zip(a, e)) and all(torch.equal(p, q) for p, q in zip(b, ref))
+
+
+def check_rows(x, t, k, scale):
+    """The forward pass against 64-bit torch on the device (many long rows).
+    The same tolerance as check_fwd."""
+    r = T.token_logprobs(x, t, top_k=k, scale=scale)
+    torch.cuda.synchronize()
+    V = x.shape[1]
+    ls = (4 * (math.log(V) + 1) + V / 128 + 69) * U       # a thread's share: at least 128 threads to a row
+    for a in range(0, x.shape[0], 64):
+        raw = x[a:a + 64].double()
+        z = raw * float(np.float32(scale))
+        lse = torch.logsumexp(z, 1)
+        q = z - lse[:, None]
+        H = -(torch.exp(q) * q.masked_fill(torch.isinf(q), 0)).sum(1)
+        lp = q.gather(1, t[a:a + 64].long()[:, None])[:, 0]
+        ids = torch.sort(raw, dim=1, descending=True, stable=True).indices[:, :k]
+        top = q.gather(1, ids)
+        big = raw.masked_fill(torch.isinf(raw), 0).abs().amax(1) * scale
+        assert torch.equal(r.top_ids[a:a + 64].long(), ids)
+        for got, ref, tol in ((r.logprob, lp, ls + 8 * U * (lp.abs() + 1)), (r.lse, lse, ls + 4 * U * (lse.abs() + big)),
+                              (r.entropy, H, 2 * ls * (1 + math.log(V)) + 4 * U * (H.abs() + 1)),
+                              (r.top_logprobs, top, ls + 8 * U * (top.abs() + 1))):
+            got = got[a:a + 64].double()
+            same = got == ref                              # -inf
+            assert (same | ((got - ref).abs() <= tol)).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,M,V,k,masked", [("bf16", 640, 140003, 8, 0.0), ("fp32", 601, 70001, 32, 0.5),
+                                                ("fp16", 1200, 33000, 1, 0.9), ("bf16", 300, 140003, 20, 0.0),
+                                                ("bf16", 9000, 1027, 5, 0.2)])
+def test_many_long_rows(dtype, M, V, k, masked):
+    g = torch.Generator(device="cuda").manual_seed(M)
+    x = torch.randn(M, V, generator=g, device="cuda") * 3
+    x[torch.rand(M, V, generator=g, device="cuda") < masked] = -math.inf
+    t = torch.randint(0, V, (M,), generator=g, device="cuda", dtype=torch.int32)
+    check_rows(x.to(DT[dtype]), t, k, 1.3)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("order", ["up", "flat", "saw"])
+def test_many_rows_in_order(order):
+    """Rows that fill the SMs by themselves and overflow the survivor buffers."""
+    V = 40007
+    i = torch.arange(V, dtype=torch.float32)
+    row = {"up": i / V * 20 - 10, "flat": torch.full((V,), 0.5), "saw": (i % 64) / 8}[order]
+    x = row.bfloat16().expand(620, V).contiguous().cuda()
+    check_rows(x, torch.arange(620, device="cuda", dtype=torch.int32), 32, 1.0)
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits():
+    """Rows whose first element lies past 2^31: forward and gradient of the
+    last rows, with the first rows as they were."""
+    M, V = 17000, 131000
+    x = torch.zeros(M, V, dtype=torch.bfloat16, device="cuda")
+    rows = torch.tensor([0, 1, M // 2, M - 2, M - 1], device="cuda")
+    x[rows] = (torch.randn(len(rows), V, device="cuda") * 3).bfloat16()
+    t = torch.full((M,), 5, device="cuda", dtype=torch.int32)
+    t[rows] = torch.tensor([V - 1, 7, V // 2, 3, V - 2], device="cuda", dtype=torch.int32)
+    r = T.token_logprobs(x, t, top_k=3)
+    torch.cuda.synchronize()
+    z = x[rows].double()
+    lse = torch.logsumexp(z, 1)
+    assert ((r.lse[rows].double() - lse).abs() <= 1e-5).all()
+    lp = z.gather(1, t[rows].long()[:, None])[:, 0] - lse
+    assert ((r.logprob[rows].double() - lp).abs() <= 2e-5).all()
+    assert torch.equal(r.top_ids[rows].long(), torch.sort(z, dim=1, descending=True, stable=True).indices[:, :3])
+    gl = torch.ones(M, device="cuda")
+    T.token_logprobs_backward(x, t, r.lse, r.entropy, gl, out=x)
+    torch.cuda.synchronize()
+    ref = -torch.exp(z - lse[:, None])
+    ref.scatter_add_(1, t[rows].long()[:, None], torch.ones(len(rows), 1, device="cuda", dtype=torch.float64))
+    assert ((x[rows].double() - ref).abs() <= 2 ** -8 * ref.abs() * (1 + 2 ** -6) + 1e-7).all()
