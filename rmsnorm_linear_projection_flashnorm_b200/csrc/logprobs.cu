@@ -703,8 +703,10 @@ cudaError_t launch_fwd(const LogprobArgs& a) {
 // p_v = e^{z_v - lse}: one read and one write of the row, bound by HBM.  A
 // thread reads and writes the same elements, so the gradient may overwrite
 // the logits.
-constexpr int THREADS = 256;     // of the gradient kernel
-constexpr int BWD_VECS = 4;
+// 8 vectors a thread and blocks of 128: 2048 x 131072 bf16 in 175 us (6.1 TB/s);
+// 4, 12 and 16 vectors took 187, 186 and 200 us with blocks of 256.
+constexpr int THREADS = 128;
+constexpr int BWD_VECS = 8;
 
 struct BwdParams {
   const void* logits;

@@ -208,20 +208,6 @@ def _dense(t: Optional[torch.Tensor], name: str, dtype, shape, dev) -> None:
         raise ValueError(f"{name}: contiguous {dtype} {shape} on {dev} is needed")
 
 
-class _Here:
-    """The tensors' device is the current one and the stream its current one:
-    nothing to switch."""
-
-    def __enter__(self):
-        return None
-
-    def __exit__(self, *exc):
-        return None
-
-
-_HERE = _Here()
-
-
 class _Elsewhere:
     """Another device than the current one, or a stream of the caller's
     (torch.cuda.Stream or a raw handle): what is allocated or zeroed inside
@@ -241,11 +227,13 @@ class _Elsewhere:
             part.__exit__(*exc)
 
 
-def _on(dev: torch.device, stream):
+def _elsewhere(dev: torch.device, stream) -> Optional[_Elsewhere]:
+    """None where the tensors' device is the current one and its current stream
+    is meant; else what to switch to (the callers then call themselves inside)."""
     if dev.type != "cuda":
         raise ValueError(f"tensors on {dev}: a CUDA device is needed")
     if stream is None and dev.index == torch.cuda.current_device():
-        return _HERE
+        return None
     return _Elsewhere(dev, stream)
 
 
@@ -289,28 +277,30 @@ def proj(x: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None, 
     if act not in _ACT:
         raise ValueError(f"act: one of {list(_ACT)}")
     _vec(bias, "bias", torch.float32, N, dev)
-    with _on(dev, stream):
-        if out is None:
-            dt = out_dtype or (residual.dtype if residual is not None else torch.bfloat16)
-            out = torch.empty(M, N, dtype=dt, device=dev)
-        ldy = _rows(out, "out", _BF16_FP32, (M, N))
-        if residual is None:
-            ldr = 0
-        elif residual is out:
-            ldr = ldy
-        else:
-            ldr = _rows(residual, "residual", (out.dtype,), (M, N))
-        if W.device != dev or out.device != dev or (residual is not None and residual.device != dev):
-            raise ValueError(f"every tensor must be on {dev}")
-        # a single row's stride is free: the library wants multiples of 8
-        if M <= 1:
-            ldx = (ldx + 7) // 8 * 8
-        if K == 1:
-            ldw = (ldw + 7) // 8 * 8
-        buf = _workspace(ws, dev, fn_workspace_size_proj(M, K, N))
-        check(lib().fn_proj(x.data_ptr(), ldx, M, K, W.data_ptr(), ldw, N, _at(bias), _ACT[act], _at(residual), ldr,
-                            _DTYPE[out.dtype], out.data_ptr(), ldy, buf.data_ptr(), buf.numel(), _handle(dev)),
-              "fn_proj")
+    other = _elsewhere(dev, stream)
+    if other is not None:
+        with other:
+            return proj(x, W, bias, act, residual, ws, out, out_dtype)
+    if out is None:
+        dt = out_dtype or (residual.dtype if residual is not None else torch.bfloat16)
+        out = torch.empty(M, N, dtype=dt, device=dev)
+    ldy = _rows(out, "out", _BF16_FP32, (M, N))
+    if residual is None:
+        ldr = 0
+    elif residual is out:
+        ldr = ldy
+    else:
+        ldr = _rows(residual, "residual", (out.dtype,), (M, N))
+    if W.device != dev or out.device != dev or (residual is not None and residual.device != dev):
+        raise ValueError(f"every tensor must be on {dev}")
+    # a single row's stride is free: the library wants multiples of 8
+    if M <= 1:
+        ldx = (ldx + 7) // 8 * 8
+    if K == 1:
+        ldw = (ldw + 7) // 8 * 8
+    buf = _workspace(ws, dev, fn_workspace_size_proj(M, K, N))
+    check(lib().fn_proj(x.data_ptr(), ldx, M, K, W.data_ptr(), ldw, N, _at(bias), _ACT[act], _at(residual), ldr,
+                        _DTYPE[out.dtype], out.data_ptr(), ldy, buf.data_ptr(), buf.numel(), _handle(dev)), "fn_proj")
     return out
 
 
@@ -326,11 +316,13 @@ def fold_experts(W_gate: torch.Tensor, g: torch.Tensor, W_up: torch.Tensor, stre
     _dense(W_gate, "W_gate", torch.bfloat16, (E, d, N), dev)
     _dense(W_up, "W_up", torch.bfloat16, (E, d, N), dev)
     _vec(g, "g", torch.float32, d, dev)
-    with _on(dev, stream):
-        out = torch.empty((E, d, 2 * N), dtype=torch.bfloat16, device=dev)
-        for e in range(E):
-            check(fn_fold_weights(W_gate[e], W_up[e], g, d, N, FN_W_BF16, out[e], None, _handle(dev)),
-                  "fn_fold_weights")
+    other = _elsewhere(dev, stream)
+    if other is not None:
+        with other:
+            return fold_experts(W_gate, g, W_up)
+    out = torch.empty((E, d, 2 * N), dtype=torch.bfloat16, device=dev)
+    for e in range(E):
+        check(fn_fold_weights(W_gate[e], W_up[e], g, d, N, FN_W_BF16, out[e], None, _handle(dev)), "fn_fold_weights")
     return out
 
 
@@ -360,16 +352,20 @@ def moe_swiglu(x: torch.Tensor, g: Optional[torch.Tensor], router: torch.Tensor,
     _dense(out, "out", bf, (M, d), dev)
     _vec(g, "g", torch.float32, d, dev)
     _vec(select_bias, "select_bias", torch.float32, E, dev)
-    with _on(dev, stream):
-        if out is None:
-            out = torch.empty(M, d, dtype=bf, device=dev)
-        ids = torch.empty(M, top_k, dtype=torch.int32, device=dev)
-        w = torch.empty(M, top_k, dtype=torch.float32, device=dev)
-        buf = _workspace(ws, dev, fn_workspace_size_moe(M, d, I, E, top_k))
-        check(lib().fn_moe_swiglu(x.data_ptr(), M, d, _at(g), router.data_ptr(), E, Wgu.data_ptr(), Wd.data_ptr(), I,
-                                  top_k, _SCORE[score], _at(select_bias), 1 if renorm else 0, route_scale, eps,
-                                  _at(residual), out.data_ptr(), ids.data_ptr(), w.data_ptr(), buf.data_ptr(),
-                                  buf.numel(), _handle(dev)), "fn_moe_swiglu")
+    other = _elsewhere(dev, stream)
+    if other is not None:
+        with other:
+            return moe_swiglu(x, g, router, Wgu, Wd, top_k, eps, score, select_bias, renorm, route_scale, residual, ws,
+                              out)
+    if out is None:
+        out = torch.empty(M, d, dtype=bf, device=dev)
+    ids = torch.empty(M, top_k, dtype=torch.int32, device=dev)
+    w = torch.empty(M, top_k, dtype=torch.float32, device=dev)
+    buf = _workspace(ws, dev, fn_workspace_size_moe(M, d, I, E, top_k))
+    check(lib().fn_moe_swiglu(x.data_ptr(), M, d, _at(g), router.data_ptr(), E, Wgu.data_ptr(), Wd.data_ptr(), I, top_k,
+                              _SCORE[score], _at(select_bias), 1 if renorm else 0, route_scale, eps, _at(residual),
+                              out.data_ptr(), ids.data_ptr(), w.data_ptr(), buf.data_ptr(), buf.numel(), _handle(dev)),
+          "fn_moe_swiglu")
     return out, ids, w
 
 
@@ -390,22 +386,27 @@ def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None,
     M, V = logits.shape
     dev = logits.device
     _vec(targets, "targets", torch.int32, M, dev)
-    with _on(dev, stream):
-        if out is None:
-            lp, ent, lse = torch.empty(3, M, dtype=torch.float32, device=dev).unbind()
-            out = TokenLogprobs(lp if targets is not None else None, ent, lse,
-                                torch.empty(M, top_k, dtype=torch.int32, device=dev),
-                                torch.empty(M, top_k, dtype=torch.float32, device=dev))
-        else:
-            _vec(out.logprob, "logprob", torch.float32, M, dev)
-            _vec(out.entropy, "entropy", torch.float32, M, dev)
-            _vec(out.lse, "lse", torch.float32, M, dev)
-            _dense(out.top_ids, "top_ids", torch.int32, (M, top_k), dev)
-            _dense(out.top_logprobs, "top_logprobs", torch.float32, (M, top_k), dev)
+    other = _elsewhere(dev, stream)
+    if other is not None:
+        with other:
+            return token_logprobs(logits, targets, top_k, scale, out)
+    if out is None:
+        lp, ent, lse = torch.empty(3, M, dtype=torch.float32, device=dev).unbind()
+        ids = torch.empty(M, top_k, dtype=torch.int32, device=dev)
+        top = torch.empty(M, top_k, dtype=torch.float32, device=dev)
+        if targets is None:
+            lp = None
+        out = TokenLogprobs(lp, ent, lse, ids, top)
+    else:
         lp, ent, lse, ids, top = out
-        check(lib().fn_token_logprobs(logits.data_ptr(), _DTYPE[logits.dtype], M, V, ld, _at(targets), scale, top_k,
-                                      _at(lp), _at(ent), _at(lse), ids.data_ptr() if top_k else None,
-                                      top.data_ptr() if top_k else None, _handle(dev)), "fn_token_logprobs")
+        _vec(lp, "logprob", torch.float32, M, dev)
+        _vec(ent, "entropy", torch.float32, M, dev)
+        _vec(lse, "lse", torch.float32, M, dev)
+        _dense(ids, "top_ids", torch.int32, (M, top_k), dev)
+        _dense(top, "top_logprobs", torch.float32, (M, top_k), dev)
+    check(lib().fn_token_logprobs(logits.data_ptr(), _DTYPE[logits.dtype], M, V, ld, _at(targets), scale, top_k,
+                                  _at(lp), _at(ent), _at(lse), ids.data_ptr() if top_k else None,
+                                  top.data_ptr() if top_k else None, _handle(dev)), "fn_token_logprobs")
     return out
 
 
@@ -423,13 +424,16 @@ def token_logprobs_backward(logits: torch.Tensor, targets: Optional[torch.Tensor
     _vec(entropy, "entropy", torch.float32, M, dev)
     _vec(grad_logprob, "grad_logprob", torch.float32, M, dev)
     _vec(grad_entropy, "grad_entropy", torch.float32, M, dev)
-    with _on(dev, stream):
-        if out is None:
-            out = torch.empty((M, V), dtype=logits.dtype, device=dev)
-        ldd = _rows(out, "out", (logits.dtype,), (M, V))
-        if out.device != dev:
-            raise ValueError(f"out on {out.device}, logits on {dev}")
-        check(lib().fn_token_logprobs_backward(logits.data_ptr(), _DTYPE[logits.dtype], M, V, ld, _at(targets),
-                                               lse.data_ptr(), _at(entropy), _at(grad_logprob), _at(grad_entropy),
-                                               scale, out.data_ptr(), ldd, _handle(dev)), "fn_token_logprobs_backward")
+    other = _elsewhere(dev, stream)
+    if other is not None:
+        with other:
+            return token_logprobs_backward(logits, targets, lse, entropy, grad_logprob, grad_entropy, scale, out)
+    if out is None:
+        out = torch.empty(M, V, dtype=logits.dtype, device=dev)
+    ldd = _rows(out, "out", (logits.dtype,), (M, V))
+    if out.device != dev:
+        raise ValueError(f"out on {out.device}, logits on {dev}")
+    check(lib().fn_token_logprobs_backward(logits.data_ptr(), _DTYPE[logits.dtype], M, V, ld, _at(targets),
+                                           lse.data_ptr(), _at(entropy), _at(grad_logprob), _at(grad_entropy), scale,
+                                           out.data_ptr(), ldd, _handle(dev)), "fn_token_logprobs_backward")
     return out
