@@ -411,8 +411,11 @@ typedef enum {
  *   workspace, ws_bytes  >= fn_workspace_size_proj(M, K, N), zeroed before
  *            first use; the calls leave what they need zero at zero
  * M == 0 is a no-op.  M <= 64 runs a split-K kernel that streams the weight
- * over all SMs, larger M a tensor-core tile kernel on pairs of SMs; one launch
- * each, deterministic.
+ * over all SMs, larger M a tensor-core tile kernel on pairs of SMs; where SMs
+ * share a tile's k range and M > 16 a second kernel adds their sums.
+ * Deterministic.  A weight of more than 2^24 blocks of 64 x 128 is refused
+ * (FN_ERR_UNSUPPORTED_SHAPE).  After FN_ERR_TIMEOUT in the status word the
+ * workspace must be zeroed before its next use.
  */
 fn_status fn_proj(const void* x, int64_t ldx, int64_t M, int64_t K, const void* W, int64_t ldw, int64_t N,
                   const float* bias, fn_act act, const void* residual, int64_t ldr, fn_dtype out_type, void* y,
@@ -421,7 +424,9 @@ fn_status fn_proj(const void* x, int64_t ldx, int64_t M, int64_t K, const void* 
 /* fn_workspace_size_proj — workspace bytes of fn_proj: the 256-byte header
  * (status word, counters) and the fp32 partial sums of the tiles whose k range
  * several SMs share.  One workspace serves any of this library's calls, one
- * after another.  Depends on the SM count of the current device. */
+ * after another; calls that may run at the same time (two streams, two graphs
+ * replayed together) need one each.  Depends on the SM count of the current
+ * device. */
 size_t fn_workspace_size_proj(int64_t M, int64_t K, int64_t N);
 
 typedef enum {
@@ -443,7 +448,8 @@ typedef enum {
  *   x        bf16 [M, d] raw activations
  *   g        fp32 [d], 16-byte aligned: the norm gain, for the router; NULL
  *            where the router weight holds it already
- *   router   bf16 [E, d], not folded
+ *   router   bf16 [E, d], not folded; an expert whose row holds an infinity or
+ *            NaN has a NaN logit
  *   Wgu      bf16 [E, d, 2I]: per expert the interleaved fold of (G_e, U_e)
  *            by fn_fold_weights; must be finite, Wd too (the rows that did not
  *            choose an expert meet it with zeros)
@@ -460,7 +466,9 @@ typedef enum {
  * fp32 sums; the expert activations are rounded to bf16 once, after the
  * routing weight, and the result once, after the residual.  Only the chosen
  * experts' weights are read.  A row with a non-finite activation has NaN or
- * infinite outputs in its own row only.  M == 0 is a no-op.  Deterministic.
+ * infinite outputs in its own row only.  M == 0 is a no-op.  Three launches
+ * (router, gate/up, down), deterministic.  After FN_ERR_TIMEOUT in the status
+ * word the workspace must be zeroed before its next use.
  */
 fn_status fn_moe_swiglu(const void* x, int64_t M, int64_t d, const float* g, const void* router, int64_t E,
                         const void* Wgu, const void* Wd, int64_t I, int top_k, fn_score score,

@@ -496,7 +496,7 @@ Plan best_plan(int64_t M, int64_t K, int64_t N, int num_sms) {
 template <bool F32, int H>
 cudaError_t launch_kernel(const Params& p, const Plan& q, cudaStream_t stream, const CUtensorMap& tx,
                           const CUtensorMap& tw) {
-  const cudaError_t e = ensure_smem_limit<proj_tile_kernel<F32, H>>(static_cast<int>(SMEM));
+  const cudaError_t e = ensure_shared<proj_tile_kernel<F32, H>>(static_cast<int>(SMEM));
   if (e != cudaSuccess) return e;
   return launch_pdl(proj_tile_kernel<F32, H>, static_cast<unsigned>(2 * q.pairs), NUM_THREADS, SMEM, stream, tx, tw, p);
 }

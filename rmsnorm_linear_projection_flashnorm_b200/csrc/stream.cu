@@ -538,7 +538,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 template <int MPAD, int HALVES, int MODE>
 cudaError_t launch(Params& p, const CUtensorMap& tx, const CUtensorMap& tw, int num_sms, cudaStream_t stream) {
   constexpr size_t SMEM = smem_bytes<MPAD, HALVES, MODE>();
-  const cudaError_t e = ensure_smem_limit<stream_kernel<MPAD, HALVES, MODE>>(static_cast<int>(SMEM));
+  const cudaError_t e = ensure_shared<stream_kernel<MPAD, HALVES, MODE>>(static_cast<int>(SMEM));
   if (e != cudaSuccess) return e;
   if (num_sms > kMaxCounters) num_sms = kMaxCounters;
   // the experts' space is known to the kernel only
