@@ -410,9 +410,10 @@ typedef enum {
  *   the padding is not read.  y, residual and bias need element alignment.
  *   workspace, ws_bytes  >= fn_workspace_size_proj(M, K, N), zeroed before
  *            first use; the calls leave what they need zero at zero
- * M == 0 is a no-op.  M <= 64 runs a split-K kernel that streams the weight
- * over all SMs, larger M a tensor-core tile kernel on pairs of SMs; where SMs
- * share a tile's k range and M > 16 a second kernel adds their sums.
+ * M == 0 is a no-op.  Few rows (up to 128, by N and K) run a split-K kernel that
+ * streams the weight over all SMs, others a tensor-core tile kernel on pairs of
+ * SMs; where SMs share a tile's k range and M > 16 a second kernel adds their
+ * sums.
  * Deterministic.  A weight of more than 2^24 blocks of 64 x 128 is refused
  * (FN_ERR_UNSUPPORTED_SHAPE).  After FN_ERR_TIMEOUT in the status word the
  * workspace must be zeroed before its next use.

@@ -101,7 +101,8 @@ bool make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType dt, in
 
 // Rows `ld` elements apart (ld * elem_bytes a multiple of 16).
 bool make_tmap_2d_ld(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int elem_bytes, uint64_t rows,
-                     uint64_t cols, uint64_t ld, uint32_t box_rows, uint32_t box_cols, bool swizzle128) {
+                     uint64_t cols, uint64_t ld, uint32_t box_rows, uint32_t box_cols, bool swizzle128,
+                     CUtensorMapL2promotion promotion) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
   const cuuint64_t dims[2] = {cols, rows};
@@ -112,7 +113,7 @@ bool make_tmap_2d_ld(CUtensorMap* map, const void* base, CUtensorMapDataType dt,
   const CUresult r = enc(map, dt, 2, const_cast<void*>(base), dims, strides, box, estr,
                          CU_TENSOR_MAP_INTERLEAVE_NONE,
                          swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                         promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 
@@ -520,7 +521,7 @@ bool misaligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintpt
 size_t fn_workspace_size_proj(int64_t M, int64_t K, int64_t N) {
   if (M <= 0 || K <= 0 || N <= 0 || M > kMaxProjDim || K > kMaxProjDim || N > kMaxProjDim) return kWsHeaderBytes;
   const int sms = current_sms_or_default();
-  return M <= 64 ? proj_stream_workspace_bytes(M, sms) : proj_tile_workspace_bytes(M, K, N, sms);
+  return proj_takes_stream(M, K, N, sms) ? proj_stream_workspace_bytes(M, sms) : proj_tile_workspace_bytes(M, K, N, sms);
 }
 
 fn_status fn_proj(const void* x, int64_t ldx, int64_t M, int64_t K, const void* W, int64_t ldw, int64_t N,
@@ -554,7 +555,7 @@ fn_status fn_proj(const void* x, int64_t ldx, int64_t M, int64_t K, const void* 
   int sms = 0;
   const fn_status st = check_device(sms);
   if (st != FN_OK) return st;
-  const bool stream_path = M <= 64;
+  const bool stream_path = proj_takes_stream(M, K, N, sms);
   if (ws_bytes < (stream_path ? proj_stream_workspace_bytes(M, sms) : proj_tile_workspace_bytes(M, K, N, sms)))
     return FN_ERR_WORKSPACE;
   ProjArgs a;

@@ -65,7 +65,8 @@ EncodeTiledFn encode_fn();
 // 2D row-major tensor map with 128-byte swizzle: rows x cols elements of
 // `elem_bytes`, box of box_rows x box_cols (box_cols * elem_bytes <= 128).
 bool make_tmap_2d_ld(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int elem_bytes, uint64_t rows,
-                     uint64_t cols, uint64_t ld, uint32_t box_rows, uint32_t box_cols, bool swizzle128 = true);
+                     uint64_t cols, uint64_t ld, uint32_t box_rows, uint32_t box_cols, bool swizzle128 = true,
+                     CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 bool make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int elem_bytes, uint64_t rows,
                   uint64_t cols, uint32_t box_rows, uint32_t box_cols, bool swizzle128 = true);
 
@@ -132,7 +133,7 @@ cudaError_t launch_dequant_fp8(const void* q, const float* scales, int64_t d, in
 cudaError_t launch_adaln_shift_bias(const float* shift, int64_t n_cond, const void* W0, const void* W1, int64_t d,
                                     int64_t N, float* B, cudaStream_t s);
 
-// fn_proj: y = act(x W + bias) + residual (stream.cu up to 64 rows, proj_tile.cu above).
+// fn_proj: y = act(x W + bias) + residual (stream.cu for few rows, proj_tile.cu else).
 struct Epilogue {
   const float* bias;      // [N] or null
   int act;                // fn_act
@@ -173,6 +174,7 @@ struct FixupArgs {
   cudaStream_t stream;
 };
 cudaError_t launch_proj_fixup(const FixupArgs& a);
+bool proj_takes_stream(int64_t M, int64_t K, int64_t N, int num_sms);   // else the tile kernel
 size_t proj_stream_workspace_bytes(int64_t M, int num_sms);
 size_t proj_tile_workspace_bytes(int64_t M, int64_t K, int64_t N, int num_sms);
 int64_t proj_tile_count(int64_t M, int64_t N);

@@ -1,4 +1,5 @@
-// fn_proj above 64 rows: y = act(x W + b) + residual on pairs of SMs, sm_100a.
+// fn_proj for more rows, or many columns: y = act(x W + b) + residual on pairs of
+// SMs, sm_100a.
 //
 // Each 2-CTA cluster computes 256 weight columns x H * NB rows with
 // tcgen05.mma.cta_group::2 (swap-AB: the weight columns on the MMA's M side,

@@ -1,10 +1,10 @@
-// Projections of at most 64 rows whose cost is the weight stream, sm_100a:
+// Projections of few rows (at most 128) whose cost is the weight stream, sm_100a:
 //   kProj  y = act(x W + b) + residual (fn_proj)
 //   kUp    the chosen experts' SwiGLU, act = w silu(r x G') (r x U') (fn_moe_swiglu)
 //   kDown  y = residual + sum over the chosen experts of act D  (fn_moe_swiglu)
 //
 // Swap-AB as in the norm-fused decode kernel: D[n, m] += W^T[n, k] x^T[k, m],
-// 128 weight columns on the MMA's M side, the rows padded to 16, 32 or 64 on
+// 128 weight columns on the MMA's M side, the rows padded to 16, 32, 64 or 128 on
 // its N side (tcgen05.mma kind::f16, fp32 accumulators in TMEM), both operands
 // staged by TMA with 128-byte swizzle.  Bound by HBM: every weight byte is
 // read once, the MMAs hide under the stream.
@@ -47,7 +47,10 @@ constexpr int MAX_SHARE = 16;              // CTAs to a tile: the last one reads
 constexpr unsigned ALIGN_SLACK = 3, WHOLE_SLACK = 8;
 constexpr int FIXUP_ROWS = 16;             // kProj: more rows than these are finished by the fix-up kernel
 
-enum Mode : int { kProj = 0, kUp = 1, kDown = 2 };
+// kProjRows: kProj where CTAs finish whole tiles of more than RC rows.
+enum Mode : int { kProj = 0, kUp = 1, kDown = 2, kProjRows = 3 };
+template <int MODE>
+constexpr bool is_proj = MODE == kProj || MODE == kProjRows;
 enum : unsigned { kSiteProdEmpty = 1, kSiteMmaAccEmpty, kSiteMmaFull, kSiteEpiAccFull };
 
 struct Params {
@@ -64,6 +67,7 @@ struct Params {
   int prefetch_iters;
   int fixup;                     // kProj: shared tiles are finished by the fix-up kernel
   Epilogue epi;                  // kProj, kDown
+  int vec;                       // kProj: the epilogue's vector form applies
   MoeRoute route;                // kUp, kDown
   __nv_bfloat16* act;            // kUp writes [slot][MPAD][I]
 };
@@ -72,7 +76,7 @@ template <int MPAD, int HALVES, int MODE>
 struct Cfg {
   // The expert kernels up to 32 rows leave room for a second CTA on the SM: the
   // next kernel's, which starts on its weights while this one drains.
-  static constexpr int SMEM_BUDGET = (MODE == kProj || MPAD > 32 ? 200 : MODE == kUp ? 104 : 112) * 1024;
+  static constexpr int SMEM_BUDGET = (is_proj<MODE> || MPAD > 32 ? 200 : MODE == kUp ? 104 : 112) * 1024;
   static constexpr int W_BYTES = HALVES * 2 * W_BOX_BYTES;
   static constexpr int X_BYTES = MPAD * BK * 2;
   static constexpr int STAGE_BYTES = W_BYTES + X_BYTES;
@@ -83,8 +87,9 @@ struct Cfg {
   static constexpr int SLOT_FLOATS = HALVES * MPAD * 128;
 };
 
-template <int STAGES, bool SWAP>
+template <int STAGES, bool SWAP, bool ROWS>
 struct alignas(16) Bars {
+  float scratch[ROWS ? 4 : 1][ROWS ? SCRATCH_FLOATS : 4];   // kProjRows: of the epilogue warps
   uint64_t full[STAGES], empty[STAGES];
   uint64_t acc_full[2], acc_empty[2];
   uint64_t drain;
@@ -101,7 +106,7 @@ struct alignas(16) Bars {
 template <int MPAD, int HALVES, int MODE>
 constexpr size_t smem_bytes() {
   using C = Cfg<MPAD, HALVES, MODE>;
-  return 1024 + C::STAGES * C::STAGE_BYTES + sizeof(Bars<C::STAGES, MODE == kUp && HALVES == 1>);
+  return 1024 + C::STAGES * C::STAGE_BYTES + sizeof(Bars<C::STAGES, MODE == kUp && HALVES == 1, MODE == kProjRows>);
 }
 static_assert(smem_bytes<16, 1, kProj>() <= 232448 && smem_bytes<64, 2, kUp>() <= 232448, "shared memory budget");
 static_assert(smem_bytes<32, 2, kUp>() + smem_bytes<32, 1, kDown>() + 2048 <= 233472 &&
@@ -130,6 +135,34 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, unsig
   }
 }
 
+// kProj: all rows of this warp's 32 columns, from its TMEM lanes.
+template <bool F32>
+__device__ __forceinline__ void finish_rows(const Params& p, uint32_t taddr, float* scratch, int lane, int64_t col0) {
+  float4 bias = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (p.epi.bias) {
+    const int64_t last = p.ncols - 1, c = col0 + lane % 8 * 4;
+    bias = make_float4(__ldg(p.epi.bias + min(c, last)), __ldg(p.epi.bias + min(c + 1, last)),
+                       __ldg(p.epi.bias + min(c + 2, last)), __ldg(p.epi.bias + min(c + 3, last)));
+  }
+  const bool ahead = p.vec && p.epi.residual;
+  typename Quad<F32>::Raw raw[2][4];
+  if (ahead) epi_fetch<F32>(p.epi, lane, 0, min(p.M, 16), col0, p.ncols, raw[0]);
+#pragma unroll 1
+  for (int m0 = 0; m0 < p.M; m0 += 16) {
+    const int rows = min(p.M - m0, 16);
+    uint32_t v[16];
+    float z[16];
+    tmem_ld16(taddr + m0, v);
+    if (ahead) epi_fetch<F32>(p.epi, lane, m0 + 16, min(p.M - m0 - 16, 16), col0, p.ncols, raw[1]);
+    tmem_ld_wait();
+    epi_transpose_act(p.epi, scratch, lane, bias, v, z);
+    if (p.vec) epi_store_vec<F32>(p.epi, raw[0], lane, m0, rows, col0, p.ncols, z);
+    else epi_store_scalar<F32>(p.epi, lane, m0, rows, col0, p.ncols, z);
+#pragma unroll
+    for (int g = 0; g < 4; ++g) raw[0][g] = raw[1][g];
+  }
+}
+
 template <int MPAD, int HALVES, int MODE>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     stream_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
@@ -138,7 +171,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   constexpr int STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  using Shared = Bars<STAGES, MODE == kUp && HALVES == 1>;
+  using Shared = Bars<STAGES, MODE == kUp && HALVES == 1, MODE == kProjRows>;
   Shared& bars = *reinterpret_cast<Shared*>(smem + STAGES * C::STAGE_BYTES);
   auto stage_w = [&](int s) { return smem + s * C::STAGE_BYTES; };
   auto stage_x = [&](int s) { return smem + s * C::STAGE_BYTES + C::W_BYTES; };
@@ -167,7 +200,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tmem_alloc(&bars.tmem_base, C::TMEM_COLS);
     tmem_relinquish();
   }
-  if (MODE != kProj)
+  if (!is_proj<MODE>)
     for (int i = threadIdx.x; i < kMoeMaxExperts / 32; i += NUM_THREADS) bars.active[i] = 0;
 
   // The iteration space: tiles x kblocks, cut into one contiguous share per CTA.
@@ -179,7 +212,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     it0 = cta < grid ? cta * total / grid : 0;
     it1 = cta < grid ? (cta + 1) * total / grid : 0;
   };
-  if (MODE == kProj) {
+  if (is_proj<MODE>) {
     cut();
     // This overlaps the previous kernel in the stream: an L2 prefetch of the
     // share's first k blocks cannot return stale data, whoever wrote the
@@ -205,7 +238,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     grid_dependency_wait();
     grid_launch_dependents();
   }
-  if (MODE != kProj) {
+  if (!is_proj<MODE>) {
     // the chosen experts in ascending order, from the router's ids
     for (int i = threadIdx.x; i < p.M * p.route.k; i += NUM_THREADS) {
       const int e = __ldcg(p.route.ids + i);
@@ -442,6 +475,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
           for (int j = 0; j < RC; ++j) acc[h][j] = __uint_as_float(raw[h][j]);
       };
+      if (MODE == kProjRows && kb0 == 0 && kb1 == kblocks) {
+        // A whole tile of more rows: through shared memory, as in the tile kernel
+        // (one column per thread took 27 us for 48 x 256 x 65536, this 14).
+        const int64_t col0 = static_cast<int64_t>(tile) * 128 + q * 32;
+        if (p.epi.out_fp32) finish_rows<true>(p, taddr, bars.scratch[q], lane, col0);
+        else finish_rows<false>(p, taddr, bars.scratch[q], lane, col0);
+        tc_fence_before();
+        mbar_arrive(&bars.acc_empty[b]);
+        continue;
+      }
       if (kb0 == 0 && kb1 == kblocks) {
 #pragma unroll 1
         for (int m0 = 0; m0 < p.M; m0 += RC) {
@@ -474,7 +517,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       tc_fence_before();
       mbar_arrive(&bars.acc_empty[b]);
-      if (MODE == kProj && p.fixup) continue;
+      if (is_proj<MODE> && p.fixup) continue;
       const unsigned t0 = static_cast<unsigned>(tile) * kblocks;
       const int c_first = static_cast<int>(owner_of(t0)), c_last = static_cast<int>(owner_of(t0 + kblocks - 1));
       route(0);
@@ -542,7 +585,7 @@ cudaError_t launch(Params& p, const CUtensorMap& tx, const CUtensorMap& tw, int 
   if (e != cudaSuccess) return e;
   if (num_sms > kMaxCounters) num_sms = kMaxCounters;
   // the experts' space is known to the kernel only
-  const unsigned grid = MODE == kProj ? share_count(p.tiles, p.kblocks, num_sms) : static_cast<unsigned>(num_sms);
+  const unsigned grid = is_proj<MODE> ? share_count(p.tiles, p.kblocks, num_sms) : static_cast<unsigned>(num_sms);
   return launch_pdl(stream_kernel<MPAD, HALVES, MODE>, grid, NUM_THREADS, SMEM, stream, tx, tw, p);
 }
 
@@ -553,16 +596,47 @@ inline size_t part_bytes(int mpad, int halves, int num_sms) {
 
 }  // namespace strm
 
+// The stream kernel where its weight stream is the cost; the tile kernel, whose
+// epilogue has twice the warps and whose pairs read 256 adjacent columns, where
+// whole tiles' epilogues are, or rows off the 128-byte lines.  Measured, stream
+// against tile kernel (us): 16 x 4096 x 51200 68 : 71, 16 x 4096 x 50000 87 : 73;
+// 64 x 8192 x 32768 90 : 94, 64 x 1024 x 32768 22 : 18, 64 x 2048 x 8192 12 : 15;
+// 100 x 4096 x 8192 19 : 23, 100 x 2000 x 12000 19 : 17.
+bool proj_takes_stream(int64_t M, int64_t K, int64_t N, int num_sms) {
+  const int64_t tiles = (N + 127) / 128;
+  const bool lines = N % 64 == 0;
+  if (M <= 16) return lines || tiles < 2 * num_sms;
+  if (M <= 64) return 2 * tiles < 3 * num_sms || (lines && K >= 6144);
+  return M <= 128 && 2 * tiles <= num_sms;
+}
+
+namespace {
+int proj_mpad(int64_t M) { return M <= 64 ? decode_mpad(M) : 128; }
+}  // namespace
+
 size_t proj_stream_workspace_bytes(int64_t M, int num_sms) {
-  return kWsHeaderBytes + strm::part_bytes(decode_mpad(M), 1, num_sms);
+  return kWsHeaderBytes + strm::part_bytes(proj_mpad(M), 1, num_sms);
+}
+
+template <int MODE>
+static cudaError_t launch_rows(int mp, strm::Params& p, const CUtensorMap& tx, const CUtensorMap& tw, const ProjArgs& a) {
+  if (mp == 16) return strm::launch<16, 1, MODE>(p, tx, tw, a.num_sms, a.stream);
+  if (mp == 32) return strm::launch<32, 1, MODE>(p, tx, tw, a.num_sms, a.stream);
+  if (mp == 64) return strm::launch<64, 1, MODE>(p, tx, tw, a.num_sms, a.stream);
+  return strm::launch<128, 1, MODE>(p, tx, tw, a.num_sms, a.stream);
 }
 
 cudaError_t launch_proj_stream(const ProjArgs& a) {
   using namespace strm;
-  const int mp = decode_mpad(a.M);
+  const int mp = proj_mpad(a.M);
   CUtensorMap tx, tw;
   if (!make_tmap_2d_ld(&tx, a.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.M, a.K, a.ldx, mp, BK)) return cudaErrorInvalidValue;
-  if (!make_tmap_2d_ld(&tw, a.W, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.K, a.N, a.ldw, BK, 64)) return cudaErrorInvalidValue;
+  // A row of a box is 128 bytes; where rows start off 128-byte lines, a fetch
+  // widened to 256 bytes brings a neighbour's bytes that L2 drops again before
+  // they are used (32 x 4096 x 50000: 110 us, 88 without, 71 with aligned rows).
+  const auto promotion = a.ldw % 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
+  if (!make_tmap_2d_ld(&tw, a.W, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.K, a.N, a.ldw, BK, 64, true, promotion))
+    return cudaErrorInvalidValue;
   Params p = {};
   p.M = static_cast<int>(a.M);
   p.ncols = static_cast<int>(a.N);
@@ -578,12 +652,12 @@ cudaError_t launch_proj_stream(const ProjArgs& a) {
   p.w_row_bytes = a.ldw * 2;
   p.prefetch_iters = a.prefetch_iters;
   p.epi = a.epi;
+  p.vec = epi_vector_ok(a.epi, a.N);
   p.fixup = a.M > FIXUP_ROWS;
-  const cudaError_t e = mp == 16   ? strm::launch<16, 1, kProj>(p, tx, tw, a.num_sms, a.stream)
-                        : mp == 32 ? strm::launch<32, 1, kProj>(p, tx, tw, a.num_sms, a.stream)
-                                   : strm::launch<64, 1, kProj>(p, tx, tw, a.num_sms, a.stream);
-  if (e != cudaSuccess || !p.fixup) return e;
   const int ctas = a.num_sms < kMaxCounters ? a.num_sms : kMaxCounters;
+  const bool whole = a.M > RC && share_count(p.tiles, p.kblocks, ctas) <= static_cast<unsigned>(p.tiles);
+  const cudaError_t e = whole ? launch_rows<kProjRows>(mp, p, tx, tw, a) : launch_rows<kProj>(mp, p, tx, tw, a);
+  if (e != cudaSuccess || !p.fixup) return e;
   FixupArgs f = {};
   f.sharers = static_cast<int>(share_count(p.tiles, p.kblocks, ctas));
   if (f.sharers <= p.tiles && p.tiles % f.sharers == 0) return e;       // whole tiles only

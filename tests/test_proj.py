@@ -322,3 +322,14 @@ def test_offsets_past_32_bits():
     ref = x[:, at].double() @ w[at].double()
     mag = x[:, at].double().abs() @ w[at].double().abs()
     assert ((y.double() - ref).abs() <= (8 + math.sqrt(K)) * 2 * U * mag + U * ref.abs() + 1e-30).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,K,N", [(16, 256, 38000), (16, 256, 38016), (64, 64, 28416), (48, 128, 30001), (64, 6144, 28416),
+                                   (128, 1024, 9472), (128, 1024, 9600), (65, 4096, 1000), (120, 100, 72), (20, 64, 16384)])
+def test_few_rows_many_columns(M, K, N):
+    """Both sides of the choice between the weight-stream and the tile kernel,
+    whole tiles and shared ones, rows on and off the 128-byte lines."""
+    case(M, K, N, residual=True, bias=True, seed=M)
+    aligned(M, K, N, False, True, "none", seed=K)
+    aligned(M, K, N, True, False, "silu", seed=K)
