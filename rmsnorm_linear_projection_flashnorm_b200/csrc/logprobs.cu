@@ -40,6 +40,10 @@
 // when there are few rows, so one decoded token still uses 8 SMs.  The CTAs'
 // (m, s, t) and top lists meet in distributed shared memory in rank order:
 // one launch, no workspace, no atomics on results, bit-identical repeats.
+//
+// Measured: 4096 x 131072 bf16 with 8 alternatives 205 us (5.2 TB/s; issue slots
+// of the threshold tests), without 160 us (6.7 TB/s); one row with 20
+// alternatives 10 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -22,8 +22,9 @@
 //
 // The logits meet in distributed shared memory; the choice has no serial
 // rounds: an expert's place is the number of experts that come before it, which
-// every thread counts for its own experts (all k rounds of a warp-wide maximum
-// took 4 us at k = 8).
+// every thread counts for its own experts.  One row, 64 experts x 2048, 8 chosen:
+// 5.9 us; warps with an expert each, conversions and k rounds of a warp-wide
+// maximum took 11.4.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -24,6 +24,10 @@
 // finishes the tile (no CTA waits for another, no floating-point atomics,
 // bit-identical repeats).
 //
+// Measured (device time a call): 4096 x 14336 x 4096 with bias and residual
+// 347..367 us (1310..1388 TFLOP/s, under the power cap), 1024 x 8192 x 4096 56 us,
+// 300 x 14336 x 4096 45 us.
+//
 // Layout per CTA: 10 warps.
 //   warp 0      TMA producer (own weight columns, own rows)
 //   warp 1      TMEM owner; in CTA 0 the pair-MMA issuer

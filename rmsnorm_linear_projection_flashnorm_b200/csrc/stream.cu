@@ -20,7 +20,13 @@
 // the flops are not (64 rows x all weights is under a tenth of the tensor
 // rate at the HBM rate).  kUp stores zeros for the rows that did not choose an
 // expert, scaled by the routing weight for those that did, so kDown needs no
-// masks.
+// masks.  Their one rounding to bf16, behind the routing weight, makes them the
+// next MMA's operand.
+//
+// Measured (device time a call): 4096 x 4096, one row, 10.6 us, of which the
+// stream takes 4.7 (7.1 TB/s), the first load 0.8, the exchange 3 and the
+// kernel boundary 1.2; 8 experts of 2048 x 1024 and one row 35.8 us with the
+// router's 5.9; 64 rows and 8 experts of 4096 x 14336 489 us (5.8 TB/s).
 //
 // A tile whose k range falls to one CTA is finished by it.  The CTAs that
 // share a tile write fp32 partials to the workspace.  With few rows, and for
@@ -108,7 +114,10 @@ constexpr size_t smem_bytes() {
   using C = Cfg<MPAD, HALVES, MODE>;
   return 1024 + C::STAGES * C::STAGE_BYTES + sizeof(Bars<C::STAGES, MODE == kUp && HALVES == 1, MODE == kProjRows>);
 }
-static_assert(smem_bytes<16, 1, kProj>() <= 232448 && smem_bytes<64, 2, kUp>() <= 232448, "shared memory budget");
+static_assert(smem_bytes<16, 1, kProjRows>() <= 232448 && smem_bytes<32, 1, kProjRows>() <= 232448 &&
+                  smem_bytes<64, 1, kProjRows>() <= 232448 && smem_bytes<128, 1, kProjRows>() <= 232448 &&
+                  smem_bytes<64, 2, kUp>() <= 232448,
+              "shared memory budget");
 static_assert(smem_bytes<32, 2, kUp>() + smem_bytes<32, 1, kDown>() + 2048 <= 233472 &&
                   smem_bytes<16, 2, kUp>() + smem_bytes<16, 1, kDown>() + 2048 <= 233472 &&
                   smem_bytes<16, 1, kUp>() + smem_bytes<16, 1, kDown>() + 2048 <= 233472,
@@ -413,7 +422,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       named_bar_sync(1, 128);
       if (!bars.epi_ok[b]) break;
       tc_fence_after();
-      // Chunks of 16 rows: the code of one chunk serves them all.
+      // Chunks of RC rows: the code of one chunk serves them all.
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + b * HALVES * MPAD;
       float w[RC], r[RC];                         // kUp: routing weight and 1 / rms of the chunk's rows
       auto route = [&](int m0) {
