@@ -453,12 +453,14 @@ struct Plan {
 // (per_tile 0), shared evenly by per_tile pairs each, or by all pairs (-1).
 //
 // The estimate, from measurements of this kernel: a k step is bound by the
-// operand bytes that L2 delivers (75 GB/s to an SM while all read: 0.44 us at
-// 256 rows, 0.36 at 160) or by the tensor cores (0.30 us per 256 rows); the
-// last epilogue, and every one of the wide form, takes 4 us per 256 rows;
+// tensor cores, 0.30 us per 256 rows while few pairs work and 0.44 when all 74
+// do (power), or by the operand bytes that L2 delivers to all SMs (11.1 MB per
+// us: 160 rows take 0.36 instead of 0.27 us, the reason for two MMAs per step);
+// the last epilogue, and every one of the wide form, takes 4 us per 256 rows;
 // sharing costs a second kernel (6 us) and the partials' way through L2
-// (3.5 GB per ms).  1024 rows: 64 tiles of 256 x 256 with K 14336 took 129 us shared by
-// all pairs, and 109 us as 32 wide tiles.
+// (3.5 MB per us).  Estimate and measurement (us): 300 x 14336 x 4096 wide 46 : 46,
+// narrow 48 : 50; 1024 x 8192 x 4096 whole 56 : 59, shared 69 : 75;
+// 4096 x 4096 x 4096 whole 110 : 121, wide 125 : 138.
 Plan make_plan(int h, int per_tile, int64_t M, int64_t K, int64_t N, int num_sms) {
   Plan q;
   q.h = h;
@@ -478,13 +480,18 @@ Plan make_plan(int h, int per_tile, int64_t M, int64_t K, int64_t N, int num_sms
   q.rest = static_cast<int>(sharers ? rest : 0);
   q.sharers = static_cast<int>(sharers);
   q.pairs = static_cast<int>(tiles >= pairs ? pairs : sharers ? sharers : tiles);
-  const double step = std::max((W_BYTES + q.rows() * BK) / 75e3, q.rows() * 0.30 / 256);
-  const double epilogue = q.rows() * 4.0 / 256;
-  const double rounds = static_cast<double>((q.full + pairs - 1) / pairs);
-  q.us = rounds * q.kblocks * step + (h == 2 ? rounds : rounds > 0 ? 1 : 0) * epilogue;
+  const double rows = q.rows();
+  auto step = [&](double active) {       // us per k step while so many pairs work
+    const double load = active / 74.0;
+    return std::max(rows / 256 * (0.30 + 0.137 * load * load), (W_BYTES + rows * BK) * 2 * active / 11.1e6);
+  };
+  const double epilogue = rows * 4.0 / 256;
+  const int64_t rounds = q.full / pairs, last = q.full % pairs;
+  q.us = q.kblocks * (rounds * step(static_cast<double>(pairs)) + (last ? step(static_cast<double>(last)) : 0));
+  q.us += epilogue * (h == 2 ? static_cast<double>(rounds + (last ? 1 : 0)) : q.full > 0 ? 1 : 0);
   if (sharers)
-    q.us += static_cast<double>(rest) * q.kblocks / sharers * step + epilogue + 6 +
-            static_cast<double>(sharers % rest ? sharers + rest : sharers) * q.rows() * BN * 4 / 3.5e6;
+    q.us += static_cast<double>(rest) * q.kblocks / sharers * step(static_cast<double>(sharers)) + epilogue + 6 +
+            static_cast<double>(sharers % rest ? sharers + rest : sharers) * rows * BN * 4 / 3.5e6;
   return q;
 }
 
