@@ -755,9 +755,62 @@ __global__ void __launch_bounds__(THREADS) logprobs_bwd_kernel(const BwdParams p
     if (i == t && !empty) g += hot;
     dx[i] = E::from(g);
   };
+  // N gradients from a vector whose first logit is i
+  auto vec = [&](const uint4& q, int i) {
+    float f[N];
+    E::unpack(q, f);
+    const int rel = t - i;                     // the target's place in this vector
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      float g = grad_of<FAST>(f[e], p.scale, lse, gl, gh, H);
+      if (rel == e) g += hot;
+      f[e] = empty ? 0.f : g;
+    }
+    return E::pack(f);
+  };
   const uintptr_t ax = reinterpret_cast<uintptr_t>(x + lo), ad = reinterpret_cast<uintptr_t>(dx + lo);
-  if (((ax ^ ad) & 15u) != 0) {              // the rows lie differently to 16-byte boundaries
-    for (int i = lo + static_cast<int>(threadIdx.x); i < hi; i += THREADS) one(i);
+  if (((ax ^ ad) & 15u) != 0) {
+    // The rows lie differently to 16-byte boundaries: whole vectors of the
+    // gradient, each from the two vectors of logits that it straddles (the
+    // second comes from L1), as far as both lie within this block's logits.
+    const int misd = static_cast<int>((ad & 15u) / sizeof(T));
+    int b = lo + (misd ? N - misd : 0);                                   // dx + b is aligned
+    const int m = static_cast<int>((reinterpret_cast<uintptr_t>(x + b) & 15u) / sizeof(T));
+    if (b - m < lo) b += N;                                               // x + b - m is aligned
+    const int nv = b - m + 2 * N <= hi ? (hi - (b - m)) / N - 1 : 0;
+    for (int i = lo + static_cast<int>(threadIdx.x); i < min(b, hi); i += THREADS) one(i);
+    for (int i = b + nv * N + static_cast<int>(threadIdx.x); i < hi; i += THREADS) one(i);
+    const uint4* xv = reinterpret_cast<const uint4*>(x + b - m);
+    uint4* dv = reinterpret_cast<uint4*>(dx + b);
+    const int words = m * static_cast<int>(sizeof(T)) / 4;                // 0..3, and half a word
+    const bool half = (m * sizeof(T)) % 4 != 0;
+    constexpr int BATCH = 4;
+    for (int base = static_cast<int>(threadIdx.x); base < nv; base += THREADS * BATCH) {
+      uint4 q[BATCH][2];
+#pragma unroll
+      for (int j = 0; j < BATCH; ++j) {
+        const int k = min(base + j * THREADS, nv - 1);
+        q[j][0] = __ldg(xv + k);
+        q[j][1] = __ldg(xv + k + 1);
+      }
+#pragma unroll
+      for (int j = 0; j < BATCH; ++j) {
+        const int k = base + j * THREADS;
+        if (k < nv) {
+          uint32_t w[8] = {q[j][0].x, q[j][0].y, q[j][0].z, q[j][0].w, q[j][1].x, q[j][1].y, q[j][1].z, q[j][1].w};
+          if (words & 2)
+#pragma unroll
+            for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+          if (words & 1)
+#pragma unroll
+            for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+          if (half)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+          __stcs(dv + k, vec(make_uint4(w[0], w[1], w[2], w[3]), b + k * N));
+        }
+      }
+    }
     return;
   }
   const int mis = static_cast<int>((ax & 15u) / sizeof(T));
@@ -778,18 +831,7 @@ __global__ void __launch_bounds__(THREADS) logprobs_bwd_kernel(const BwdParams p
 #pragma unroll
     for (int j = 0; j < BWD_VECS; ++j) {
       const int i = base + j * THREADS + static_cast<int>(threadIdx.x);
-      if (i < nv) {
-        float f[N];
-        E::unpack(q[j], f);
-        const int rel = t - (b + i * N);       // the target's place in this vector
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-          float g = grad_of<FAST>(f[e], p.scale, lse, gl, gh, H);
-          if (rel == e) g += hot;
-          f[e] = empty ? 0.f : g;
-        }
-        __stcs(dv + i, E::pack(f));
-      }
+      if (i < nv) __stcs(dv + i, vec(q[j], b + i * N));
     }
   }
 }

@@ -483,3 +483,29 @@ def test_offsets_past_32_bits():
     ref = -torch.exp(z - lse[:, None])
     ref.scatter_add_(1, t[rows].long()[:, None], torch.ones(len(rows), 1, device="cuda", dtype=torch.float64))
     assert ((x[rows].double() - ref).abs() <= 2 ** -8 * ref.abs() * (1 + 2 ** -6) + 1e-7).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("V", [1, 3, 17, 40, 1000, 8191, 20007])
+@pytest.mark.parametrize("shift", range(1, 9))
+def test_backward_of_rows_that_lie_differently(dtype, V, shift):
+    """Logits and gradient at every distance to each other's 16-byte
+    boundaries: the same values as with equally placed rows, nothing written
+    beside them."""
+    g = torch.Generator(device="cuda").manual_seed(V)
+    dt = DT[dtype]
+    x0 = (torch.randn(3, V, generator=g, device="cuda") * 3).to(dt)
+    t = torch.randint(0, V, (3,), generator=g, device="cuda", dtype=torch.int32)
+    r = T.token_logprobs(x0, t)
+    gl, gh = torch.randn(3, generator=g, device="cuda"), torch.randn(3, generator=g, device="cuda")
+    ref = T.token_logprobs_backward(x0, t, r.lse, r.entropy, gl, gh)
+    buf = torch.full((3, V + 16), math.nan, dtype=dt, device="cuda")
+    x = buf[:, shift:shift + V]
+    x.copy_(x0)
+    out = torch.full((5, V + 3), 7.0, dtype=dt, device="cuda")
+    T.token_logprobs_backward(x, t, r.lse, r.entropy, gl, gh, out=out[1:4, 1:V + 1])
+    torch.cuda.synchronize()
+    assert torch.equal(out[1:4, 1:V + 1], ref)
+    out[1:4, 1:V + 1] = 7.0
+    assert (out == 7).all()
