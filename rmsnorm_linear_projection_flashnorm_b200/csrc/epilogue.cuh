@@ -17,6 +17,24 @@ namespace fn {
 constexpr int kCounterOffset = 16;
 constexpr int kMaxCounters = static_cast<int>(kWsHeaderBytes) - kCounterOffset;
 
+// CTAs that take a share of tiles x kblocks iterations: all of them, but no
+// more than s to a tile (s rounds of partials to add, kblocks / s iterations to
+// stream: the sum is least near the root of kblocks); or a whole number per
+// tile where that costs at most ALIGN_SLACK iterations more, since a share that
+// ends with its tile has one exchange instead of two, and none if it is whole.
+constexpr unsigned ALIGN_SLACK = 3, WHOLE_SLACK = 8;
+__host__ __device__ __forceinline__ unsigned share_count(int tiles, int kblocks, unsigned ctas) {
+  const unsigned total = static_cast<unsigned>(tiles) * kblocks;
+  unsigned most = total < ctas ? total : ctas;
+  unsigned per_tile = 16;
+  while (per_tile < 64 && per_tile * per_tile < 2u * kblocks) per_tile += 16;
+  if (most > tiles * per_tile) most = tiles * per_tile;
+  const unsigned s = most / tiles;
+  if (s == 0) return most;
+  const unsigned slack = s == 1 ? WHOLE_SLACK : ALIGN_SLACK;
+  return (kblocks + s - 1) / s <= (total + most - 1) / most + slack ? s * tiles : most;
+}
+
 // Count this CTA's partial; true for the last of `n` (which resets the byte).
 // One thread calls it behind a barrier that follows all of the CTA's stores,
 // and a barrier follows before the others' partials are read: the acquire and

@@ -156,6 +156,17 @@ struct ProjArgs {
   int withhold;
   int prefetch_iters;
 };
+// fn_moe_swiglu: what the router writes for the expert kernels.
+constexpr int kMoeMaxRows = 64;
+constexpr int kMoeMaxExperts = 512;
+constexpr int kMoeMaxTopK = 16;
+struct MoeRoute {
+  const int* ids;         // [M][k] chosen experts
+  const float* weight;    // [E][kMoeMaxRows] routing weight, 0 where the row did not choose the expert
+  const float* rinv;      // [M] 1 / rms
+  int E, k;
+};
+
 // Fix-up of the tiles whose k range several CTAs shared (proj_fixup.cu): the
 // partials' layout and the cut.  Sharer c (a CTA, or a pair with ranks == 2)
 // holds iterations [c total / sharers, (c + 1) total / sharers) of the tiles
@@ -169,6 +180,8 @@ struct FixupArgs {
   int kblocks, sharers, ranks;
   int tile0, tiles;
   int group_m, num_m, num_n, rows;   // raster and rows of a tile
+  MoeRoute route;                    // fn_moe_swiglu: its chosen experts (routed ids) multiply kblocks,
+  int routed;                        // and sharers is the number of CTAs
   int64_t M, N;
   Epilogue epi;
   cudaStream_t stream;
@@ -180,17 +193,6 @@ size_t proj_tile_workspace_bytes(int64_t M, int64_t K, int64_t N, int num_sms);
 int64_t proj_tile_count(int64_t M, int64_t N);
 cudaError_t launch_proj_stream(const ProjArgs& a);
 cudaError_t launch_proj_tile(const ProjArgs& a);
-
-// fn_moe_swiglu: what the router writes for the expert kernels.
-constexpr int kMoeMaxRows = 64;
-constexpr int kMoeMaxExperts = 512;
-constexpr int kMoeMaxTopK = 16;
-struct MoeRoute {
-  const int* ids;         // [M][k] chosen experts
-  const float* weight;    // [E][kMoeMaxRows] routing weight, 0 where the row did not choose the expert
-  const float* rinv;      // [M] 1 / rms
-  int E, k;
-};
 
 struct MoeArgs {
   const void* x;          // bf16 [M, d]

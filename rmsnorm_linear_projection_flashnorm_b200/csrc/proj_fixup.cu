@@ -1,5 +1,6 @@
-// Fix-up of fn_proj: adds the fp32 partials of the tiles whose k range several
-// CTAs shared, in ascending k order, and runs the epilogue, sm_100a.
+// Fix-up of fn_proj and of fn_moe_swiglu's down projection: adds the fp32
+// partials of the tiles whose k range several CTAs shared, in ascending k order,
+// and runs the epilogue, sm_100a.
 //
 // One thread per (tile, 8 rows, column): all SMs take part, so its cost is a
 // launch and one round through L2 (about 4 us).  The CTA that happens to be
@@ -30,9 +31,28 @@ __global__ void __launch_bounds__(THREADS) proj_fixup_kernel(const FixupArgs p) 
   const int rank = b % p.ranks;
   const int t = b / p.ranks;                           // tile, from tile0 on
   const int n = static_cast<int>(threadIdx.x & 127);
-  const long long t0 = static_cast<long long>(t) * p.kblocks;
-  const int first = static_cast<int>(div64((t0 + 1) * p.sharers - 1, p.total));
-  const int last = static_cast<int>(div64((t0 + p.kblocks) * p.sharers - 1, p.total));
+  int kblocks = p.kblocks, sharers = p.sharers;
+  long long total = p.total;
+  if (p.routed) {
+    // The experts are counted as the down kernel counted them; the router's ids
+    // were complete before that kernel could launch.
+    __shared__ uint32_t chosen[kMoeMaxExperts / 32];
+    for (int i = threadIdx.x; i < kMoeMaxExperts / 32; i += THREADS) chosen[i] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.routed; i += THREADS) {
+      const int e = __ldcg(p.route.ids + i);
+      atomicOr(&chosen[e >> 5], 1u << (e & 31));
+    }
+    __syncthreads();
+    int n = 0;
+    for (int i = 0; i < kMoeMaxExperts / 32; ++i) n += __popc(chosen[i]);
+    kblocks *= n;
+    total = static_cast<long long>(p.tiles) * kblocks;
+    sharers = static_cast<int>(share_count(p.tiles, kblocks, static_cast<unsigned>(p.sharers)));
+  }
+  const long long t0 = static_cast<long long>(t) * kblocks;
+  const int first = static_cast<int>(div64((t0 + 1) * sharers - 1, total));
+  const int last = static_cast<int>(div64((t0 + kblocks) * sharers - 1, total));
   const int tile = p.tile0 + t;
   const int per_group = p.group_m * p.num_n;
   const int first_m = tile / per_group * p.group_m;
@@ -51,7 +71,7 @@ __global__ void __launch_bounds__(THREADS) proj_fixup_kernel(const FixupArgs p) 
 #pragma unroll
     for (int j = 0; j < IN_FLIGHT; ++j) {
       const int c = min(c0 + j, last);
-      const int64_t slot = (static_cast<int64_t>(c) * p.ranks + rank) * 2 + (div64(c * p.total, p.sharers) >= t0 ? 0 : 1);
+      const int64_t slot = (static_cast<int64_t>(c) * p.ranks + rank) * 2 + (div64(c * total, sharers) >= t0 ? 0 : 1);
       const float4* src = reinterpret_cast<const float4*>(p.part + slot * p.slot_floats) + g * 128 + n;
       q[j][0] = __ldcg(src);
       q[j][1] = __ldcg(src + second);

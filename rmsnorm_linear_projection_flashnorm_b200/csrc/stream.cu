@@ -32,8 +32,8 @@
 // share a tile write fp32 partials to the workspace.  With few rows, and for
 // the experts, they count themselves, and the one that counts last adds all
 // partials in ascending k order (a fixed order, so repeats are bit-identical)
-// and finishes; kProj above 16 rows leaves that to the fix-up kernel.  No CTA
-// waits for another.
+// and finishes; kProj and kDown above 16 rows leave that to the fix-up kernel.
+// No CTA waits for another.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -49,9 +49,7 @@ constexpr int BK = 64;
 constexpr int NUM_THREADS = 192;           // producer, MMA issuer, 4 epilogue warps
 constexpr int W_BOX_BYTES = 64 * BK * 2;   // 64 columns x 64 k rows
 constexpr int RC = 8;                      // rows of an epilogue chunk
-constexpr int MAX_SHARE = 16;              // CTAs to a tile: the last one reads all their partials
-constexpr unsigned ALIGN_SLACK = 3, WHOLE_SLACK = 8;
-constexpr int FIXUP_ROWS = 16;             // kProj: more rows than these are finished by the fix-up kernel
+constexpr int FIXUP_ROWS = 16;             // kProj, kDown: more rows than these are finished by the fix-up kernel
 
 // kProjRows: kProj where CTAs finish whole tiles of more than RC rows.
 enum Mode : int { kProj = 0, kUp = 1, kDown = 2, kProjRows = 3 };
@@ -71,7 +69,7 @@ struct Params {
   const uint8_t* w;              // weight base and row bytes (L2 prefetch addresses, kProj)
   int64_t w_row_bytes;
   int prefetch_iters;
-  int fixup;                     // kProj: shared tiles are finished by the fix-up kernel
+  int fixup;                     // kProj, kDown: shared tiles are finished by the fix-up kernel
   Epilogue epi;                  // kProj, kDown
   int vec;                       // kProj: the epilogue's vector form applies
   MoeRoute route;                // kUp, kDown
@@ -102,6 +100,7 @@ struct alignas(16) Bars {
   uint32_t tmem_base;
   int abort_flag;
   float swap[SWAP ? 2 : 1][2][SWAP ? RC / 2 * 64 : 1];   // kUp: rows passed between the gate and the up threads
+  float weight[2][kMoeMaxRows], rinv[kMoeMaxRows];   // kUp: of the segment's expert; of the rows
   int epi_ok[2];
   int last;                        // the count of the tile's contributors is complete
   int n_active;
@@ -122,20 +121,6 @@ static_assert(smem_bytes<32, 2, kUp>() + smem_bytes<32, 1, kDown>() + 2048 <= 23
                   smem_bytes<16, 2, kUp>() + smem_bytes<16, 1, kDown>() + 2048 <= 233472 &&
                   smem_bytes<16, 1, kUp>() + smem_bytes<16, 1, kDown>() + 2048 <= 233472,
               "two CTAs to an SM");
-
-// CTAs that take a share of tiles x kblocks iterations: all of them, but no
-// more than MAX_SHARE to a tile; or a whole number per tile where that costs
-// at most ALIGN_SLACK iterations more, since a share that ends with its tile
-// has one exchange instead of two.
-__host__ __device__ __forceinline__ unsigned share_count(int tiles, int kblocks, unsigned ctas) {
-  const unsigned total = static_cast<unsigned>(tiles) * kblocks;
-  unsigned most = total < ctas ? total : ctas;
-  if (most > static_cast<unsigned>(tiles) * MAX_SHARE) most = static_cast<unsigned>(tiles) * MAX_SHARE;
-  const unsigned s = most / tiles;
-  if (s == 0) return most;
-  const unsigned slack = s == 1 ? WHOLE_SLACK : ALIGN_SLACK;
-  return (kblocks + s - 1) / s <= (total + most - 1) / most + slack ? s * tiles : most;
-}
 
 __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, unsigned long long budget) {
   const uint64_t t0 = globaltimer_ns();
@@ -407,6 +392,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       grid_dependency_wait();
       grid_launch_dependents();
     }
+    if (MODE == kUp && et < MPAD) bars.rinv[et] = et < p.M ? __ldcg(p.route.rinv + et) : 0.f;
     int next_tile = first_tile, next_kb = first_kb, left = share;
     for (int seg = 0; left > 0; ++seg) {
       const int tile = next_tile, kb0 = next_kb;
@@ -416,6 +402,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       next_kb = 0;
       const int b = seg & 1;
       const uint32_t aph = (seg >> 1) & 1;
+      if (MODE == kUp && et < MPAD)               // what the tile's expert weighs in each row
+        bars.weight[seg & 1][et] =
+            et < p.M ? __ldcg(p.route.weight + bars.experts[tile / p.tiles] * kMoeMaxRows + et) : 0.f;
       // One thread waits and the whole group follows its decision, so the
       // group never splits at the named barriers or the .sync.aligned loads.
       if (et == 0) bars.epi_ok[b] = mbar_wait(&bars.acc_full[b], aph, ctl, kSiteEpiAccFull) ? 1 : 0;
@@ -427,12 +416,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       float w[RC], r[RC];                         // kUp: routing weight and 1 / rms of the chunk's rows
       auto route = [&](int m0) {
         if constexpr (MODE == kUp) {
-          const float* wt = p.route.weight + bars.experts[tile / p.tiles] * kMoeMaxRows + m0;
 #pragma unroll
           for (int j = 0; j < RC; ++j) {
-            const int m = min(j, p.M - 1 - m0);          // rows past the end are not stored
-            w[j] = __ldcg(wt + m);
-            r[j] = __ldcg(p.route.rinv + m0 + m);
+            w[j] = bars.weight[seg & 1][m0 + j];
+            r[j] = bars.rinv[m0 + j];
           }
         }
       };
@@ -526,7 +513,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       tc_fence_before();
       mbar_arrive(&bars.acc_empty[b]);
-      if (is_proj<MODE> && p.fixup) continue;
+      if (MODE != kUp && p.fixup) continue;
       const unsigned t0 = static_cast<unsigned>(tile) * kblocks;
       const int c_first = static_cast<int>(owner_of(t0)), c_last = static_cast<int>(owner_of(t0 + kblocks - 1));
       route(0);
@@ -722,13 +709,32 @@ static cudaError_t launch_experts(strm::Params& p, const MoeArgs& a, const CUten
   p.tiles = static_cast<int>(a.I / (64 * UP_HALVES));
   p.kblocks = static_cast<int>(a.d / BK);
   p.wrows = static_cast<int>(a.d);
-  const cudaError_t e = strm::launch<MPAD, UP_HALVES, kUp>(p, maps[0], maps[1], a.num_sms, a.stream);
+  cudaError_t e = strm::launch<MPAD, UP_HALVES, kUp>(p, maps[0], maps[1], a.num_sms, a.stream);
   if (e != cudaSuccess) return e;
   p.ncols = static_cast<int>(a.d);
   p.tiles = static_cast<int>((a.d + 127) / 128);
   p.kblocks = static_cast<int>(a.I / BK);
   p.wrows = static_cast<int>(a.I);
-  return strm::launch<MPAD, 1, kDown>(p, maps[2], maps[3], a.num_sms, a.stream);
+  p.fixup = a.M > FIXUP_ROWS;
+  e = strm::launch<MPAD, 1, kDown>(p, maps[2], maps[3], a.num_sms, a.stream);
+  if (e != cudaSuccess || !p.fixup) return e;
+  FixupArgs f = {};
+  f.part = p.part;
+  f.slot_floats = MPAD * 128;
+  f.kblocks = p.kblocks;                 // per expert: the kernel counts the experts
+  f.route = p.route;
+  f.routed = static_cast<int>(a.M) * a.top_k;
+  f.sharers = a.num_sms < kMaxCounters ? a.num_sms : kMaxCounters;
+  f.ranks = 1;
+  f.tiles = p.tiles;
+  f.group_m = f.num_m = 1;
+  f.num_n = p.tiles;
+  f.rows = static_cast<int>((a.M + 3) / 4 * 4);
+  f.M = a.M;
+  f.N = a.d;
+  f.epi = p.epi;
+  f.stream = a.stream;
+  return launch_proj_fixup(f);
 }
 
 cudaError_t launch_moe(const MoeArgs& a) {
