@@ -44,14 +44,20 @@ constexpr int PER_THREAD = kMoeMaxExperts / THREADS; // experts a thread chooses
 constexpr double SCALE = 0x1p600, UNSCALE = 0x1p296;
 
 struct Smem {
-  double part[WARPS][4][PER_RANK];     // [warp][row][expert / RANKS]
+  union {
+    double part[WARPS][4][PER_RANK];   // [warp][row][expert / RANKS]
+    double key[kMoeMaxExperts];        // later: what the choice goes by
+  };
   double ssq[WARPS][4];
   double dot[4][PER_RANK];             // [row][expert / RANKS], read by the other ranks
-  double key[kMoeMaxExperts];
   double chosen[kMoeMaxTopK];          // scores, best first
   double red[WARPS];
   double r;
 };
+// The gate/up kernel's CTAs start beside this kernel's: at most 20 KB of shared
+// memory and 128 registers a thread leave room for them.  (16 experts in flight
+// took 171 registers, and 16 rows of 4544, 4 of 5 experts 48 us instead of 37.)
+static_assert(sizeof(Smem) <= 20 * 1024, "beside a gate/up CTA");
 
 struct Params {
   const __nv_bfloat16* x;
@@ -94,7 +100,7 @@ __device__ __forceinline__ double widen(uint32_t b) {
 }
 
 template <int ROWS>
-__global__ void __cluster_dims__(RANKS, 1, 1) __launch_bounds__(THREADS) router_kernel(const Params p) {
+__global__ void __cluster_dims__(RANKS, 1, 1) __launch_bounds__(THREADS, 2) router_kernel(const Params p) {
   constexpr int GROUP = 8 / ROWS < 4 ? 4 : 8 / ROWS;      // experts in flight
   constexpr int NV = ROWS * GROUP;
   __shared__ Smem sm;

@@ -117,6 +117,7 @@ static_assert(smem_bytes<16, 1, kProjRows>() <= 232448 && smem_bytes<32, 1, kPro
                   smem_bytes<64, 1, kProjRows>() <= 232448 && smem_bytes<128, 1, kProjRows>() <= 232448 &&
                   smem_bytes<64, 2, kUp>() <= 232448,
               "shared memory budget");
+static_assert(smem_bytes<64, 2, kUp>() + 20 * 1024 + 2048 <= 233472, "the router's CTA beside gate/up's");
 static_assert(smem_bytes<32, 2, kUp>() + smem_bytes<32, 1, kDown>() + 2048 <= 233472 &&
                   smem_bytes<16, 2, kUp>() + smem_bytes<16, 1, kDown>() + 2048 <= 233472 &&
                   smem_bytes<16, 1, kUp>() + smem_bytes<16, 1, kDown>() + 2048 <= 233472,
