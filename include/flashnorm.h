@@ -468,7 +468,8 @@ typedef enum {
  * routing weight, and the result once, after the residual.  Only the chosen
  * experts' weights are read.  A row with a non-finite activation has NaN or
  * infinite outputs in its own row only.  M == 0 is a no-op.  Three launches
- * (router, gate/up, down), deterministic.  After FN_ERR_TIMEOUT in the status
+ * (router, gate/up, down; above 16 rows a fix-up behind either of the latter),
+ * deterministic.  After FN_ERR_TIMEOUT in the status
  * word the workspace must be zeroed before its next use.
  */
 fn_status fn_moe_swiglu(const void* x, int64_t M, int64_t d, const float* g, const void* router, int64_t E,

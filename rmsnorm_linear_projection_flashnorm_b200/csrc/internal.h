@@ -292,10 +292,10 @@ void count_launch();
 // run its prologue) while the preceding kernel in the stream finishes; it
 // calls griddepcontrol.wait before touching global memory.
 template <typename... Params, typename... Args>
-cudaError_t launch_pdl(void (*kernel)(Params...), unsigned grid, unsigned block, size_t smem, cudaStream_t stream,
+cudaError_t launch_pdl_grid(void (*kernel)(Params...), dim3 grid, unsigned block, size_t smem, cudaStream_t stream,
                        Args&&... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -307,6 +307,12 @@ cudaError_t launch_pdl(void (*kernel)(Params...), unsigned grid, unsigned block,
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
   if (e == cudaSuccess) count_launch();
   return e;
+}
+
+template <typename... Params, typename... Args>
+cudaError_t launch_pdl(void (*kernel)(Params...), unsigned grid, unsigned block, size_t smem, cudaStream_t stream,
+                       Args&&... args) {
+  return launch_pdl_grid(kernel, dim3(grid), block, smem, stream, std::forward<Args>(args)...);
 }
 
 // Same, with thread-block clusters of `cluster` CTAs along x.

@@ -32,8 +32,8 @@
 // share a tile write fp32 partials to the workspace.  With few rows, and for
 // the experts, they count themselves, and the one that counts last adds all
 // partials in ascending k order (a fixed order, so repeats are bit-identical)
-// and finishes; kProj and kDown above 16 rows leave that to the fix-up kernel.
-// No CTA waits for another.
+// and finishes; above 16 rows a fix-up kernel does (kUp: where few experts' tiles
+// are all shared).  No CTA waits for another.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -49,7 +49,7 @@ constexpr int BK = 64;
 constexpr int NUM_THREADS = 192;           // producer, MMA issuer, 4 epilogue warps
 constexpr int W_BOX_BYTES = 64 * BK * 2;   // 64 columns x 64 k rows
 constexpr int RC = 8;                      // rows of an epilogue chunk
-constexpr int FIXUP_ROWS = 16;             // kProj, kDown: more rows than these are finished by the fix-up kernel
+constexpr int FIXUP_ROWS = 16;             // shared tiles of more rows are left to a fix-up kernel
 
 // kProjRows: kProj where CTAs finish whole tiles of more than RC rows.
 enum Mode : int { kProj = 0, kUp = 1, kDown = 2, kProjRows = 3 };
@@ -69,7 +69,7 @@ struct Params {
   const uint8_t* w;              // weight base and row bytes (L2 prefetch addresses, kProj)
   int64_t w_row_bytes;
   int prefetch_iters;
-  int fixup;                     // kProj, kDown: shared tiles are finished by the fix-up kernel
+  int fixup;                     // shared tiles are left to a fix-up kernel
   Epilogue epi;                  // kProj, kDown
   int vec;                       // kProj: the epilogue's vector form applies
   MoeRoute route;                // kUp, kDown
@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       tc_fence_before();
       mbar_arrive(&bars.acc_empty[b]);
-      if (MODE != kUp && p.fixup) continue;
+      if (p.fixup) continue;
       const unsigned t0 = static_cast<unsigned>(tile) * kblocks;
       const int c_first = static_cast<int>(owner_of(t0)), c_last = static_cast<int>(owner_of(t0 + kblocks - 1));
       route(0);
@@ -584,6 +584,85 @@ cudaError_t launch(Params& p, const CUtensorMap& tx, const CUtensorMap& tw, int 
   // the experts' space is known to the kernel only
   const unsigned grid = is_proj<MODE> ? share_count(p.tiles, p.kblocks, num_sms) : static_cast<unsigned>(num_sms);
   return launch_pdl(stream_kernel<MPAD, HALVES, MODE>, grid, NUM_THREADS, SMEM, stream, tx, tw, p);
+}
+
+// Fix-up of kUp (128 + 128 columns) above FIXUP_ROWS: adds the partials of the
+// shared tiles in ascending k order and stores their activations.  A tile is
+// shared where a share begins inside it; the block row of its second sharer
+// takes it.  One thread per (4 rows, column), 64 rows in 8 blocks.
+constexpr int UP_FIX_THREADS = 256;
+__global__ void __launch_bounds__(UP_FIX_THREADS) up_fixup_kernel(const Params p, int mpad, int ctas) {
+  __shared__ uint32_t chosen[kMoeMaxExperts / 32];
+  grid_launch_dependents();              // the down kernel waits for this one before it reads what either wrote
+  // The router's ids: complete before the gate/up kernel could let this one start.
+  for (int i = threadIdx.x; i < kMoeMaxExperts / 32; i += UP_FIX_THREADS) chosen[i] = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < p.M * p.route.k; i += UP_FIX_THREADS) {
+    const int e = __ldcg(p.route.ids + i);
+    atomicOr(&chosen[e >> 5], 1u << (e & 31));
+  }
+  __syncthreads();
+  int active = 0;
+  for (int i = 0; i < kMoeMaxExperts / 32; ++i) active += __popc(chosen[i]);
+  const int tiles = p.tiles * active;
+  const unsigned total = static_cast<unsigned>(tiles) * p.kblocks;
+  const unsigned grid = share_count(tiles, p.kblocks, static_cast<unsigned>(ctas));
+  const unsigned c = blockIdx.x;
+  const int g = static_cast<int>(blockIdx.y) * 2 + static_cast<int>(threadIdx.x >> 7);   // group of 4 rows
+  const int n = static_cast<int>(threadIdx.x & 127);
+  auto begin = [&](unsigned i) { return i * total / grid; };
+  const unsigned tile = c < grid ? begin(c) / p.kblocks : 0, t0 = tile * p.kblocks;
+  const unsigned first = ((t0 + 1) * grid - 1) / total, last = ((t0 + p.kblocks) * grid - 1) / total;
+  const bool mine = c > 0 && c < grid && begin(c) != t0 && first + 1 == c;
+  grid_dependency_wait();
+  if (!mine || 4 * g >= p.M) return;
+  float4 sum[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+  const int64_t half = static_cast<int64_t>(mpad / 4) * 128;      // float4s of a half
+  constexpr unsigned IN_FLIGHT = 4;
+  for (unsigned c0 = first; c0 <= last; c0 += IN_FLIGHT) {
+    float4 q[IN_FLIGHT][2];
+#pragma unroll
+    for (unsigned j = 0; j < IN_FLIGHT; ++j) {
+      const unsigned o = min(c0 + j, last);
+      const float4* src = reinterpret_cast<const float4*>(p.part) +
+                          (static_cast<int64_t>(o) * 2 + (begin(o) >= t0 ? 0 : 1)) * 2 * half + g * 128 + n;
+      q[j][0] = __ldcg(src);
+      q[j][1] = __ldcg(src + half);
+    }
+#pragma unroll
+    for (unsigned j = 0; j < IN_FLIGHT; ++j) {
+      if (c0 + j <= last) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          sum[h].x += q[j][h].x;
+          sum[h].y += q[j][h].y;
+          sum[h].z += q[j][h].z;
+          sum[h].w += q[j][h].w;
+        }
+      }
+    }
+  }
+  const int slot = static_cast<int>(tile) / p.tiles;
+  int expert = 0;                        // the slot-th chosen one
+  for (int left = slot, w = 0; w < kMoeMaxExperts / 32; ++w) {
+    const int here = __popc(chosen[w]);
+    if (left < here) {
+      expert = w * 32 + static_cast<int>(__fns(chosen[w], 0, left + 1));
+      break;
+    }
+    left -= here;
+  }
+  const float gate[4] = {sum[0].x, sum[0].y, sum[0].z, sum[0].w}, up[4] = {sum[1].x, sum[1].y, sum[1].z, sum[1].w};
+  const float* wt = p.route.weight + expert * kMoeMaxRows;
+  __nv_bfloat16* dst =
+      p.act + (static_cast<int64_t>(slot) * mpad + 4 * g) * p.ncols + static_cast<int>(tile) % p.tiles * 128 + n;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int m = min(4 * g + j, p.M - 1);
+    const float w = __ldcg(wt + m), r = __ldcg(p.route.rinv + m);
+    const float v = w * (silu_f32(gate[j] * r) * (up[j] * r));
+    if (4 * g + j < p.M) dst[static_cast<int64_t>(j) * p.ncols] = __float2bfloat16_rn(w != 0.f ? v : 0.f);
+  }
 }
 
 // Partials: two slots per CTA.
@@ -710,8 +789,22 @@ static cudaError_t launch_experts(strm::Params& p, const MoeArgs& a, const CUten
   p.tiles = static_cast<int>(a.I / (64 * UP_HALVES));
   p.kblocks = static_cast<int>(a.d / BK);
   p.wrows = static_cast<int>(a.d);
+  // Gate/up: only where no CTA finishes whole tiles (55 rows, 5 experts of 4544 x
+  // 384: layer 50 -> 38 us); among whole ones the last sharer's work hides (40 rows,
+  // 256 experts of 4096 x 256: 238 us, 244 with the fix-up kernel).
+  const int64_t slots = a.E < a.M * a.top_k ? a.E : a.M * a.top_k;
+  p.fixup = a.M > FIXUP_ROWS && slots * p.tiles < a.num_sms;
+  const int ctas = a.num_sms < kMaxCounters ? a.num_sms : kMaxCounters;
   cudaError_t e = strm::launch<MPAD, UP_HALVES, kUp>(p, maps[0], maps[1], a.num_sms, a.stream);
   if (e != cudaSuccess) return e;
+  if (p.fixup) {
+    static_assert(UP_HALVES == 2 || MPAD <= FIXUP_ROWS, "the fix-up adds gate and up");
+    e = ensure_shared<up_fixup_kernel>(0);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl_grid(up_fixup_kernel, dim3(static_cast<unsigned>(ctas), static_cast<unsigned>((a.M + 7) / 8)),
+                        UP_FIX_THREADS, 0, a.stream, p, MPAD, ctas);
+    if (e != cudaSuccess) return e;
+  }
   p.ncols = static_cast<int>(a.d);
   p.tiles = static_cast<int>((a.d + 127) / 128);
   p.kblocks = static_cast<int>(a.I / BK);
@@ -725,7 +818,7 @@ static cudaError_t launch_experts(strm::Params& p, const MoeArgs& a, const CUten
   f.kblocks = p.kblocks;                 // per expert: the kernel counts the experts
   f.route = p.route;
   f.routed = static_cast<int>(a.M) * a.top_k;
-  f.sharers = a.num_sms < kMaxCounters ? a.num_sms : kMaxCounters;
+  f.sharers = ctas;
   f.ranks = 1;
   f.tiles = p.tiles;
   f.group_m = f.num_m = 1;

@@ -414,3 +414,16 @@ def test_weights_past_32_bits():
     sb[torch.tensor([0, 68, 70, 71])] = 10.0                # the first and the last experts
     for M in (1, 20):
         check(layer, M, 4, select_bias=sb)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [17, 32, 33, 55, 64])
+@pytest.mark.parametrize("d,I,E,k", [(4544, 384, 5, 4), (64, 6912, 3, 2), (192, 2176, 16, 8), (1536, 512, 4, 1), (5120, 128, 1, 1)])
+def test_shared_tiles_of_many_rows(M, d, I, E, k):
+    """Few tiles with long k ranges: every tile of both products is shared by
+    many CTAs, and fix-up kernels finish them."""
+    layer = Layer(d, I, E, seed=d + E)
+    ws = T.Workspace("cuda")
+    check(layer, M, k, seed=M, ws=ws)
+    check(layer, M, k, seed=M + 1, ws=ws, alias=True)
+    assert ws.status()[0] == fnb.FN_OK and (ws.buf[:256] == 0).all()
