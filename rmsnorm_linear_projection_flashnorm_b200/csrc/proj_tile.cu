@@ -398,12 +398,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
           for (int c = half; c < 2 * chunks; c += 2) {
             const int r0 = row0 + 16 * c;
             if (r0 >= p.M) break;
-            uint32_t v[16];
-            float z[16];
-            tmem_ld16(taddr + c * 16, v);
-            tmem_ld_wait();
-            epi_transpose_act(p.epi, scratch, lane, bias, v, z);
-            epi_store_scalar<F32>(p.epi, lane, r0, min(p.M - r0, 16), col0, p.N, z);
+            float v[16];
+            dec::tmem_ld_cols<16>(taddr + c * 16, v);
+            if (col0 + lane < p.N) epi_finish<16>(p.epi, r0, min(p.M - r0, 16), col0 + lane, v);
           }
         }
         release();
@@ -449,7 +446,7 @@ struct Plan {
   int rows() const { return h * nb; }
 };
 
-// One way to cut: tiles of h MMAs; the tiles of the last, partial round whole
+// One way to cut: tiles of h MMAs of at most most_rows rows; the tiles of the last, partial round whole
 // (per_tile 0), shared evenly by per_tile pairs each, or by all pairs (-1).
 //
 // The estimate, from measurements of this kernel: a k step is bound by the
@@ -461,10 +458,10 @@ struct Plan {
 // (3.5 MB per us).  Estimate and measurement (us): 300 x 14336 x 4096 wide 46 : 46,
 // narrow 48 : 50; 1024 x 8192 x 4096 whole 56 : 59, shared 69 : 75;
 // 4096 x 4096 x 4096 whole 110 : 121, wide 125 : 138.
-Plan make_plan(int h, int per_tile, int64_t M, int64_t K, int64_t N, int num_sms) {
+Plan make_plan(int h, int most_rows, int per_tile, int64_t M, int64_t K, int64_t N, int num_sms) {
   Plan q;
   q.h = h;
-  const int64_t blocks = (M + h * MAX_NB - 1) / (h * MAX_NB);
+  const int64_t blocks = (M + h * most_rows - 1) / (h * most_rows);
   q.num_m = static_cast<int>(blocks);
   q.nb = static_cast<int>(((M + h * blocks - 1) / (h * blocks) + 31) / 32 * 32);
   q.num_n = static_cast<int>((N + BN - 1) / BN);
@@ -496,12 +493,16 @@ Plan make_plan(int h, int per_tile, int64_t M, int64_t K, int64_t N, int num_sms
 }
 
 Plan best_plan(int64_t M, int64_t K, int64_t N, int num_sms) {
-  Plan best = make_plan(1, 0, M, K, N, num_sms);
+  Plan best = make_plan(1, MAX_NB, 0, M, K, N, num_sms);
+  auto consider = [&](const Plan& q) {
+    if (q.us < best.us) best = q;
+  };
   for (int h = 1; h <= (M > MAX_NB ? 2 : 1); ++h)
-    for (int per_tile = -1; per_tile <= 8; ++per_tile) {
-      const Plan q = make_plan(h, per_tile, M, K, N, num_sms);
-      if (q.us < best.us) best = q;
-    }
+    for (int per_tile = -1; per_tile <= 8; ++per_tile) consider(make_plan(h, MAX_NB, per_tile, M, K, N, num_sms));
+  // fewer rows to a tile, while that makes work for idle pairs (with a short K
+  // the epilogue is most of a tile)
+  for (int rows = MAX_NB / 2; rows >= 32 && best.num_m * best.num_n < num_sms / 2; rows /= 2)
+    consider(make_plan(1, rows, 0, M, K, N, num_sms));
   return best;
 }
 

@@ -133,26 +133,32 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, unsig
 // kProj: all rows of this warp's 32 columns, from its TMEM lanes.
 template <bool F32>
 __device__ __forceinline__ void finish_rows(const Params& p, uint32_t taddr, float* scratch, int lane, int64_t col0) {
+  if (!p.vec) {
+#pragma unroll 1
+    for (int m0 = 0; m0 < p.M; m0 += 16) {
+      float v[16];
+      dec::tmem_ld_cols<16>(taddr + m0, v);
+      if (col0 + lane < p.ncols) epi_finish<16>(p.epi, m0, min(p.M - m0, 16), col0 + lane, v);
+    }
+    return;
+  }
   float4 bias = make_float4(0.f, 0.f, 0.f, 0.f);
   if (p.epi.bias) {
     const int64_t last = p.ncols - 1, c = col0 + lane % 8 * 4;
     bias = make_float4(__ldg(p.epi.bias + min(c, last)), __ldg(p.epi.bias + min(c + 1, last)),
                        __ldg(p.epi.bias + min(c + 2, last)), __ldg(p.epi.bias + min(c + 3, last)));
   }
-  const bool ahead = p.vec && p.epi.residual;
   typename Quad<F32>::Raw raw[2][4];
-  if (ahead) epi_fetch<F32>(p.epi, lane, 0, min(p.M, 16), col0, p.ncols, raw[0]);
+  if (p.epi.residual) epi_fetch<F32>(p.epi, lane, 0, min(p.M, 16), col0, p.ncols, raw[0]);
 #pragma unroll 1
   for (int m0 = 0; m0 < p.M; m0 += 16) {
-    const int rows = min(p.M - m0, 16);
     uint32_t v[16];
     float z[16];
     tmem_ld16(taddr + m0, v);
-    if (ahead) epi_fetch<F32>(p.epi, lane, m0 + 16, min(p.M - m0 - 16, 16), col0, p.ncols, raw[1]);
+    if (p.epi.residual) epi_fetch<F32>(p.epi, lane, m0 + 16, min(p.M - m0 - 16, 16), col0, p.ncols, raw[1]);
     tmem_ld_wait();
     epi_transpose_act(p.epi, scratch, lane, bias, v, z);
-    if (p.vec) epi_store_vec<F32>(p.epi, raw[0], lane, m0, rows, col0, p.ncols, z);
-    else epi_store_scalar<F32>(p.epi, lane, m0, rows, col0, p.ncols, z);
+    epi_store_vec<F32>(p.epi, raw[0], lane, m0, min(p.M - m0, 16), col0, p.ncols, z);
 #pragma unroll
     for (int g = 0; g < 4; ++g) raw[0][g] = raw[1][g];
   }

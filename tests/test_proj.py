@@ -333,3 +333,12 @@ def test_few_rows_many_columns(M, K, N):
     case(M, K, N, residual=True, bias=True, seed=M)
     aligned(M, K, N, False, True, "none", seed=K)
     aligned(M, K, N, True, False, "silu", seed=K)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,K,N", [(3737, 75, 110), (2671, 151, 29), (498, 416, 277), (590, 64, 64), (1000, 512, 512), (130, 1024, 260)])
+@pytest.mark.parametrize("fp32", [False, True])
+def test_small_tiles(M, K, N, fp32):
+    """Few tiles and a short k range: fewer rows to a tile."""
+    case(M, K, N, residual=True, bias=True, act="gelu", fp32=fp32, seed=M)
+    aligned(M, K, N, fp32, True, "silu", seed=N)
