@@ -266,25 +266,6 @@ cudaError_t ensure_smem_limit(int bytes) {
   return e;
 }
 
-// The same, and the whole of the SM's carve-out as shared memory.  Kernels that
-// overlap by programmatic launch share an SM only under one carve-out, and a
-// change of it waits until the SM is idle: left to the driver, which followed
-// the process's earlier launches, a mixture-of-experts call took 35 or 49 us.
-template <auto Kernel>
-cudaError_t ensure_shared(int dynamic_bytes) {
-  static std::atomic<unsigned long long> done{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const unsigned long long bit = 1ull << (dev & 63);
-  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
-  if (dynamic_bytes) e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, dynamic_bytes);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
-  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_acq_rel);
-  return e;
-}
-
 // Process-wide count of kernels enqueued by the library.
 void count_launch();
 

@@ -287,8 +287,6 @@ __global__ void __cluster_dims__(RANKS, 1, 1) __launch_bounds__(THREADS, 2) rout
 
 template <int ROWS>
 cudaError_t launch(const Params& p, cudaStream_t stream) {
-  const cudaError_t e = ensure_shared<router_kernel<ROWS>>(0);
-  if (e != cudaSuccess) return e;
   const int clusters = (p.M + ROWS - 1) / ROWS;
   return launch_pdl(router_kernel<ROWS>, static_cast<unsigned>(clusters * RANKS), THREADS, 0, stream, p);
 }

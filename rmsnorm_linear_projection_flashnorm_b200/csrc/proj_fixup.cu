@@ -95,8 +95,6 @@ __global__ void __launch_bounds__(THREADS) proj_fixup_kernel(const FixupArgs p) 
 }  // namespace fix
 
 cudaError_t launch_proj_fixup(const FixupArgs& a) {
-  const cudaError_t e = ensure_shared<fix::proj_fixup_kernel>(0);
-  if (e != cudaSuccess) return e;
   const unsigned grid = static_cast<unsigned>(a.tiles) * a.ranks * ((a.rows + 15) / 16);
   return launch_pdl(fix::proj_fixup_kernel, grid, fix::THREADS, 0, a.stream, a);
 }

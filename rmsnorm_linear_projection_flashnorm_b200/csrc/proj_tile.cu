@@ -25,8 +25,8 @@
 // bit-identical repeats).
 //
 // Measured (device time a call): 4096 x 14336 x 4096 with bias and residual
-// 347..367 us (1310..1388 TFLOP/s, under the power cap), 1024 x 8192 x 4096 56 us,
-// 300 x 14336 x 4096 45 us.
+// 345..367 us (1310..1396 TFLOP/s, under the power cap), 1024 x 8192 x 4096 57 us,
+// 300 x 14336 x 4096 42 us, 498 x 416 x 277 8 us.
 //
 // Layout per CTA: 10 warps.
 //   warp 0      TMA producer (own weight columns, own rows)
@@ -509,7 +509,7 @@ Plan best_plan(int64_t M, int64_t K, int64_t N, int num_sms) {
 template <bool F32, int H>
 cudaError_t launch_kernel(const Params& p, const Plan& q, cudaStream_t stream, const CUtensorMap& tx,
                           const CUtensorMap& tw) {
-  const cudaError_t e = ensure_shared<proj_tile_kernel<F32, H>>(static_cast<int>(SMEM));
+  const cudaError_t e = ensure_smem_limit<proj_tile_kernel<F32, H>>(static_cast<int>(SMEM));
   if (e != cudaSuccess) return e;
   return launch_pdl(proj_tile_kernel<F32, H>, static_cast<unsigned>(2 * q.pairs), NUM_THREADS, SMEM, stream, tx, tw, p);
 }

@@ -25,8 +25,8 @@
 //
 // Measured (device time a call): 4096 x 4096, one row, 10.6 us, of which the
 // stream takes 4.7 (7.1 TB/s), the first load 0.8, the exchange 3 and the
-// kernel boundary 1.2; 8 experts of 2048 x 1024 and one row 35.8 us with the
-// router's 5.9; 64 rows and 8 experts of 4096 x 14336 489 us (5.8 TB/s).
+// kernel boundary 1.2; 8 experts of 2048 x 1024 and one row 35..37 us with the
+// router's 5.9; 64 rows and 8 experts of 4096 x 14336 478 us (5.9 TB/s).
 //
 // A tile whose k range falls to one CTA is finished by it.  The CTAs that
 // share a tile write fp32 partials to the workspace.  With few rows, and for
@@ -584,7 +584,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 template <int MPAD, int HALVES, int MODE>
 cudaError_t launch(Params& p, const CUtensorMap& tx, const CUtensorMap& tw, int num_sms, cudaStream_t stream) {
   constexpr size_t SMEM = smem_bytes<MPAD, HALVES, MODE>();
-  const cudaError_t e = ensure_shared<stream_kernel<MPAD, HALVES, MODE>>(static_cast<int>(SMEM));
+  const cudaError_t e = ensure_smem_limit<stream_kernel<MPAD, HALVES, MODE>>(static_cast<int>(SMEM));
   if (e != cudaSuccess) return e;
   if (num_sms > kMaxCounters) num_sms = kMaxCounters;
   // the experts' space is known to the kernel only
@@ -805,8 +805,6 @@ static cudaError_t launch_experts(strm::Params& p, const MoeArgs& a, const CUten
   if (e != cudaSuccess) return e;
   if (p.fixup) {
     static_assert(UP_HALVES == 2 || MPAD <= FIXUP_ROWS, "the fix-up adds gate and up");
-    e = ensure_shared<up_fixup_kernel>(0);
-    if (e != cudaSuccess) return e;
     e = launch_pdl_grid(up_fixup_kernel, dim3(static_cast<unsigned>(ctas), static_cast<unsigned>((a.M + 7) / 8)),
                         UP_FIX_THREADS, 0, a.stream, p, MPAD, ctas);
     if (e != cudaSuccess) return e;
