@@ -49,6 +49,7 @@
 #include <cuda_runtime.h>
 #include <cfloat>
 
+#include "dsmem.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 

@@ -28,6 +28,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include "dsmem.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
