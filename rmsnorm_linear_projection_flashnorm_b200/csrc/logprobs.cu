@@ -491,8 +491,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
       st.m = max_nan(st.m, bm);               // NaN stays
     }
     const float mu = __fmul_rn(st.m, c);
-    uint32_t low;                             // nothing below it counts: masked logits are finite from here on
-    if (E::floor_word(st.m + FAR / c, low) && fabsf(mu) < ORDINARY) {
+    // Nothing below `low` counts: masked logits are finite from here on.  Rounded
+    // down, so it stays below the maximum however coarse the steps there are.
+    uint32_t low;
+    if (E::floor_word(__fadd_rd(st.m, FAR / c), low) && fabsf(mu) < ORDINARY) {
       const uint64_t nm2 = f2_pack(-mu, -mu), c2 = f2_pack(c, c);
       uint64_t s2 = f2_pack(st.s, 0.f), t2 = f2_pack(st.t, 0.f);
       auto add = [&](const uint4& v) {

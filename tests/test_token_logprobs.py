@@ -509,3 +509,18 @@ def test_backward_of_rows_that_lie_differently(dtype, V, shift):
     assert torch.equal(out[1:4, 1:V + 1], ref)
     out[1:4, 1:V + 1] = 7.0
     assert (out == 7).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("M,V", [(3, 20011), (5, 70001), (700, 4099)])
+def test_one_logit_far_above_the_others(dtype, M, V):
+    """A token forced by a large bias (2^33: steps of 2^10 in fp32) takes all
+    the probability, wherever it stands and whatever its thread reads after it."""
+    x = logits_(M, V, V, dtype, seed=V)
+    rows = torch.arange(M)
+    t = (rows * 7919) % V
+    t[0], t[1] = 0, V - 1
+    x[rows.cuda(), t.cuda()] = 2.0 ** 33
+    r = check_fwd(x, t.numpy().astype(np.int32), 5, 1.0)
+    assert (r.logprob == 0).all() and (r.entropy == 0).all()
