@@ -8,7 +8,8 @@
 // grows by D the sums become s' = s e^{-D}, t' = e^{-D} (t - s D).  The
 // products run in the base-2 exponent domain, c = scale log2 e, 32-bit floats:
 // d = fma(x, c, -mu) with mu = m c rounded, one instruction for a pair, and the
-// rounding of mu (known exactly, fma(m, c, -mu)) taken out at the end.
+// rounding of mu (known exactly, fma(m, c, -mu)) taken out at the end.  Where
+// that rounding is not small, d = (x - m) c.
 //
 // The pass is bound by HBM (2 or 4 bytes per logit, read once).  The SM side
 // stays below it: per pair of 16-bit logits two ex2 and about 8 issue slots.
@@ -252,13 +253,19 @@ struct Stat {
   float m, s, t;   // maximum (raw logits), sum of 2^d, sum of d 2^d
 };
 // The reference of d for maximum m: d = fma(x, c, -mu) where mu = m c is of
-// ordinary size, else d = (x - m) c (a maximum near the type's lowest value,
-// or infinite).
-constexpr float ORDINARY = 1e30f;
+// ordinary size, else d = (x - m) c (a mask's finite fill, a large scale, a
+// maximum near the type's lowest value, or infinite).  Ordinary ends at 2^24:
+// mu is then off by at most 1/2, so the largest term of the sum, 2^delta with
+// delta = m c - mu, lies within a factor of 2^(1/2) of 1.  (Half a step of mu
+// passes 127 at 2^31; from there 2^delta may be infinite or 0.)
+constexpr float ORDINARY = 0x1p24f;
 __device__ __forceinline__ float distance(float a, float b, float c) {   // of a's reference below b's, >= FAR
   if (a == b) return 0.f;
-  const float mu = __fmul_rn(b, c);
-  return max_nan(fabsf(mu) < ORDINARY ? __fsub_rn(__fmul_rn(a, c), mu) : (a - b) * c, FAR);
+  const float ma = __fmul_rn(a, c), mb = __fmul_rn(b, c);
+  const bool oa = fabsf(ma) < ORDINARY, ob = fabsf(mb) < ORDINARY;
+  // one rounding each, also where one reference is m c rounded and the other m itself
+  const float d = oa ? (ob ? __fsub_rn(ma, mb) : -fmaf(b, c, -ma)) : (ob ? fmaf(a, c, -mb) : (a - b) * c);
+  return max_nan(d, FAR);
 }
 __device__ __forceinline__ Stat merge_stat(const Stat& a, const Stat& b, float c) {
   Stat r;
@@ -518,7 +525,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
       st.s = f2_lo(s2) + f2_hi(s2);
       st.t = f2_lo(t2) + f2_hi(t2);
     } else if (st.m != -INFINITY) {
-      // a maximum near the type's lowest value (or infinite, or NaN): exact differences
+      // a maximum out of the ordinary (or infinite, or NaN): exact differences
 #pragma unroll 1
       for (int j = 0; j < have; ++j) {
         const uint4 v = j == 0 ? q[0] : j == 1 ? q[1] : j == 2 ? q[2] : q[3];

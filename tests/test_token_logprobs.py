@@ -524,3 +524,94 @@ def test_one_logit_far_above_the_others(dtype, M, V):
     x[rows.cuda(), t.cuda()] = 2.0 ** 33
     r = check_fwd(x, t.numpy().astype(np.int32), 5, 1.0)
     assert (r.logprob == 0).all() and (r.entropy == 0).all()
+
+
+FILLS = [("bf16", f) for f in (-1e4, -1e9, -5e9, -1e10, -1e11, -1e12, -1e15, -1e20, -1e30)]
+FILLS += [("fp32", f) for f in (-1e4, -1e7, -1.2e7, -1e9, -5e9, -1e10, -1e11, -1e12, -1e15, -1e20, -1e30)]
+FILLS += [("fp16", f) for f in (-1e4, -65504.0)]
+
+
+def filled_(M, V, dtype, fill, seed):
+    """Rows masked by a finite fill: here and there, in long runs (threads that
+    see nothing else, or nothing else for many tiles), all but one, throughout."""
+    x = logits_(M, V, V, dtype, seed)
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    for m in range(M):
+        if m % 6 == 0:
+            x[m][torch.rand(V, generator=gen, device="cuda") < 0.4] = fill
+        elif m % 6 == 1:
+            x[m, :V * 3 // 4] = fill
+        elif m % 6 == 2:
+            x[m, V // 4:] = fill
+        elif m % 6 == 3:
+            x[m, :m * 37 % V] = fill
+            x[m, m * 37 % V + 1:] = fill
+        elif m % 6 == 4:
+            x[m] = fill
+        else:
+            x[m, :V - 2] = fill
+    return x
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,fill", FILLS)
+def test_forward_masked_by_a_finite_fill(dtype, fill):
+    for M, V, scale in ((6, 50021, 1.0), (12, 3001, 0.7), (606, 4099, 1.0)):
+        check_fwd(filled_(M, V, dtype, fill, seed=V), targets_(M, V, M), 8, scale)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("top", [2e7, 1e10, 1e12, 1e20, 1e30])
+def test_forward_large_logits(dtype, top):
+    """A forced token, two that tie, and rows that lie far up as a whole."""
+    V = 30011
+    x = logits_(5, V, V, dtype, seed=3)
+    x[0, 17] = top
+    x[1, 20000] = top
+    x[2, 5] = x[2, 25000] = top
+    x[3] = x[3] * (top / 4)
+    x[4] = top
+    t = np.array([17, 20000, 25000, 9, 8], dtype=np.int32)
+    check_fwd(x, t, 6, 1.0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("scale", [1e-10, 1e-8, 1e-6, 1e-3, 1e3, 1e6, 1e8, 1e10, 1e20, 1e30])
+def test_forward_scales(dtype, scale):
+    for M, V in ((3, 20011), (600, 2051)):
+        x = logits_(M, V, V, dtype, seed=V, masked=0.1)
+        x[2, 5], x[2, 1900] = x[2].max(), x[2].max()      # a tie for the first place
+        check_fwd(x, targets_(M, V, M), 8, scale)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_forward_between_the_forms(dtype):
+    """Maxima on both sides of 2^24 in units of ln 2, a few units apart, so that
+    threads with either reference of their exponents meet."""
+    V = 20011
+    gen = torch.Generator().manual_seed(0)
+    base = 2.0 ** 24 * math.log(2)
+    for sign in (1.0, -1.0):
+        x = sign * base + torch.randint(-8, 9, (4, V), generator=gen).double()
+        x[1, 1000:] -= 6
+        x[2, :15000] -= 4
+        check_fwd(x.to(DT[dtype]).cuda(), targets_(4, V, 1), 4, 1.0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,fill", FILLS)
+def test_backward_masked_by_a_finite_fill(dtype, fill):
+    """Filled logits have no gradient; a row keeps its other ones."""
+    rng = np.random.default_rng(4)
+    M, V = 12, 9001
+    x = filled_(M, V, dtype, fill, seed=2)
+    x[4::6] = x[0].clone()                                 # (rows with something left)
+    gl, gh = rng.standard_normal(M).astype(np.float32), rng.standard_normal(M).astype(np.float32)
+    t = np.full(M, V - 1, dtype=np.int32)
+    g = check_bwd(x, t, gl, gh, 1.0)
+    off = x == torch.tensor(fill, dtype=x.dtype)
+    off[torch.arange(M), torch.from_numpy(t).long()] = False
+    assert (g[off] == 0).all() and g.isfinite().all()
