@@ -9,7 +9,7 @@
 // products run in the base-2 exponent domain, c = scale log2 e, 32-bit floats:
 // d = fma(x, c, -mu) with mu = m c rounded, one instruction for a pair, and the
 // rounding of mu (known exactly, fma(m, c, -mu)) taken out at the end.  Where
-// that rounding is not small, d = (x - m) c.
+// that rounding is not small, d = (x - m) scale log2 e.
 //
 // The pass is bound by HBM (2 or 4 bytes per logit, read once).  The SM side
 // stays below it: per pair of 16-bit logits two ex2 and about 8 issue slots.
@@ -253,24 +253,28 @@ struct Stat {
   float m, s, t;   // maximum (raw logits), sum of 2^d, sum of d 2^d
 };
 // The reference of d for maximum m: d = fma(x, c, -mu) where mu = m c is of
-// ordinary size, else d = (x - m) c (a mask's finite fill, a large scale, a
+// ordinary size, else d = (x - m) scale log2 e (a mask's finite fill, a large scale, a
 // maximum near the type's lowest value, or infinite).  Ordinary ends at 2^24:
 // mu is then off by at most 1/2, so the largest term of the sum, 2^delta with
 // delta = m c - mu, lies within a factor of 2^(1/2) of 1.  (Half a step of mu
 // passes 127 at 2^31; from there 2^delta may be infinite or 0.)
 constexpr float ORDINARY = 0x1p24f;
-__device__ __forceinline__ float distance(float a, float b, float c) {   // of a's reference below b's, >= FAR
+__device__ __forceinline__ float exact_distance(float x, float m, float scale) {
+  return (x - m) * scale * LOG2E;        // not c: it is infinite at scales above 2.3e38, and 0 times it NaN
+}
+__device__ __forceinline__ float distance(float a, float b, float scale) {   // of a's reference below b's, >= FAR
   if (a == b) return 0.f;
+  const float c = scale * LOG2E;
   const float ma = __fmul_rn(a, c), mb = __fmul_rn(b, c);
   const bool oa = fabsf(ma) < ORDINARY, ob = fabsf(mb) < ORDINARY;
   // one rounding each, also where one reference is m c rounded and the other m itself
-  const float d = oa ? (ob ? __fsub_rn(ma, mb) : -fmaf(b, c, -ma)) : (ob ? fmaf(a, c, -mb) : (a - b) * c);
+  const float d = oa ? (ob ? __fsub_rn(ma, mb) : -fmaf(b, c, -ma)) : (ob ? fmaf(a, c, -mb) : exact_distance(a, b, scale));
   return max_nan(d, FAR);
 }
-__device__ __forceinline__ Stat merge_stat(const Stat& a, const Stat& b, float c) {
+__device__ __forceinline__ Stat merge_stat(const Stat& a, const Stat& b, float scale) {
   Stat r;
   r.m = max_nan(a.m, b.m);
-  const float da = distance(a.m, r.m, c), db = distance(b.m, r.m, c);
+  const float da = distance(a.m, r.m, scale), db = distance(b.m, r.m, scale);
   const float fa = ex2(da), fb = ex2(db);
   r.s = fa * a.s + fb * b.s;
   r.t = fa * fmaf(a.s, da, a.t) + fb * fmaf(b.s, db, b.t);
@@ -490,7 +494,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
     // running softmax statistics
     if (!(bm <= st.m)) {                      // grows, or NaN
       if (st.s > 0.f) {
-        const float D = distance(st.m, bm, c);
+        const float D = distance(st.m, bm, p.scale);
         const float f = ex2(D);
         st.t = f * fmaf(st.s, D, st.t);
         st.s *= f;
@@ -533,7 +537,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
         E::unpack(v, f);
 #pragma unroll
         for (int e = 0; e < N; ++e) {
-          const float d = fabsf(mu) < ORDINARY ? max_nan(fmaf(f[e], c, -mu), FAR) : max_nan((f[e] - st.m) * c, FAR);
+          const float d =
+              max_nan(fabsf(mu) < ORDINARY ? fmaf(f[e], c, -mu) : exact_distance(f[e], st.m, p.scale), FAR);
           const float w = ex2(d);
           st.s += w;
           st.t = fmaf(d, w, st.t);
@@ -586,7 +591,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
     b.m = __shfl_down_sync(0xffffffffu, st.m, o);
     b.s = __shfl_down_sync(0xffffffffu, st.s, o);
     b.t = __shfl_down_sync(0xffffffffu, st.t, o);
-    st = merge_stat(st, b, c);
+    st = merge_stat(st, b, p.scale);
   }
   if (lane == 0) sm.wstat[warp] = st;
   __syncthreads();                            // every thread is done with its vectors
@@ -608,7 +613,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
   }
   if (threadIdx.x == 0) {
     Stat a = sm.wstat[0];
-    for (int w = 1; w < WARPS; ++w) a = merge_stat(a, sm.wstat[w], c);
+    for (int w = 1; w < WARPS; ++w) a = merge_stat(a, sm.wstat[w], p.scale);
     sm.stat = a;
   }
   if (THREADS == MAX_THREADS && p.C > 1) {    // warp w serves rank w
@@ -627,7 +632,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
       if constexpr (TOPK) select_top(sm, p.C * p.k, p.k);
       if (threadIdx.x == 0) {
         Stat a = sm.stat;
-        for (int r = 1; r < p.C; ++r) a = merge_stat(a, sm.wstat[r], c);
+        for (int r = 1; r < p.C; ++r) a = merge_stat(a, sm.wstat[r], p.scale);
         sm.stat = a;
       }
     }

@@ -615,3 +615,19 @@ def test_backward_masked_by_a_finite_fill(dtype, fill):
     off = x == torch.tensor(fill, dtype=x.dtype)
     off[torch.arange(M), torch.from_numpy(t).long()] = False
     assert (g[off] == 0).all() and g.isfinite().all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("scale", [2e38, 3e38, 1e-38, 1e-43])
+def test_forward_scales_at_the_ends_of_the_range(dtype, scale):
+    """Scales whose product with log2 e is infinite or subnormal; every z is a
+    finite fp32 value, every difference too."""
+    V = 20011
+    x = logits_(6, V, V, dtype, seed=1) * (0.02 if scale > 1 else 1e10)
+    x[1] = 0
+    x[2] = x[2] * (2.0 ** -124 if scale > 1 else 1e20)     # z of a few, or all alike
+    x[3, 9:] = -math.inf
+    x[4] = -math.inf
+    x[5, ::2] = x[5, 0]
+    check_fwd(x, targets_(6, V, 3), 8, scale)
