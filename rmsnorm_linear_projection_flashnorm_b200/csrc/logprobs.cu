@@ -8,7 +8,7 @@
 // grows by D the sums become s' = s e^{-D}, t' = e^{-D} (t - s D).  The
 // products run in the base-2 exponent domain, c = scale log2 e, 32-bit floats:
 // d = fma(x, c, -mu) with mu = m c rounded, one instruction for a pair, and the
-// rounding of mu (known exactly, fma(m, c, -mu)) taken out at the end.  Where
+// rounding of mu (known exactly, fma(m, c, -mu)) taken out behind the loop.  Where
 // that rounding is not small, d = (x - m) scale log2 e.
 //
 // The pass is bound by HBM (2 or 4 bytes per logit, read once).  The SM side
@@ -262,22 +262,21 @@ constexpr float ORDINARY = 0x1p24f;
 __device__ __forceinline__ float exact_distance(float x, float m, float scale) {
   return (x - m) * scale * LOG2E;        // not c: it is infinite at scales above 2.3e38, and 0 times it NaN
 }
-__device__ __forceinline__ float distance(float a, float b, float scale) {   // of a's reference below b's, >= FAR
-  if (a == b) return 0.f;
-  const float c = scale * LOG2E;
-  const float ma = __fmul_rn(a, c), mb = __fmul_rn(b, c);
-  const bool oa = fabsf(ma) < ORDINARY, ob = fabsf(mb) < ORDINARY;
-  // one rounding each, also where one reference is m c rounded and the other m itself
-  const float d = oa ? (ob ? __fsub_rn(ma, mb) : -fmaf(b, c, -ma)) : (ob ? fmaf(a, c, -mb) : exact_distance(a, b, scale));
-  return max_nan(d, FAR);
+__device__ __forceinline__ float reference_delta(float m, float c) {
+  const float mu = __fmul_rn(m, c);
+  return fabsf(mu) < ORDINARY ? fmaf(m, c, -mu) : 0.f;
 }
+// Two results whose reference is the maximum itself.
 __device__ __forceinline__ Stat merge_stat(const Stat& a, const Stat& b, float scale) {
+  const bool first = a.m >= b.m;
+  const float lo = first ? b.m : a.m, hi = first ? a.m : b.m;
+  const float ls = first ? b.s : a.s, lt = first ? b.t : a.t;
+  const float D = lo == hi ? 0.f : max_nan(exact_distance(lo, hi, scale), FAR);
+  const float f = ex2(D);
   Stat r;
   r.m = max_nan(a.m, b.m);
-  const float da = distance(a.m, r.m, scale), db = distance(b.m, r.m, scale);
-  const float fa = ex2(da), fb = ex2(db);
-  r.s = fa * a.s + fb * b.s;
-  r.t = fa * fmaf(a.s, da, a.t) + fb * fmaf(b.s, db, b.t);
+  r.s = fmaf(f, ls, first ? a.s : b.s);
+  r.t = fmaf(f, fmaf(ls, D, lt), first ? a.t : b.t);
   return r;
 }
 
@@ -494,7 +493,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
     // running softmax statistics
     if (!(bm <= st.m)) {                      // grows, or NaN
       if (st.s > 0.f) {
-        const float D = distance(st.m, bm, p.scale);
+        // from the old reference to the new one (bm > st.m here, or NaN)
+        const float D = max_nan(exact_distance(st.m, bm, p.scale) + (reference_delta(bm, c) - reference_delta(st.m, c)), FAR);
         const float f = ex2(D);
         st.t = f * fmaf(st.s, D, st.t);
         st.s *= f;
@@ -584,7 +584,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
   }
   if (TOPK && queued > 0) process();
 
-  // this CTA's statistics, fixed order
+  // this CTA's statistics, fixed order; from here on the reference is the maximum itself
+  const float delta = reference_delta(st.m, c), back = ex2(-delta);
+  st.t = back * fmaf(st.s, -delta, st.t);
+  st.s *= back;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     Stat b;
@@ -657,9 +660,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
   const Stat a = sm.stat;
   const float zmax = a.m * p.scale;
   const bool empty = zmax == -INFINITY;      // the mask leaves nothing
-  const float mu = __fmul_rn(a.m, c);
-  const float delta = fabsf(mu) < ORDINARY ? fmaf(a.m, c, -mu) : 0.f;   // d's reference against the maximum itself
-  const float ls = logf(a.s) - delta * LN2;
+  const float ls = logf(a.s);
   if (TOPK && lane < p.k) {
     const Key k = sm.top[lane];
     p.top_ids[row * p.k + lane] = key_index(k);
@@ -668,7 +669,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
   if (lane == 0) {
     if (p.lse) p.lse[row] = empty ? -INFINITY : zmax + ls;
     if (p.entropy) {
-      const float h = ls - (a.t / a.s - delta) * LN2;
+      const float h = ls - a.t / a.s * LN2;
       p.entropy[row] = empty || h < 0.f ? 0.f : h;
     }
     if (p.logprob) {
