@@ -154,7 +154,11 @@ __global__ void __cluster_dims__(RANKS, 1, 1) __launch_bounds__(THREADS, 2) rout
           const float a = bf16lo_to_f32(xw), b = bf16hi_to_f32(xw);
           x0[t] = static_cast<double>(a) * g0;
           x1[t] = static_cast<double>(b) * g1;
-          if (e0 == 0) ssq[t] += static_cast<double>(a * a) + static_cast<double>(b * b);
+          // squared in 64 bits: in 32 a square leaves the range from 1.8e19 and below 1e-19
+          if (e0 == 0) {
+            const double a64 = a, b64 = b;
+            ssq[t] = fma(a64, a64, fma(b64, b64, ssq[t]));
+          }
         }
 #pragma unroll
         for (int q = 0; q < GROUP; ++q) {

@@ -427,3 +427,28 @@ def test_shared_tiles_of_many_rows(M, d, I, E, k):
     check(layer, M, k, seed=M, ws=ws)
     check(layer, M, k, seed=M + 1, ws=ws, alias=True)
     assert ws.status()[0] == fnb.FN_OK and (ws.buf[:256] == 0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [3, 20, 64])
+def test_norms_of_the_whole_range(M):
+    """Activations whose squares leave the range of 32 bits.  Without eps the
+    layer does not depend on the scale of its rows, and a power of two changes
+    no rounding: the same experts, weights and outputs, bit by bit."""
+    layer = Layer(256, 128, 16, seed=11)
+    x = layer.x(M, 3)
+
+    def call(x):
+        out = T.moe_swiglu(x, layer.g, layer.router, layer.Wgu, layer.down, 4, 0.0)
+        torch.cuda.synchronize()
+        return out
+    y, ids, w = call(x)
+    ref_ids, ref_w = P.moe_route(x.cpu(), layer.g.cpu().numpy(), layer.router.cpu(), 4, 0.0)
+    assert np.array_equal(ids.cpu().numpy(), ref_ids)
+    assert np.allclose(w.double().cpu().numpy(), ref_w, rtol=2 * U, atol=1e-37)
+    for e in (83, 100, -66, -83):
+        a, b, c = call(x * 2.0 ** e)
+        assert torch.equal(b, ids) and torch.equal(c, w) and torch.equal(a, y), e
+    big = x.clone()
+    big[1] *= 2.0 ** 83
+    check(layer, M, 4, x=big, residual=False)
