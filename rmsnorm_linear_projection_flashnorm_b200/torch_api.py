@@ -40,22 +40,36 @@ def fold(W0: torch.Tensor, g: torch.Tensor, W1: Optional[torch.Tensor] = None, w
     return Wp, scales
 
 
+def _capturing(device) -> bool:
+    return torch.device(device).type == "cuda" and torch.cuda.is_current_stream_capturing()
+
+
 class Workspace:
-    """A zero-initialised device workspace that grows on demand."""
+    """A zero-initialised device workspace that grows on demand.
+
+    A captured graph keeps the address it was captured with, so buffers that a
+    larger one has replaced live as long as the workspace (each is at least
+    twice the one before, so all of them together are less than twice the last).
+    While the current stream is being captured the workspace does not grow: a
+    call that needs more gets a zeroed buffer of its own, which belongs to the
+    graph and is zeroed at every replay.  One call of the largest size before
+    the capture saves that, and puts its status word where `status` reads it."""
 
     def __init__(self, device="cuda"):
         self.device = device
         self.buf = torch.zeros(256, dtype=torch.uint8, device=device)
+        self._replaced = []
 
     def get(self, M: int, d: int, N: int, wt: int, swiglu: bool) -> torch.Tensor:
-        need = fn_workspace_size(M, d, N, wt, int(swiglu))
-        if self.buf.numel() < need:
-            self.buf = torch.zeros(need, dtype=torch.uint8, device=self.device)
-        return self.buf
+        return self.reserve(fn_workspace_size(M, d, N, wt, int(swiglu)))
 
     def reserve(self, need: int) -> torch.Tensor:
-        if self.buf.numel() < need:
-            self.buf = torch.zeros(need, dtype=torch.uint8, device=self.device)
+        have = self.buf.numel()
+        if have < need:
+            if _capturing(self.device):
+                return torch.zeros(need, dtype=torch.uint8, device=self.device)
+            self._replaced.append(self.buf)
+            self.buf = torch.zeros(max(need, 2 * have), dtype=torch.uint8, device=self.device)
         return self.buf
 
     def status(self, stream=None):
@@ -161,13 +175,11 @@ def norm_proj_adaln(x: torch.Tensor, Wp: torch.Tensor, N: int, eps: float, adaln
     wt = weight_type(Wp, scales)
     if ws is None:
         ws = Workspace(x.device)
-    need = fn_workspace_size_adaln(d, N, wt, int(swiglu))
-    if ws.buf.numel() < need:
-        ws.buf = torch.zeros(need, dtype=torch.uint8, device=ws.device)
+    buf = ws.reserve(fn_workspace_size_adaln(d, N, wt, int(swiglu)))
     if out is None:
         out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
     check(fn_norm_proj_adaln(x, M, d, Wp, scales, wt, N, int(swiglu), eps, adaln_scale, shift_bias, adaln_index,
-                             adaln_scale.shape[0], out, ws.buf, ws.buf.numel(), stream), "fn_norm_proj_adaln")
+                             adaln_scale.shape[0], out, buf, buf.numel(), stream), "fn_norm_proj_adaln")
     return out
 
 

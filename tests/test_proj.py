@@ -12,6 +12,7 @@ damped by the logistic factor).  The bias and residual add u each, and the
 store eps / 2 of the value.
 """
 import math
+import weakref
 
 import numpy as np
 import pytest
@@ -342,3 +343,66 @@ def test_small_tiles(M, K, N, fp32):
     """Few tiles and a short k range: fewer rows to a tile."""
     case(M, K, N, residual=True, bias=True, act="gelu", fp32=fp32, seed=M)
     aligned(M, K, N, fp32, True, "silu", seed=N)
+
+
+def test_workspace_keeps_the_buffers_it_replaced():
+    """A captured graph holds the address of the buffer it was captured with."""
+    ws = T.Workspace("cpu")
+    refs = [weakref.ref(ws.buf)]
+    for need in (1000, 1100, 5000, 100, 5000, 1 << 20):
+        buf = ws.reserve(need)
+        assert buf is ws.buf and buf.numel() >= need and not buf.any()
+        if refs[-1]() is not buf:
+            refs.append(weakref.ref(buf))
+        buf.fill_(1)
+        del buf
+        ws.buf.zero_()
+    bufs = [r() for r in refs]
+    assert len(bufs) == 5 and all(b is not None for b in bufs)
+    assert sum(b.numel() for b in bufs) < 2 * ws.buf.numel()
+
+
+def test_workspace_does_not_grow_in_a_capture(monkeypatch):
+    """Its zeroing would only be recorded, and the memory would be the graph's."""
+    ws = T.Workspace("cpu")
+    ws.reserve(1000)
+    own = ws.buf
+    monkeypatch.setattr(T, "_capturing", lambda device: True, raising=False)
+    assert ws.reserve(900) is own
+    a, b = ws.reserve(2000), ws.reserve(2000)
+    assert a.numel() == b.numel() == 2000 and not a.any() and a is not b and ws.buf is own
+
+
+@pytest.mark.gpu
+def test_workspace_grows_behind_a_captured_graph():
+    x, w = padded(7, 4096, 4096, 1), padded(4096, 1000, 1000, 2, 1 / 64)
+    xl, wl = padded(100, 8192, 8192, 3), padded(8192, 512, 512, 4, 1 / 90)      # needs 19 MB where the first needs 2
+    ws = T.Workspace("cuda")
+    ref, large = T.proj(x, w, ws=ws), T.proj(xl, wl)
+    old = ws.buf.numel()
+    out, first = torch.empty_like(ref), torch.empty_like(ref)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        T.proj(x, w, ws=ws, out=out)
+    assert torch.equal(T.proj(xl, wl, ws=ws), large) and ws.buf.numel() > old
+    others = [torch.full((old,), 0xA5, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    for _ in range(3):
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref) and all((o == 0xA5).all() for o in others)
+        assert torch.equal(T.proj(xl, wl, ws=ws), large)
+    # captured before the workspace has its size, and used before the first replay
+    ws = T.Workspace("cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        T.proj(x, w, ws=ws, out=first)
+        T.proj(x, w, ws=ws, out=out)
+    assert torch.equal(T.proj(x, w, ws=ws), ref) and torch.equal(T.proj(xl, wl, ws=ws), large)
+    for _ in range(3):
+        first.zero_()
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(first, ref) and torch.equal(out, ref)
+    assert torch.equal(T.proj(x, w, ws=ws), ref) and ws.status()[0] == fnb.FN_OK
