@@ -412,8 +412,9 @@ typedef enum {
  *            first use; the calls leave what they need zero at zero
  * M == 0 is a no-op.  Few rows (up to 128, by N and K) run a split-K kernel that
  * streams the weight over all SMs, others a tensor-core tile kernel on pairs of
- * SMs; where SMs share a tile's k range and M > 16 a second kernel adds their
- * sums.
+ * SMs.  A second kernel adds the sums of SMs that share a tile's k range: behind
+ * the stream kernel above 16 rows, behind the tile kernel at any number of rows
+ * (at 16 and fewer it runs more than 37760 columns that are no multiple of 64).
  * Deterministic.  A weight of more than 2^24 blocks of 64 x 128 is refused
  * (FN_ERR_UNSUPPORTED_SHAPE).  After FN_ERR_TIMEOUT in the status word the
  * workspace must be zeroed before its next use.

@@ -406,3 +406,34 @@ def test_workspace_grows_behind_a_captured_graph():
         torch.cuda.synchronize()
         assert torch.equal(first, ref) and torch.equal(out, ref)
     assert torch.equal(T.proj(x, w, ws=ws), ref) and ws.status()[0] == fnb.FN_OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [1, 5, 16])
+def test_few_rows_whose_last_tiles_are_shared(M):
+    """Few rows on the tile kernel with a k range long enough that the pairs
+    share the last tile: the one case of a second kernel at so few rows."""
+    K, N = 14336, 37900
+    assert fnb.fn_workspace_size_proj(M, K, N) > 256
+    g = torch.Generator(device="cuda").manual_seed(M)
+    x = torch.randn(M, K, generator=g, device="cuda").bfloat16()
+    w = torch.full((K, up8(N)), math.nan, dtype=torch.bfloat16, device="cuda")[:, :N]
+    w.copy_(torch.randn(K, N, generator=g, device="cuda", dtype=torch.bfloat16) * K ** -0.5)
+    r = torch.randn(M, N, generator=g, device="cuda")
+    ws = T.Workspace("cuda")
+    T.proj(x, w, residual=r, ws=ws)
+    n = fnb.fn_kernel_launches()
+    y = T.proj(x, w, residual=r, ws=ws)
+    assert fnb.fn_kernel_launches() == n + 2
+    n += 2
+    for m, launches in ((1, 1), (16, 1), (17, 2)):             # the stream kernel
+        T.proj(x[:1, :4096].expand(m, 4096).contiguous(), w[:4096, :4096], ws=ws)
+        assert fnb.fn_kernel_launches() == n + launches
+        n += launches
+    torch.cuda.synchronize()
+    for a in range(0, N, 4096):
+        wd = w[:, a:a + 4096].double()
+        ref = x.double() @ wd + r[:, a:a + 4096].double()
+        tol = (8 + math.sqrt(K)) * 2 * U * (x.double().abs() @ wd.abs()) + 2 * U * ref.abs()
+        assert ((y[:, a:a + 4096].double() - ref).abs() <= tol).all()
+    assert ws.status()[0] == fnb.FN_OK and (ws.buf[:256] == 0).all()
