@@ -444,7 +444,7 @@ typedef enum {
  *   l[m, e]  = h[m, :] . router[e, :]          (fp64: a choice between close values)
  *   s        = softmax_e(l) or sigmoid(l)
  *   ids[m]   = the top_k experts by l, or by s + select_bias where that is
- *              given; ties to the lower index, NaN below every number
+ *              given; ties to the lower index, a NaN counts as -infinity
  *   w[m, j]  = s[ids] (renorm != 0: divided by their sum) * route_scale
  *   y[m]     = residual[m] + sum_j w[m, j] (silu(h G_e) * (h U_e)) D_e
  *   x        bf16 [M, d] raw activations
@@ -496,6 +496,9 @@ size_t fn_workspace_size_moe(int64_t M, int64_t d, int64_t I, int64_t E, int top
  * Sums are fp32; a masked logit (-inf) adds nothing.  A row whose mask leaves
  * nothing (its largest z is -inf) has lse = -inf, log probabilities -inf and
  * entropy 0.  A row that holds NaN or +inf has NaN results (top_ids as above).
+ * Finite logits and fills of any size are right at any scale: distances to the
+ * row's maximum are taken before they are rounded, so log probabilities and
+ * entropies do not lose what lse, rounded to fp32, has lost.
  *   logits   [M, V] of `type` (bf16, fp16 or fp32), rows ld >= V elements
  *            apart; only element alignment is needed (rows at odd addresses
  *            run at the same speed)
@@ -527,6 +530,10 @@ fn_status fn_token_logprobs(const void* logits, fn_dtype type, int64_t M, int64_
  *   dlogits        [M, V] of `type`, rows ldd >= V elements apart, one round at
  *                  the store; may be the logits themselves (same address and
  *                  row stride), may not overlap any input otherwise
+ * p_v carries the rounding of lse, a relative error of |lse| 2^-24 (1e-6 at lse =
+ * 16, 1e-3 at 16384); in a row with |lse| above 10^6, such as one filled
+ * throughout with a mask's -1e9, it means nothing: pass such rows with
+ * targets[m] < 0 and grad_entropy 0, or filled with -inf.
  * The top alternatives carry no gradient.  M == 0 is a no-op.
  */
 fn_status fn_token_logprobs_backward(const void* logits, fn_dtype type, int64_t M, int64_t V, int64_t ld,

@@ -11,8 +11,9 @@
 // rounding of mu (known exactly, fma(m, c, -mu)) taken out behind the loop.  Where
 // that rounding is not small, d = (x - m) scale log2 e.
 //
-// The pass is bound by HBM (2 or 4 bytes per logit, read once).  The SM side
-// stays below it: per pair of 16-bit logits two ex2 and about 8 issue slots.
+// The pass is bound by HBM (2 or 4 bytes per logit, read once) without
+// alternatives, by issue slots with them: a pair of 16-bit logits takes 15
+// instructions, two of them ex2, and 20 with 8 alternatives.
 // Every thread copies the vectors that it will read itself to shared memory
 // two tiles ahead (cp.async), so loads are in flight while it computes and the
 // main loop has no barrier.
@@ -21,8 +22,8 @@
 // bit pattern above the complement of its index, so keys are unique, ties go
 // to the lower index and the order of arrival does not matter.  Each warp
 // keeps its 32 largest keys, sorted, one per lane.  A threshold key, never
-// above the true k-th largest, filters the stream: one comparison per 32
-// logits of a thread.  It is the largest of
+// above the true k-th largest, filters the stream: one comparison per tile of a
+// thread (32 logits, 16 in fp32).  It is the largest of
 //   the k-th largest of all threads' maxima, taken after 1, 4, 16, ... tiles
 //     (about k logits of a tile lie above it, however many there were before);
 //   the warps' own k-th keys;
@@ -42,9 +43,12 @@
 // (m, s, t) and top lists meet in distributed shared memory in rank order:
 // one launch, no workspace, no atomics on results, bit-identical repeats.
 //
-// Measured: 4096 x 131072 bf16 with 8 alternatives 205 us (5.2 TB/s; issue slots
-// of the threshold tests), without 160 us (6.7 TB/s); one row with 20
-// alternatives 10 us.
+// Measured at 1965 MHz (and in a long run under the power cap, at 1.6 to 1.7
+// GHz): 4096 x 131072 bf16 with 8 alternatives 207 us (239), 5.2 TB/s; without
+// 161 us (193), 6.7 TB/s; 2048 x 131072 fp32 with 8 alternatives 181 us (191);
+// one row with 20 alternatives 10 us.  A thread that has met nothing but a mask's
+// fill of -2^24 / c and below takes the exact differences: with such a fill in the
+// first three quarters of each row 2048 x 131072 bf16 takes 116 us instead of 94.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -723,8 +727,14 @@ cudaError_t launch_fwd(const LogprobArgs& a) {
 // p_v = e^{z_v - lse}: one read and one write of the row, bound by HBM.  A
 // thread reads and writes the same elements, so the gradient may overwrite
 // the logits.
-// 8 vectors a thread and blocks of 128: 2048 x 131072 bf16 in 175 us (6.1 TB/s);
-// 4, 12 and 16 vectors took 187, 186 and 200 us with blocks of 256.
+// 8 vectors a thread and blocks of 128: 2048 x 131072 bf16 in 176 us (6.1 TB/s)
+// at 1965 MHz, 197 in a long run under the power cap; 4, 12 and 16 vectors took
+// 187, 186 and 200 us with blocks of 256.
+//
+// lse comes rounded to fp32, so log p is off by half a step of lse: p by a
+// relative |lse| 2^-24.  Where |lse| is in the millions p has no digit left (a row
+// filled throughout with -1e9 has p = 1 for each logit); only the forward pass,
+// which has the sum itself, is exact there.
 constexpr int THREADS = 128;
 constexpr int BWD_VECS = 8;
 

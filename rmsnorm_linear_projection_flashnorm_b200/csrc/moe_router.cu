@@ -3,12 +3,13 @@
 //
 //   l_e = r sum_k x_k g_k R[e, k],  r = 1 / sqrt(mean x^2 + eps)
 //   score softmax or sigmoid of l; top k by l, or by score + bias; ties to the
-//   lower index, NaN below every number
+//   lower index, NaN as minus infinity
 //
 // Which experts are chosen is a comparison of values that may lie close, so
-// the logits are fp64 sums of exact fp32 products x R (16 significant bits);
-// the result then does not depend on the order of the sum in any case a 32-bit
-// reference could tell apart.
+// the logits are fp64 sums of the products x g R (8 + 24 + 8 significant bits,
+// exact in fp64), and the squares of the norm are fp64 too; the result then does
+// not depend on the order of the sum in any case a 32-bit reference could tell
+// apart.
 //
 // Bound by latency: 2 E d bytes of router weight from L2 or HBM (0.5 MB at 128
 // experts x 2048) and M E d multiply-adds.  One cluster of 8 CTAs takes 1, 2 or

@@ -24,9 +24,10 @@
 // finishes the tile (no CTA waits for another, no floating-point atomics,
 // bit-identical repeats).
 //
-// Measured (device time a call): 4096 x 14336 x 4096 with bias and residual
-// 345..367 us (1310..1396 TFLOP/s, under the power cap), 1024 x 8192 x 4096 57 us,
-// 300 x 14336 x 4096 42 us, 498 x 416 x 277 8 us.
+// Measured (device time a call) at 1965 MHz, and in a long run under the power
+// cap: 4096 x 14336 x 4096 with bias and residual 360 us (1335 TFLOP/s), 419 at
+// 1305 MHz; 1024 x 8192 x 4096 53 us, 63 at 1537 MHz; 300 x 14336 x 4096 43 us, 50
+// at 1650 MHz; 498 x 416 x 277 6 us.
 //
 // Layout per CTA: 10 warps.
 //   warp 0      TMA producer (own weight columns, own rows)

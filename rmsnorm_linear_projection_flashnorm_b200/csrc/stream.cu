@@ -23,10 +23,11 @@
 // masks.  Their one rounding to bf16, behind the routing weight, makes them the
 // next MMA's operand.
 //
-// Measured (device time a call): 4096 x 4096, one row, 10.6 us, of which the
+// Measured (device time a call): 4096 x 4096, one row, 10.8 us, of which the
 // stream takes 4.7 (7.1 TB/s), the first load 0.8, the exchange 3 and the
-// kernel boundary 1.2; 8 experts of 2048 x 1024 and one row 35..37 us with the
-// router's 5.9; 64 rows and 8 experts of 4096 x 14336 478 us (5.9 TB/s).
+// kernel boundary 1.2; 8 experts of 2048 x 1024 and one row 35 us with the
+// router's 5.9; 64 rows and 8 experts of 4096 x 14336 460 us (6.1 TB/s) at 1965
+// MHz, 487 in a long run under the power cap at 1500 MHz.
 //
 // A tile whose k range falls to one CTA is finished by it.  The CTAs that
 // share a tile write fp32 partials to the workspace.  With few rows, and for

@@ -393,7 +393,8 @@ def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None,
                    out: Optional[TokenLogprobs] = None, stream=None) -> TokenLogprobs:
     """Log probabilities of the int32 `targets` [M] under softmax(scale * logits),
     the rows' entropies and log sums, and the top_k alternatives (see
-    fn_token_logprobs).  logits: bf16, fp16 or fp32 [M, V], rows contiguous."""
+    fn_token_logprobs).  logits: bf16, fp16 or fp32 [M, V], rows contiguous.
+    Not recorded by autograd: token_logprobs_backward gives the gradient."""
     ld = _rows(logits, "logits", _DTYPE)
     M, V = logits.shape
     dev = logits.device
