@@ -531,9 +531,9 @@ fn_status fn_token_logprobs(const void* logits, fn_dtype type, int64_t M, int64_
  *                  the store; may be the logits themselves (same address and
  *                  row stride), may not overlap any input otherwise
  * p_v carries the rounding of lse, a relative error of |lse| 2^-24 (1e-6 at lse =
- * 16, 1e-3 at 16384); in a row with |lse| above 10^6, such as one filled
- * throughout with a mask's -1e9, it means nothing: pass such rows with
- * targets[m] < 0 and grad_entropy 0, or filled with -inf.
+ * 16).  In rows with |lse| of 1024 and more, such as one filled throughout with
+ * a mask's -1e9, the sum is taken again from the logits instead, by one block per
+ * row.
  * The top alternatives carry no gradient.  M == 0 is a no-op.
  */
 fn_status fn_token_logprobs_backward(const void* logits, fn_dtype type, int64_t M, int64_t V, int64_t ld,

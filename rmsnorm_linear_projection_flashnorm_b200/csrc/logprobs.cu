@@ -731,12 +731,16 @@ cudaError_t launch_fwd(const LogprobArgs& a) {
 // at 1965 MHz, 197 in a long run under the power cap; 4, 12 and 16 vectors took
 // 187, 186 and 200 us with blocks of 256.
 //
-// lse comes rounded to fp32, so log p is off by half a step of lse: p by a
-// relative |lse| 2^-24.  Where |lse| is in the millions p has no digit left (a row
-// filled throughout with -1e9 has p = 1 for each logit); only the forward pass,
-// which has the sum itself, is exact there.
+// lse comes rounded to fp32, so log p is off by half a step of lse, and p by a
+// relative |lse| 2^-24.  Where |lse| is in the millions no digit of p is left (a
+// row filled throughout with -1e9 would get p = 1 for each logit, the most that a
+// mask can do wrong).  So from |lse| = FAR_LSE on the row's first block takes the
+// maximum and the sum again and does the whole row alone, since the gradient may
+// overwrite the logits: such a row costs a second reading, the others a comparison.
 constexpr int THREADS = 128;
 constexpr int BWD_VECS = 8;
+
+constexpr float FAR_LSE = 1024.f;            // p off by 2^-14 at most below it
 
 struct BwdParams {
   const void* logits;
@@ -754,6 +758,57 @@ __device__ __forceinline__ float grad_of(float x, float scale, float lse, float 
   const float pv = FAST ? ex2(lp * LOG2E) : expf(lp);
   // masked: p = 0 and log p = -inf, no gradient
   return pv == 0.f ? 0.f : -scale * pv * fmaf(gh, lp + H, gl);
+}
+
+// A whole row by one block, from its own maximum and sum.
+template <typename T>
+__device__ __noinline__ void far_row(const T* x, T* dx, int V, int t, float scale, float gl, float gh, float H) {
+  using E = Elem<T>;
+  __shared__ float ms[THREADS / 32][2];
+  // running maximum and sum of e^(z - max z); masked logits add nothing
+  float m = -INFINITY, s = 0.f;
+  auto merge = [&](float om, float os) {
+    const float hi = fmaxf(m, om);
+    if (hi == -INFINITY) return;
+    s = s * expf((m - hi) * scale) + os * expf((om - hi) * scale);
+    m = hi;
+  };
+  constexpr int BATCH = 8;                    // loads in flight
+  for (int64_t i0 = threadIdx.x; i0 < V; i0 += THREADS * BATCH) {
+    float v[BATCH];
+#pragma unroll
+    for (int j = 0; j < BATCH; ++j) v[j] = i0 + j * THREADS < V ? E::load(x + i0 + j * THREADS) : -INFINITY;
+#pragma unroll
+    for (int j = 0; j < BATCH; ++j) merge(v[j], 1.f);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float om = __shfl_down_sync(0xffffffffu, m, o), os = __shfl_down_sync(0xffffffffu, s, o);
+    merge(om, os);
+  }
+  if ((threadIdx.x & 31) == 0) {
+    ms[threadIdx.x >> 5][0] = m;
+    ms[threadIdx.x >> 5][1] = s;
+  }
+  __syncthreads();                            // also: the row has been read before it is written
+  m = ms[0][0];
+  s = ms[0][1];
+  for (int w = 1; w < THREADS / 32; ++w) merge(ms[w][0], ms[w][1]);
+  const float ls = logf(s), hot = gl * scale;
+  for (int64_t i0 = threadIdx.x; i0 < V; i0 += THREADS * BATCH) {
+    float v[BATCH];
+#pragma unroll
+    for (int j = 0; j < BATCH; ++j) v[j] = i0 + j * THREADS < V ? E::load(x + i0 + j * THREADS) : -INFINITY;
+#pragma unroll
+    for (int j = 0; j < BATCH; ++j) {
+      const int64_t i = i0 + j * THREADS;
+      const float lp = (v[j] - m) * scale - ls;
+      const float pv = expf(lp);
+      float g = pv == 0.f ? 0.f : -scale * pv * fmaf(gh, lp + H, gl);
+      if (i == t) g += hot;
+      if (i < V) dx[i] = E::from(g);
+    }
+  }
 }
 
 template <typename T>
@@ -774,6 +829,10 @@ __global__ void __launch_bounds__(THREADS) logprobs_bwd_kernel(const BwdParams p
   const float lse = __ldg(p.lse + row);
   const float hot = gl * p.scale;
   const bool empty = lse == -INFINITY;
+  if (!empty && fabsf(lse) >= FAR_LSE) {
+    if (chunk == 0) far_row<T>(x, dx, p.V, t, p.scale, gl, gh, H);
+    return;
+  }
   const int lo = static_cast<int>(static_cast<int64_t>(p.V) * chunk / p.chunks);
   const int hi = static_cast<int>(static_cast<int64_t>(p.V) * (chunk + 1) / p.chunks);
   auto one = [&](int i) {

@@ -631,3 +631,100 @@ def test_forward_scales_at_the_ends_of_the_range(dtype, scale):
     x[4] = -math.inf
     x[5, ::2] = x[5, 0]
     check_fwd(x, targets_(6, V, 3), 8, scale)
+
+
+def check_far_bwd(x, t, gl, gh, scale, out=None):
+    """The gradient where lse is too large to tell p from: the row's own sum is
+    used.  z - max is rounded twice (2 u of it), the sum adds V / 128 + 64 terms
+    and expf's 4 u, its logarithm and the difference u each; p then carries
+    4 u + the error of log p.  The entropy is the forward pass's (its bound)."""
+    r = T.token_logprobs(x, t, scale=scale)
+    g = T.token_logprobs_backward(x, t, r.lse, r.entropy, gl, gh, scale=scale, out=out)
+    torch.cuda.synchronize()
+    assert (r.lse.abs() >= 1024).all()
+    return g
+
+
+def far_reference(x, t, gl, gh, scale):
+    """(gradient, its tolerance), in 64 bits."""
+    z = x.double() * float(np.float32(scale))
+    V = x.shape[1]
+    q = torch.log_softmax(z, 1)
+    p = torch.exp(q)
+    safe = torch.where(p > 0, q, 0.0)
+    H = -(p * safe).sum(1, keepdim=True)
+    hot = torch.zeros_like(z).scatter_(1, t.clamp(min=0).long()[:, None], 1.0)
+    a = torch.where(t < 0, 0.0, gl).double()[:, None]
+    b = gh.double()[:, None]
+    ref = scale * (a * (hot - p) - b * p * (safe + H))
+    ls = (4 * (math.log(V) + 1) + V / 128 + 69) * U
+    eh = 2 * ls * (1 + math.log(V)) + 4 * U * (H + 1)
+    elp = ls + 4 * U * (safe.abs() + 1)
+    rel = elp + 4 * U
+    tol = scale * p * (a.abs() * (rel + 4 * U) + b.abs() * ((safe.abs() + H) * (rel + 4 * U) + elp + eh))
+    tol = tol + scale * a.abs() * 4 * U * hot + torch.finfo(x.dtype).eps / 2 * ref.abs() * (1 + 2 ** -10)
+    return ref, tol + (2.0 ** -25 if x.dtype == torch.float16 else 0.0) + scale * 2.0 ** -126
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,fill", [("bf16", -1e9), ("bf16", -3e38), ("fp16", -65504.0), ("fp16", 60000.0),
+                                        ("fp32", -1e4), ("fp32", -1e9), ("fp32", -1e20), ("fp32", -3.4028234e38),
+                                        ("fp32", 1e12)])
+@pytest.mark.parametrize("V", [1, 2, 300, 9001, 70001])
+def test_backward_of_rows_far_from_zero(dtype, fill, V):
+    """Rows filled throughout (uniform), filled but for one or for ten above,
+    and ordinary rows among them, out of place, in place and strided."""
+    M = 7
+    x = torch.full((M, V + 3), fill, dtype=DT[dtype], device="cuda")[:, :V]
+    gen = torch.Generator(device="cuda").manual_seed(V)
+    if V > 100:
+        up = torch.nextafter(torch.tensor(fill).to(DT[dtype]).float(), torch.tensor(math.inf)).item() if dtype == "fp32" \
+            else float(torch.tensor(fill).to(DT[dtype])) * (1 + math.copysign(2 ** -6, fill))
+        x[1, 5] = up
+        x[2, 20:30] = up
+        x[3, ::2] = -math.inf
+    t = torch.tensor([0, min(5, V - 1), V - 1, 0, -1, V // 2, 0], dtype=torch.int32, device="cuda")
+    gl, gh = (torch.randn(M, generator=gen, device="cuda") for _ in range(2))
+    ref, tol = far_reference(x, t, gl, gh, 1.0)
+    buf = torch.full((M + 2, V + 9), 5.0, dtype=DT[dtype], device="cuda")
+    for out in (None, buf[1:M + 1, 1:V + 1], x):
+        g = check_far_bwd(x, t, gl, gh, 1.0, out=out)
+        assert ((g.double() - ref).abs() <= tol).all()
+    buf[1:M + 1, 1:V + 1] = 5.0
+    assert (buf == 5).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("scale", [1e4, 1e10])
+def test_backward_at_large_scales(dtype, scale):
+    V = 30011
+    x = logits_(5, V, V, dtype, seed=9)
+    x[2, 100:104] = x[2].max()                          # four share the probability
+    t = torch.tensor([3, -1, 101, 9, V - 1], dtype=torch.int32, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    gl, gh = (torch.randn(5, generator=gen, device="cuda") / scale for _ in range(2))
+    ref, tol = far_reference(x, t, gl, gh, scale)
+    g = check_far_bwd(x, t, gl, gh, scale)
+    assert ((g.double() - ref).abs() <= tol).all()
+
+
+@pytest.mark.gpu
+def test_backward_of_far_rows_leaves_the_others():
+    """Rows on either side of the change in one call: the ordinary ones as
+    without them; just below and above it both forms agree with the formula."""
+    V = 20011
+    x = logits_(6, V, V, "fp32", seed=5)
+    t = torch.arange(6, device="cuda", dtype=torch.int32)
+    gl = torch.ones(6, device="cuda")
+    r = T.token_logprobs(x, t)
+    plain = T.token_logprobs_backward(x, t, r.lse, r.entropy, gl, gl)
+    y = x.clone()
+    y[1] += 1e5
+    y[4] = -1e9
+    r = T.token_logprobs(y, t)
+    mixed = T.token_logprobs_backward(y, t, r.lse, r.entropy, gl, gl)
+    torch.cuda.synchronize()
+    assert all(torch.equal(plain[i], mixed[i]) for i in (0, 2, 3, 5))
+    check_bwd(x - 1000, t.cpu().numpy(), gl.cpu().numpy(), gl.cpu().numpy(), 1.0)
+    check_bwd(x - 1100, t.cpu().numpy(), gl.cpu().numpy(), gl.cpu().numpy(), 1.0)
