@@ -727,8 +727,8 @@ cudaError_t launch_fwd(const LogprobArgs& a) {
 // p_v = e^{z_v - lse}: one read and one write of the row, bound by HBM.  A
 // thread reads and writes the same elements, so the gradient may overwrite
 // the logits.
-// 8 vectors a thread and blocks of 128: 2048 x 131072 bf16 in 176 us (6.1 TB/s)
-// at 1965 MHz, 197 in a long run under the power cap; 4, 12 and 16 vectors took
+// 8 vectors a thread and blocks of 128: 2048 x 131072 bf16 in 172 us (6.2 TB/s)
+// at 1965 MHz, 183 in a long run under the power cap; 4, 12 and 16 vectors took
 // 187, 186 and 200 us with blocks of 256.
 //
 // lse comes rounded to fp32, so log p is off by half a step of lse, and p by a
@@ -736,7 +736,8 @@ cudaError_t launch_fwd(const LogprobArgs& a) {
 // row filled throughout with -1e9 would get p = 1 for each logit, the most that a
 // mask can do wrong).  So from |lse| = FAR_LSE on the row's first block takes the
 // maximum and the sum again and does the whole row alone, since the gradient may
-// overwrite the logits: such a row costs a second reading, the others a comparison.
+// overwrite the logits: 0.27 ms where one row of 2048 is such a row, 0.92 where all
+// are.
 constexpr int THREADS = 128;
 constexpr int BWD_VECS = 8;
 
@@ -829,10 +830,7 @@ __global__ void __launch_bounds__(THREADS) logprobs_bwd_kernel(const BwdParams p
   const float lse = __ldg(p.lse + row);
   const float hot = gl * p.scale;
   const bool empty = lse == -INFINITY;
-  if (!empty && fabsf(lse) >= FAR_LSE) {
-    if (chunk == 0) far_row<T>(x, dx, p.V, t, p.scale, gl, gh, H);
-    return;
-  }
+  const bool far = !empty && fabsf(lse) >= FAR_LSE;      // then nothing is stored before far_row
   const int lo = static_cast<int>(static_cast<int64_t>(p.V) * chunk / p.chunks);
   const int hi = static_cast<int>(static_cast<int64_t>(p.V) * (chunk + 1) / p.chunks);
   auto one = [&](int i) {
@@ -855,6 +853,10 @@ __global__ void __launch_bounds__(THREADS) logprobs_bwd_kernel(const BwdParams p
   };
   const uintptr_t ax = reinterpret_cast<uintptr_t>(x + lo), ad = reinterpret_cast<uintptr_t>(dx + lo);
   if (((ax ^ ad) & 15u) != 0) {
+    if (far) {
+      if (chunk == 0) far_row<T>(x, dx, p.V, t, p.scale, gl, gh, H);
+      return;
+    }
     // The rows lie differently to 16-byte boundaries: whole vectors of the
     // gradient, each from the two vectors of logits that it straddles (the
     // second comes from L1), as far as both lie within this block's logits.
@@ -902,16 +904,22 @@ __global__ void __launch_bounds__(THREADS) logprobs_bwd_kernel(const BwdParams p
   const int b = min(lo + (mis ? N - mis : 0), hi);
   const int nv = (hi - b) / N;
   const int e0 = b + nv * N;
-  if (lo + static_cast<int>(threadIdx.x) < b) one(lo + static_cast<int>(threadIdx.x));
-  if (e0 + static_cast<int>(threadIdx.x) < hi) one(e0 + static_cast<int>(threadIdx.x));
   const uint4* xv = reinterpret_cast<const uint4*>(x + b);
   uint4* dv = reinterpret_cast<uint4*>(dx + b);
-  for (int base = 0; base < nv; base += THREADS * BWD_VECS) {
+  for (int base = 0; base == 0 || base < nv; base += THREADS * BWD_VECS) {
     uint4 q[BWD_VECS];
 #pragma unroll
     for (int j = 0; j < BWD_VECS; ++j) {
       const int i = base + j * THREADS + static_cast<int>(threadIdx.x);
       if (i < nv) q[j] = __ldcs(xv + i);
+    }
+    if (base == 0) {                           // behind the loads, which then do not wait for lse
+      if (far) {
+        if (chunk == 0) far_row<T>(x, dx, p.V, t, p.scale, gl, gh, H);
+        return;
+      }
+      if (lo + static_cast<int>(threadIdx.x) < b) one(lo + static_cast<int>(threadIdx.x));
+      if (e0 + static_cast<int>(threadIdx.x) < hi) one(e0 + static_cast<int>(threadIdx.x));
     }
 #pragma unroll
     for (int j = 0; j < BWD_VECS; ++j) {
