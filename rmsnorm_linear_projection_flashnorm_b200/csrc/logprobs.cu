@@ -263,19 +263,28 @@ struct Stat {
 // delta = m c - mu, lies within a factor of 2^(1/2) of 1.  (Half a step of mu
 // passes 127 at 2^31; from there 2^delta may be infinite or 0.)
 constexpr float ORDINARY = 0x1p24f;
-__device__ __forceinline__ float exact_distance(float x, float m, float scale) {
-  return (x - m) * scale * LOG2E;        // not c: it is infinite at scales above 2.3e38, and 0 times it NaN
+// (x - m) scale, as (x h - m h) (scale / h) with h = 1/2 at scales below 1, where
+// halves are exact as far as they count: the difference of two finite logits may
+// be infinite when its product is not.
+struct Scale {
+  float half, rest;   // h, scale / h
+};
+__device__ __forceinline__ float difference(float x, float m, const Scale& k) {
+  return fmaf(x, k.half, -(m * k.half)) * k.rest;
+}
+__device__ __forceinline__ float exact_distance(float x, float m, const Scale& k) {
+  return difference(x, m, k) * LOG2E;    // not by c: it is infinite at scales above 2.3e38, and 0 times it NaN
 }
 __device__ __forceinline__ float reference_delta(float m, float c) {
   const float mu = __fmul_rn(m, c);
   return fabsf(mu) < ORDINARY ? fmaf(m, c, -mu) : 0.f;
 }
 // Two results whose reference is the maximum itself.
-__device__ __forceinline__ Stat merge_stat(const Stat& a, const Stat& b, float scale) {
+__device__ __forceinline__ Stat merge_stat(const Stat& a, const Stat& b, const Scale& k) {
   const bool first = a.m >= b.m;
   const float lo = first ? b.m : a.m, hi = first ? a.m : b.m;
   const float ls = first ? b.s : a.s, lt = first ? b.t : a.t;
-  const float D = lo == hi ? 0.f : max_nan(exact_distance(lo, hi, scale), FAR);
+  const float D = lo == hi ? 0.f : max_nan(exact_distance(lo, hi, k), FAR);
   const float f = ex2(D);
   Stat r;
   r.m = max_nan(a.m, b.m);
@@ -325,6 +334,7 @@ struct Params {
   int V, C, k;
   const int* targets;
   float scale;
+  Scale by;
   float *logprob, *entropy, *lse, *top_logprobs;
   int* top_ids;
 };
@@ -498,7 +508,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
     if (!(bm <= st.m)) {                      // grows, or NaN
       if (st.s > 0.f) {
         // from the old reference to the new one (bm > st.m here, or NaN)
-        const float D = max_nan(exact_distance(st.m, bm, p.scale) + (reference_delta(bm, c) - reference_delta(st.m, c)), FAR);
+        const float D = max_nan(exact_distance(st.m, bm, p.by) + (reference_delta(bm, c) - reference_delta(st.m, c)), FAR);
         const float f = ex2(D);
         st.t = f * fmaf(st.s, D, st.t);
         st.s *= f;
@@ -542,7 +552,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
 #pragma unroll
         for (int e = 0; e < N; ++e) {
           const float d =
-              max_nan(fabsf(mu) < ORDINARY ? fmaf(f[e], c, -mu) : exact_distance(f[e], st.m, p.scale), FAR);
+              max_nan(fabsf(mu) < ORDINARY ? fmaf(f[e], c, -mu) : exact_distance(f[e], st.m, p.by), FAR);
           const float w = ex2(d);
           st.s += w;
           st.t = fmaf(d, w, st.t);
@@ -598,7 +608,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
     b.m = __shfl_down_sync(0xffffffffu, st.m, o);
     b.s = __shfl_down_sync(0xffffffffu, st.s, o);
     b.t = __shfl_down_sync(0xffffffffu, st.t, o);
-    st = merge_stat(st, b, p.scale);
+    st = merge_stat(st, b, p.by);
   }
   if (lane == 0) sm.wstat[warp] = st;
   __syncthreads();                            // every thread is done with its vectors
@@ -620,7 +630,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
   }
   if (threadIdx.x == 0) {
     Stat a = sm.wstat[0];
-    for (int w = 1; w < WARPS; ++w) a = merge_stat(a, sm.wstat[w], p.scale);
+    for (int w = 1; w < WARPS; ++w) a = merge_stat(a, sm.wstat[w], p.by);
     sm.stat = a;
   }
   if (THREADS == MAX_THREADS && p.C > 1) {    // warp w serves rank w
@@ -639,7 +649,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
       if constexpr (TOPK) select_top(sm, p.C * p.k, p.k);
       if (threadIdx.x == 0) {
         Stat a = sm.stat;
-        for (int r = 1; r < p.C; ++r) a = merge_stat(a, sm.wstat[r], p.scale);
+        for (int r = 1; r < p.C; ++r) a = merge_stat(a, sm.wstat[r], p.by);
         sm.stat = a;
       }
     }
@@ -668,7 +678,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
   if (TOPK && lane < p.k) {
     const Key k = sm.top[lane];
     p.top_ids[row * p.k + lane] = key_index(k);
-    p.top_logprobs[row * p.k + lane] = empty ? -INFINITY : (key_value(k) - a.m) * p.scale - ls;
+    p.top_logprobs[row * p.k + lane] = empty ? -INFINITY : difference(key_value(k), a.m, p.by) - ls;
   }
   if (lane == 0) {
     if (p.lse) p.lse[row] = empty ? -INFINITY : zmax + ls;
@@ -680,7 +690,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
       const int t = p.targets[row];
       float v = 0.f;                         // no token
       if (t >= p.V) v = NAN;                 // nothing is read out of range
-      else if (t >= 0) v = empty ? -INFINITY : (E::load(x + t) - a.m) * p.scale - ls;
+      else if (t >= 0) v = empty ? -INFINITY : difference(E::load(x + t), a.m, p.by) - ls;
       p.logprob[row] = v;
     }
   }
@@ -695,6 +705,8 @@ cudaError_t launch_fwd(const LogprobArgs& a) {
   p.k = a.top_k;
   p.targets = a.targets;
   p.scale = a.scale;
+  p.by.half = a.scale < 1.f ? 0.5f : 1.f;
+  p.by.rest = a.scale / p.by.half;
   p.logprob = a.logprob;
   p.entropy = a.entropy;
   p.lse = a.lse;

@@ -728,3 +728,16 @@ def test_backward_of_far_rows_leaves_the_others():
     assert all(torch.equal(plain[i], mixed[i]) for i in (0, 2, 3, 5))
     check_bwd(x - 1000, t.cpu().numpy(), gl.cpu().numpy(), gl.cpu().numpy(), 1.0)
     check_bwd(x - 1100, t.cpu().numpy(), gl.cpu().numpy(), gl.cpu().numpy(), 1.0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("scale", [1e-38, 2.5e-38, 1e-37])
+def test_forward_of_logits_whose_differences_are_infinite(dtype, scale):
+    """Logits all over the type's range at scales that bring them to a few units."""
+    for M, V in ((4, 20011), (600, 1027)):
+        gen = torch.Generator().manual_seed(V)
+        x = ((torch.rand(M, V, generator=gen) * 2 - 1) * 3.3e38).to(DT[dtype]).cuda()
+        x[1, :900] = -3.3e38
+        x[2, 7:] = torch.finfo(DT[dtype]).min
+        check_fwd(x, targets_(M, V, 1), 6, scale)
