@@ -418,8 +418,8 @@ def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None,
         _dense(ids, "top_ids", torch.int32, (M, top_k), dev)
         _dense(top, "top_logprobs", torch.float32, (M, top_k), dev)
     check(lib().fn_token_logprobs(logits.data_ptr(), _DTYPE[logits.dtype], M, V, ld, _at(targets), scale, top_k,
-                                  _at(lp), _at(ent), _at(lse), ids.data_ptr() if top_k else None,
-                                  top.data_ptr() if top_k else None, _handle(dev)), "fn_token_logprobs")
+                                  _at(lp), _at(ent), _at(lse), _at(ids) if top_k else None,
+                                  _at(top) if top_k else None, _handle(dev)), "fn_token_logprobs")
     return out
 
 

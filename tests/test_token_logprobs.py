@@ -741,3 +741,23 @@ def test_forward_of_logits_whose_differences_are_infinite(dtype, scale):
         x[1, :900] = -3.3e38
         x[2, 7:] = torch.finfo(DT[dtype]).min
         check_fwd(x, targets_(M, V, 1), 6, scale)
+
+
+@pytest.mark.gpu
+def test_torch_api_refuses_outputs_that_do_not_fit():
+    """What is missing among the given outputs is refused as the library refuses it."""
+    x = logits_(3, 100, 100, "bf16", seed=3)
+    t = torch.zeros(3, dtype=torch.int32, device="cuda")
+    f = torch.empty(3, device="cuda")
+    ids, top = torch.empty((3, 2), dtype=torch.int32, device="cuda"), torch.empty((3, 2), device="cuda")
+    for out, k, targets in ((T.TokenLogprobs(f, None, None, None, None), 2, t), (T.TokenLogprobs(f, None, None, ids, None), 2, t),
+                            (T.TokenLogprobs(None, None, None, None, None), 0, t), (T.TokenLogprobs(f, None, None, None, None), 0, None),
+                            (T.TokenLogprobs(f, f, None, None, None), 0, t)):
+        with pytest.raises(fnb.FnError):
+            T.token_logprobs(x, targets, top_k=k, out=out)
+    with pytest.raises(ValueError):
+        T.token_logprobs(x, t, top_k=3, out=T.TokenLogprobs(f, None, None, ids, top))
+    r = T.token_logprobs(x, t, top_k=2, out=T.TokenLogprobs(None, f, None, ids, top))
+    ref = T.token_logprobs(x, t, top_k=2)
+    torch.cuda.synchronize()
+    assert torch.equal(r.entropy, ref.entropy) and torch.equal(ids, ref.top_ids) and torch.equal(top, ref.top_logprobs)
