@@ -44,8 +44,8 @@
 // one launch, no workspace, no atomics on results, bit-identical repeats.
 //
 // Measured at 1965 MHz (and in a long run under the power cap, at 1.6 to 1.7
-// GHz): 4096 x 131072 bf16 with 8 alternatives 207 us (239), 5.2 TB/s; without
-// 161 us (193), 6.7 TB/s; 2048 x 131072 fp32 with 8 alternatives 181 us (191);
+// GHz): 4096 x 131072 bf16 with 8 alternatives 208 us (240), 5.2 TB/s; without
+// 162 us (195), 6.6 TB/s; 2048 x 131072 fp32 with 8 alternatives 183 us (191);
 // one row with 20 alternatives 10 us.  A thread that has met nothing but a mask's
 // fill of -2^24 / c and below takes the exact differences: with such a fill in the
 // first three quarters of each row 2048 x 131072 bf16 takes 116 us instead of 94.
